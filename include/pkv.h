@@ -65,7 +65,8 @@ enum {
   PKV_DEV_BAD_BLOCK_ID = 1,  /* a block table entry outside [0, num_blocks) */
   PKV_DEV_BAD_CONTEXT = 2,   /* a context length outside [1, max_context_len] */
   PKV_DEV_BAD_SLOT = 3,      /* a slot >= num_blocks * block_size */
-  PKV_DEV_TIMEOUT = 4        /* a pipeline wait gave up (should never happen) */
+  PKV_DEV_TIMEOUT = 4,       /* a pipeline wait gave up (should never happen) */
+  PKV_DEV_BAD_POSITION = 5   /* a position outside [0, max_position) */
 };
 
 /* Shape of one paged cache and of the batch that reads it.
@@ -123,7 +124,8 @@ typedef struct {
   int32_t split_tokens;     /* P, tokens per partition */
   int32_t num_splits;       /* S = ceil(max_context_len / P) */
   int32_t variant;          /* 0 = CUDA-core kernel, 1 = mma.sync tensor-core
-                               kernel, 2 = tcgen05 tensor-core kernel */
+                               kernel, 2 = tcgen05 tensor-core kernel,
+                               3 = 4-bit cache kernel (pkv_kv4_decode_plan) */
   int32_t warps_per_cta;
   int32_t stages_per_warp;
   int32_t grid_ctas;
@@ -265,6 +267,125 @@ int pkv_copy_blocks(const pkv_shape* shape, const void* src_k, const void* src_v
                     int32_t src_num_blocks, void* dst_k, void* dst_v,
                     int32_t dst_num_blocks, const int32_t* pairs, int32_t num_pairs,
                     pkv_stream_t stream);
+
+/*
+ * Position rotation of a step's rows (pkv_rope_append, pkv_kv4_append).
+ *   rot_dim       R, channels that are rotated: the first R of every query and
+ *                 key head, a multiple of 16, at most head_dim; 0 rotates
+ *                 nothing (positions and cos_sin may then be NULL)
+ *   interleaved   0: channel i < R/2 is paired with channel i + R/2;
+ *                 else: channels 2i and 2i + 1 are paired
+ *   max_position  rows of cos_sin
+ *   q_stride, k_stride, v_stride  elements from one token's row to the next
+ *                 (a fused projection's output has all three in one row); a
+ *                 multiple of 8, at least heads * head_dim; 0 means dense
+ */
+typedef struct {
+  int32_t rot_dim;
+  int32_t interleaved;
+  int32_t max_position;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+} pkv_rope;
+
+/*
+ * Rotate a step's queries and keys by their positions and append the keys and
+ * values to the paged cache, in one launch.  With c = cos_sin[p][0 .. R/2) and
+ * s = cos_sin[p][R/2 .. R) of token t's position p, every pair (a, b) of
+ * channels with index i becomes (a c_i - b s_i, b c_i + a s_i), in FP32 with
+ * one rounding at the store.  Values are copied bit for bit.
+ *
+ *   shape         uses num_q_heads, num_kv_heads, head_dim, block_size,
+ *                 num_blocks, dtype
+ *   q, k, v       [T, Hq, D], [T, Hkv, D], [T, Hkv, D], 16-byte aligned, with
+ *                 the token strides of `rope`.  q may be NULL (keys only).
+ *   positions     [T] int32
+ *   cos_sin       [max_position, R] float, 16-byte aligned
+ *   slot_mapping  [T] int32, as for pkv_kv_cache_append: a negative slot is
+ *                 padding, whose key and value are not stored (its query is
+ *                 still rotated)
+ *   q_out         [T, Hq, D] dense, 16-byte aligned; may be q itself when q is
+ *                 dense, else must not overlap it
+ *   k_cache, v_cache  [NB, Hkv, bs, D], 16-byte aligned
+ * A token whose position is outside [0, max_position) is skipped (its q_out
+ * row and slot are left as they were; PKV_DEV_BAD_POSITION).  A slot >= NB *
+ * bs stores nothing (PKV_DEV_BAD_SLOT).  Two tokens with the same slot race.
+ * num_tokens == 0 is a no-op.
+ */
+int pkv_rope_append(const pkv_shape* shape, const pkv_rope* rope, const void* q,
+                    const void* k, const void* v, const int32_t* positions,
+                    const float* cos_sin, const int32_t* slot_mapping,
+                    int32_t num_tokens, void* q_out, void* k_cache, void* v_cache,
+                    pkv_stream_t stream);
+
+/*
+ * The 4-bit paged cache.  A row (one token, one kv head) of D channels is held
+ * in groups of 32 channels, each with a binary16 scale s and zero point z:
+ * value = s * (n + z), n in 0 .. 15.  With lo, hi and m the group's smallest
+ * and largest value and largest magnitude, all in FP32 with IEEE rounding,
+ *     s = the smallest binary16 >= max((hi - lo) / 15, m / 1024, 2^-24), at
+ *         most 65504
+ *     z = binary16(lo / s), clamped to +-65504
+ *     n = clamp(round_to_even(x / s - z), 0, 15)
+ * A group with an infinity or NaN gets s = z = NaN: it reads as NaN.  That is
+ * 5 bits a value: D * 5/8 bytes a row, against 2 * D in 16 bits.
+ *
+ * A cache (K or V) is [NB, Hkv, bs * D * 5/8 bytes], 16-byte aligned.  The
+ * bytes of one (block, kv head) tile, with G = D / 32 groups:
+ *     [0, bs * D/2)   codes: row r at r * D/2; the 16 bytes of group g at
+ *                     16 * (g ^ ((r * G / 8) mod G)) of the row; byte b of them
+ *                     holds channel 2b in its low half and 2b + 1 in its high
+ *     then, for keys:    (s, z) of row r, group g at 4 * (r * G + g)
+ *     then, for values:  s of rows 2u and 2u + 1, then z of both, at
+ *                        8 * (u * G + g)
+ * pkv_copy_blocks moves its blocks as a 16-bit pool of one row of bs * D *
+ * 5/16 elements a block (block_size 1, head_dim bs * D * 5/16).
+ */
+
+/* pkv_rope_append into a 4-bit cache: keys are rotated in FP32 and held from
+ * there, without a rounding to 16 bits between.  rope->rot_dim 0 holds keys as
+ * they are.  Same arguments and rules otherwise; the caches are 4-bit ones. */
+int pkv_kv4_append(const pkv_shape* shape, const pkv_rope* rope, const void* q,
+                   const void* k, const void* v, const int32_t* positions,
+                   const float* cos_sin, const int32_t* slot_mapping,
+                   int32_t num_tokens, void* q_out, void* k_cache, void* v_cache,
+                   pkv_stream_t stream);
+
+/*
+ * Read rows of the 4-bit cache back in 16 bits (a prefix for the attention of
+ * a prompt's next chunk, an export): for every token t and kv head h,
+ *     k[t][h][:] and v[t][h][:] = the values at slot_mapping[t], one rounding.
+ *   shape         uses num_kv_heads, head_dim, block_size, num_blocks, dtype
+ *   slot_mapping  [T] int32; the row of a negative slot is set to zero
+ *   k, v          [T, Hkv, D], 16-byte aligned
+ * A slot >= NB * bs gives zeros too and sets PKV_DEV_BAD_SLOT.
+ */
+int pkv_kv4_gather(const pkv_shape* shape, const void* k_cache, const void* v_cache,
+                   const int32_t* slot_mapping, int32_t num_tokens, void* k, void* v,
+                   pkv_stream_t stream);
+
+/*
+ * Paged single-token decode attention over a 4-bit cache: as
+ * pkv_paged_attn_decode, with k_t and v_t the values that the cache holds.
+ * q and out are of shape->dtype.  shape->kernel must be 0.
+ *  - context_lens[i] may be 0: a padding row of the batch, whose out rows are
+ *    set to zero (no error).  Negative lengths and lengths above
+ *    max_context_len are errors, as for pkv_paged_attn_decode.
+ *  - workspace: pkv_kv4_workspace_bytes; NULL takes the workspace set with
+ *    pkv_set_workspace.
+ */
+int pkv_kv4_attn_decode(const pkv_shape* shape, const void* q, const void* k_cache,
+                        const void* v_cache, const int32_t* block_tables,
+                        const int32_t* context_lens, float scale, void* out,
+                        void* workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+/* How pkv_kv4_attn_decode will run on the current device, or, with num_sms >
+ * 0, on a device with that many SMs (host only then).  plan->variant is 3. */
+int pkv_kv4_decode_plan(const pkv_shape* shape, int32_t num_sms, pkv_plan* plan);
+
+/* Workspace bytes pkv_kv4_attn_decode needs for `shape` (0 if none). */
+int pkv_kv4_workspace_bytes(const pkv_shape* shape, size_t* bytes);
 
 /*
  * Block manager (host only, no GPU calls): the bookkeeping side of the paged

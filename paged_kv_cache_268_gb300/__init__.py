@@ -14,10 +14,19 @@ from ._binding import (  # noqa: F401
     decode_shape,
     decode_step,
     get_device_error,
+    kv4_append,
+    kv4_attn_decode,
+    kv4_cache,
+    kv4_decode_plan,
+    kv4_decode_shape,
+    kv4_gather,
+    kv4_workspace_bytes,
     kv_cache_append,
     launch_count,
     load_library,
     paged_attn_decode,
+    rope_append,
+    rope_table,
     selftest_wait_timeout,
     set_workspace,
     workspace_bytes,

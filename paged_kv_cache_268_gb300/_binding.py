@@ -7,7 +7,9 @@ fallback — a missing library raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 import re
 
@@ -33,6 +35,11 @@ class Shape(ctypes.Structure):
         "num_seqs", "num_q_heads", "num_kv_heads", "head_dim", "block_size",
         "num_blocks", "max_blocks_per_seq", "max_context_len", "dtype",
         "split_tokens", "kernel")]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("rot_dim", "interleaved", "max_position")]
+                + [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")])
 
 
 class Plan(ctypes.Structure):
@@ -94,6 +101,18 @@ def load_library(path: str | None = None):
     lib.pkv_decode_plan_for.restype = ctypes.c_int
     lib.pkv_workspace_bytes.argtypes = [sp, ctypes.POINTER(sz)]
     lib.pkv_workspace_bytes.restype = ctypes.c_int
+    rp = ctypes.POINTER(Rope)
+    for n in ("pkv_rope_append", "pkv_kv4_append"):
+        getattr(lib, n).argtypes = [sp, rp, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp]
+        getattr(lib, n).restype = ctypes.c_int
+    lib.pkv_kv4_gather.argtypes = [sp, vp, vp, vp, i32, vp, vp, vp]
+    lib.pkv_kv4_gather.restype = ctypes.c_int
+    lib.pkv_kv4_attn_decode.argtypes = [sp, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, sz, vp]
+    lib.pkv_kv4_attn_decode.restype = ctypes.c_int
+    lib.pkv_kv4_decode_plan.argtypes = [sp, i32, ctypes.POINTER(Plan)]
+    lib.pkv_kv4_decode_plan.restype = ctypes.c_int
+    lib.pkv_kv4_workspace_bytes.argtypes = [sp, ctypes.POINTER(sz)]
+    lib.pkv_kv4_workspace_bytes.restype = ctypes.c_int
     lib.pkv_get_device_error.argtypes = [i32p, vp]
     lib.pkv_get_device_error.restype = ctypes.c_int
     lib.pkv_selftest_wait_timeout.argtypes = [i32, vp]
@@ -371,11 +390,277 @@ def decode_step(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
     return out
 
 
+def rope_table(max_position: int, rot_dim: int, base: float = 10000.0,
+               device="cuda") -> torch.Tensor:
+    """The cos_sin table [max_position, rot_dim] float32 of rope_append and
+    kv4_append: cosines, then sines, of position * base^(-2i / rot_dim).  The
+    angles are worked out in 64 bits (far positions need them)."""
+    f = float(base) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    a = torch.arange(max_position, dtype=torch.float64, device=device)[:, None] * f
+    return torch.cat([a.cos(), a.sin()], 1).float()
+
+
+def kv4_cache(num_blocks: int, num_kv_heads: int, block_size: int, head_dim: int,
+              device="cuda") -> torch.Tensor:
+    """An empty 4-bit cache (for keys or for values): uint8 [NB, Hkv, bs, 5D/8].
+    The bytes within a (block, head) tile are the library's (include/pkv.h)."""
+    return torch.zeros((num_blocks, num_kv_heads, block_size, head_dim * 5 // 8),
+                       dtype=torch.uint8, device=device)
+
+
+def _kv4_dims(k_cache: torch.Tensor, v_cache: torch.Tensor) -> tuple[int, int, int, int]:
+    """(NB, Hkv, bs, D) of a pair of 4-bit caches."""
+    _dense(k_cache, "k_cache", torch.uint8)
+    _dense(v_cache, "v_cache", torch.uint8)
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or k_cache.shape[3] * 8 % 5:
+        raise ValueError("4-bit caches must be uint8 [NB, Hkv, bs, 5D/8] tensors of one shape")
+    NB, Hkv, bs, W = k_cache.shape
+    return NB, Hkv, bs, W * 8 // 5
+
+
+@functools.lru_cache(maxsize=256)
+def _sized(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+           max_blocks_per_seq, max_context_len, dtype, split_tokens=0) -> Shape:
+    """A Shape, made once for the same sizes.  Read only."""
+    return make_shape(num_seqs=num_seqs, num_q_heads=num_q_heads, num_kv_heads=num_kv_heads,
+                      head_dim=head_dim, block_size=block_size, num_blocks=num_blocks,
+                      max_blocks_per_seq=max_blocks_per_seq, max_context_len=max_context_len,
+                      dtype=dtype, split_tokens=split_tokens)
+
+
+def _on(dev: torch.device):
+    """Make `dev` current, where it is not."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _allocating_on(stream):
+    """Allocate for work on `stream`: memory that the caller drops is then not
+    handed out again before that work has run."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _dtype_code(dtype: torch.dtype) -> int:
+    if dtype not in _DT:
+        raise ValueError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")
+    return _DT[dtype]
+
+
+def _token_stride(t: torch.Tensor, name: str, heads: int, D: int, T: int, dtype) -> int:
+    """Elements between the token rows of a [T, heads, D] tensor whose rows are
+    dense (0 where there is no second row)."""
+    if not t.is_cuda or t.dtype != dtype:
+        raise ValueError(f"{name} must be a CUDA tensor of {dtype}")
+    if t.shape != (T, heads, D):
+        raise ValueError(f"{name} must be [{T}, {heads}, {D}], got {list(t.shape)}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}'s heads must lie densely one after the other")
+    if T > 1 and t.stride(0) < heads * D:
+        raise ValueError(f"{name}'s token rows must not overlap")
+    return t.stride(0) if T > 1 else 0
+
+
+def _append(fn: str, dims, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out,
+            interleaved, stream, dtype):
+    NB, Hkv, bs, D = dims
+    code = _dtype_code(dtype)
+    if k.dim() != 3:
+        raise ValueError("k must be [T, Hkv, D]")
+    T = k.shape[0]
+    ks = _token_stride(k, "k", Hkv, D, T, dtype)
+    vs = _token_stride(v, "v", Hkv, D, T, dtype)
+    _dense(slot_mapping, "slot_mapping", torch.int32)
+    if slot_mapping.shape != (T,):
+        raise ValueError("slot_mapping must be [T]")
+    Hq = qs = rot = rows = 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [T, Hq, D]")
+        Hq = q.shape[1]
+        qs = _token_stride(q, "q", Hq, D, T, dtype)
+        if q_out is not None:
+            _dense(q_out, "q_out", dtype)
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if (positions is None) != (cos_sin is None):
+        raise ValueError("positions and cos_sin come together")
+    if cos_sin is not None:
+        _dense(positions, "positions", torch.int32)
+        _dense(cos_sin, "cos_sin", torch.float32)
+        if positions.shape != (T,) or cos_sin.dim() != 2:
+            raise ValueError("positions must be [T], cos_sin [max_position, rot_dim]")
+        rows, rot = cos_sin.shape
+    dev = _one_device(q=q, k=k, v=v, positions=positions, cos_sin=cos_sin,
+                      slot_mapping=slot_mapping, k_cache=k_cache, v_cache=v_cache, q_out=q_out)
+    ptr = _stream_ptr(stream, dev)
+    shape = _sized(0, max(Hq, 1), Hkv, D, bs, NB, 1, 1, code)
+    rope = Rope(rot, 1 if interleaved else 0, rows, qs, ks, vs)
+    if q is not None and q_out is None:
+        with _allocating_on(stream):
+            q_out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
+    with _on(dev):
+        _check(fn, getattr(load_library(), fn)(
+            ctypes.byref(shape), ctypes.byref(rope), _ptr(q) if Hq else None, _ptr(k), _ptr(v),
+            _ptr(positions), _ptr(cos_sin), _ptr(slot_mapping), T, _ptr(q_out) if Hq else None,
+            _ptr(k_cache), _ptr(v_cache), ptr))
+    return q_out
+
+
+def rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                positions: torch.Tensor | None, cos_sin: torch.Tensor | None,
+                slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                q_out: torch.Tensor | None = None, *, interleaved: bool = False,
+                stream=None) -> torch.Tensor | None:
+    """Rotate q and k by their positions and append k and v to the 16-bit paged
+    caches, in one launch.  Returns the rotated q.
+
+    q [T, Hq, D] or None; k, v [T, Hkv, D]: heads dense, token rows at any
+    stride that is a multiple of 8 elements (slices of a fused projection).
+    positions [T] int32; cos_sin [max_position, R] float32 (rope_table), R <= D
+    the rotated channels; both None: nothing is rotated.  slot_mapping [T]
+    int32, negative: not stored.  q_out: allocated if not given; a dense q may
+    be rotated in place (q_out=q).  interleaved: pairs are neighbours, not
+    halves.
+    """
+    dims = _cache_shape(k_cache)
+    _dense(k_cache, "k_cache")
+    _dense(v_cache, "v_cache", k_cache.dtype)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("caches must have one shape")
+    return _append("pkv_rope_append", dims, q, k, v, positions, cos_sin, slot_mapping, k_cache,
+                   v_cache, q_out, interleaved, stream, k_cache.dtype)
+
+
+def kv4_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+               positions: torch.Tensor | None, cos_sin: torch.Tensor | None,
+               slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+               q_out: torch.Tensor | None = None, *, interleaved: bool = False,
+               stream=None) -> torch.Tensor | None:
+    """rope_append into 4-bit caches (kv4_cache)."""
+    dims = _kv4_dims(k_cache, v_cache)
+    return _append("pkv_kv4_append", dims, q, k, v, positions, cos_sin, slot_mapping, k_cache,
+                   v_cache, q_out, interleaved, stream, k.dtype)
+
+
+def kv4_gather(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor,
+               dtype: torch.dtype, k: torch.Tensor | None = None, v: torch.Tensor | None = None,
+               stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The rows at slot_mapping [T] of 4-bit caches as 16-bit (k, v), each
+    [T, Hkv, D] (allocated if not given).  Rows of negative slots are zero."""
+    NB, Hkv, bs, D = _kv4_dims(k_cache, v_cache)
+    code = _dtype_code(dtype)
+    _dense(slot_mapping, "slot_mapping", torch.int32)
+    if slot_mapping.dim() != 1:
+        raise ValueError("slot_mapping must be [T]")
+    T = slot_mapping.shape[0]
+    for t, n in ((k, "k"), (v, "v")):
+        if t is not None:
+            _dense(t, n, dtype)
+            if t.shape != (T, Hkv, D):
+                raise ValueError(f"{n} must be [T, Hkv, D]")
+    dev = _one_device(k_cache=k_cache, v_cache=v_cache, slot_mapping=slot_mapping, k=k, v=v)
+    ptr = _stream_ptr(stream, dev)
+    with _allocating_on(stream):
+        k = torch.empty((T, Hkv, D), dtype=dtype, device=dev) if k is None else k
+        v = torch.empty((T, Hkv, D), dtype=dtype, device=dev) if v is None else v
+    shape = _sized(0, 1, Hkv, D, bs, NB, 1, 1, code)
+    with _on(dev):
+        _check("pkv_kv4_gather",
+               load_library().pkv_kv4_gather(ctypes.byref(shape), _ptr(k_cache), _ptr(v_cache),
+                                             _ptr(slot_mapping), T, _ptr(k), _ptr(v), ptr))
+    return k, v
+
+
+def kv4_decode_shape(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tensor,
+                     max_context_len: int | None = None, split_tokens: int = 0) -> Shape:
+    """decode_shape for a 4-bit cache."""
+    NB, Hkv, bs, W = k_cache.shape
+    MB = block_tables.shape[1]
+    return _sized(q.shape[0], q.shape[1], Hkv, W * 8 // 5, bs, NB, MB,
+                  MB * bs if max_context_len is None else int(max_context_len),
+                  _dtype_code(q.dtype), int(split_tokens))
+
+
+def kv4_decode_plan(shape: Shape, num_sms: int | None = None) -> Plan:
+    """decode_plan for a 4-bit cache."""
+    plan = Plan()
+    if num_sms is not None and num_sms < 1:
+        raise ValueError("num_sms must be positive")
+    _check("pkv_kv4_decode_plan",
+           load_library().pkv_kv4_decode_plan(ctypes.byref(shape), int(num_sms or 0),
+                                              ctypes.byref(plan)))
+    return plan
+
+
+def kv4_workspace_bytes(shape: Shape) -> int:
+    """workspace_bytes for a 4-bit cache."""
+    n = ctypes.c_size_t(0)
+    _check("pkv_kv4_workspace_bytes",
+           load_library().pkv_kv4_workspace_bytes(ctypes.byref(shape), ctypes.byref(n)))
+    return int(n.value)
+
+
+def kv4_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                    out: torch.Tensor | None = None, *, max_context_len: int | None = None,
+                    split_tokens: int = 0, workspace: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """paged_attn_decode over 4-bit caches (kv4_cache): q [B, Hq, D] fp16 or
+    bf16, out of q's type.  A length of 0 marks a padding row, whose out rows
+    are set to zero.  workspace as for paged_attn_decode
+    (kv4_workspace_bytes)."""
+    NB, Hkv, bs, D = _kv4_dims(k_cache, v_cache)
+    _dense(q, "q")
+    _dtype_code(q.dtype)
+    _dense(block_tables, "block_tables", torch.int32)
+    _dense(context_lens, "context_lens", torch.int32)
+    if q.dim() != 3 or q.shape[2] != D:
+        raise ValueError("q must be [B, Hq, D] with the caches' head_dim")
+    if (block_tables.dim() != 2 or block_tables.shape[0] != q.shape[0]
+            or context_lens.shape != (q.shape[0],)):
+        raise ValueError("block_tables must be [B, MB]; context_lens [B]")
+    if out is not None:
+        _dense(out, "out", q.dtype)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape [B, Hq, D]")
+    if workspace is not None:
+        _dense(workspace, "workspace")
+    dev = _one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                      context_lens=context_lens, out=out, workspace=workspace)
+    ptr = _stream_ptr(stream, dev)
+    shape = kv4_decode_shape(q, k_cache, block_tables, max_context_len, split_tokens)
+    with _on(dev), _allocating_on(stream):
+        if workspace is None and dev.index not in _SET_WS:
+            n = kv4_workspace_bytes(shape)
+            if n:
+                workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        if out is None:
+            out = torch.empty_like(q)
+        _check("pkv_kv4_attn_decode",
+               load_library().pkv_kv4_attn_decode(
+                   ctypes.byref(shape), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+                   _ptr(context_lens), float(scale), _ptr(out), _ptr(workspace),
+                   _nbytes(workspace), ptr))
+    return out
+
+
+def _kv4_as_rows(pool: torch.Tensor) -> torch.Tensor:
+    """A 4-bit pool [NB, Hkv, bs, 5D/8] as 16-bit blocks of one row each."""
+    return pool.view(torch.float16).flatten(2).unsqueeze(2)
+
+
 def copy_blocks(src_k: torch.Tensor, src_v: torch.Tensor, dst_k: torch.Tensor,
                 dst_v: torch.Tensor, pairs: torch.Tensor, stream=None) -> None:
     """Copy block pairs[i, 0] of (src_k, src_v) to block pairs[i, 1] of
     (dst_k, dst_v).  Pools are [NB, Hkv, bs, D] tensors on the GPU or in
-    pinned host memory; pairs is an int32 [n, 2] tensor the GPU can read."""
+    pinned host memory, or 4-bit ones (kv4_cache); pairs is an int32 [n, 2]
+    tensor the GPU can read."""
+    if all(t.dtype == torch.uint8 and t.dim() == 4 and t.is_contiguous() and t.shape[3] % 2 == 0
+           for t in (src_k, src_v, dst_k, dst_v)):
+        if src_k.shape[1:] != dst_k.shape[1:]:
+            raise ValueError("pools must share the block shape")
+        src_k, src_v, dst_k, dst_v = map(_kv4_as_rows, (src_k, src_v, dst_k, dst_v))
     for t, n in ((src_k, "src_k"), (src_v, "src_v"), (dst_k, "dst_k"), (dst_v, "dst_v")):
         if not t.is_contiguous() or t.dim() != 4 or t.dtype != src_k.dtype:
             raise ValueError(f"{n} must be a contiguous [NB, Hkv, bs, D] tensor of one dtype")

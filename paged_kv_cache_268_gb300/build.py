@@ -1,8 +1,8 @@
 """Build libpkv.so (sm_103a) in-tree with nvcc.
 
 The decode kernels are split over four translation units (element type x
-kernel variant) plus the C-ABI front end, compiled in parallel and linked into
-``paged_kv_cache_268_gb300/lib/libpkv.so``.  Run ``python -m
+kernel variant) plus the C-ABI front end, the rotation append and the 4-bit
+cache's kernels, compiled in parallel and linked into ``paged_kv_cache_268_gb300/lib/libpkv.so``.  Run ``python -m
 paged_kv_cache_268_gb300.build`` or call ``build()``.
 """
 from __future__ import annotations
@@ -33,7 +33,8 @@ def nvcc() -> str:
 
 def _units():
     units = [("pkv_api", "pkv_api.cu", []), ("pkv_noalloc", "pkv_noalloc.cu", []),
-             ("pkv_blocks", "pkv_blocks.cpp", []), ("pkv_decode_tc", "pkv_decode_tc.cu", [])]
+             ("pkv_blocks", "pkv_blocks.cpp", []), ("pkv_decode_tc", "pkv_decode_tc.cu", []),
+             ("pkv_rope", "pkv_rope.cu", []), ("pkv_kv4_decode", "pkv_kv4_decode.cu", [])]
     for bf in (0, 1):
         for mma in (0, 1):
             name = f"pkv_decode_{'bf16' if bf else 'f16'}_{'mma' if mma else 'simt'}"

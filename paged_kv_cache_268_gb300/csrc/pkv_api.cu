@@ -273,6 +273,8 @@ int cache_map(CUtensorMap* out, const void* base, const pkv_shape& s, bool three
 // ------------------------------------------------------------------ checks
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+}  // namespace
+
 int check_cache_shape(const pkv_shape* s) {
   if (!s) return PKV_ERR_NULL;
   if (s->num_kv_heads < 1 || s->head_dim < 1 || s->block_size < 1 || s->num_blocks < 1)
@@ -300,6 +302,8 @@ int check_decode_shape(const pkv_shape* s) {
   if (G > 32) return PKV_ERR_UNSUPPORTED;
   return PKV_OK;
 }
+
+namespace {
 
 // Inner-loop variant (0 CUDA cores, 1 mma.sync, 2 tcgen05) for a shape, or -1
 // when the requested one cannot run it.  Every variant serves the plain
@@ -420,11 +424,31 @@ int* device_error_word() {
   return current_device(&d) == PKV_OK ? d->err : nullptr;
 }
 
+int device_sms(int* sms) {
+  DeviceInfo* d = nullptr;
+  const int rc = current_device(&d);
+  if (rc == PKV_OK) *sms = d->sms;
+  return rc;
+}
+
+int device_workspace(void** ptr, size_t* bytes) {
+  DeviceInfo* d = nullptr;
+  const int rc = current_device(&d);
+  if (rc == PKV_OK) set_workspace_of(d, ptr, bytes);
+  return rc;
+}
+
+cudaError_t launch_split_reduce(const DecodeArgs& a, bool bf16, int D, cudaStream_t stream) {
+  return bf16 ? launch_reduce<true>(a, D, stream) : launch_reduce<false>(a, D, stream);
+}
+
+void count_launch() { g_launches.fetch_add(1); }
+
 }  // namespace pkv
 
 using namespace pkv;
 
-extern "C" int pkv_version(void) { return 100; }
+extern "C" int pkv_version(void) { return 200; }
 
 extern "C" uint64_t pkv_launch_count(void) { return g_launches.load(); }
 

@@ -7,10 +7,18 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "pkv.h"
+
 namespace pkv {
 
 // Device error word codes (mirror PKV_DEV_* in include/pkv.h).
-enum : int { kDevBadBlock = 1, kDevBadContext = 2, kDevBadSlot = 3, kDevTimeout = 4 };
+enum : int {
+  kDevBadBlock = 1,
+  kDevBadContext = 2,
+  kDevBadSlot = 3,
+  kDevTimeout = 4,
+  kDevBadPosition = 5
+};
 
 // Largest number of KV blocks one CTA's partition may span.
 constexpr int kMaxBlocksPerCta = 256;
@@ -67,5 +75,34 @@ int tc_ring_slots(int group_size);   // 32 KB K/V tile slots per CTA
 int tc_warps(int group_size);        // warps per CTA (softmax, producer, MMA)
 
 int* device_error_word();  // device address of the error word (current device)
+
+// Services of the front end (pkv_api.cu) to the other entry points.
+int check_cache_shape(const pkv_shape*);     // PKV_OK or the PKV_ERR_* of a bad cache shape
+int check_decode_shape(const pkv_shape*);    // the same for a decode batch
+int device_sms(int* sms);                    // SM count of the current device
+// Workspace set for the current device with pkv_set_workspace, or {nullptr, 0}.
+int device_workspace(void** ptr, size_t* bytes);
+// Cross-split reduce of a.part_o / a.part_ml into a.out (head_dim D).
+cudaError_t launch_split_reduce(const DecodeArgs& a, bool bf16, int D, cudaStream_t stream);
+void count_launch();                         // one more kernel for pkv_launch_count
+
+// Launch with programmatic stream serialisation: the grid may become resident
+// while the stream's previous kernel finishes, so the kernel calls pdl_wait()
+// before its first access to memory.
+template <class... KArgs, class... Args>
+cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, unsigned threads, size_t smem,
+                       cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
 
 }  // namespace pkv
