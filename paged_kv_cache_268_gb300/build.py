@@ -36,6 +36,7 @@ def _units():
              ("pkv_blocks", "pkv_blocks.cpp", []), ("pkv_decode_tc", "pkv_decode_tc.cu", []),
              ("pkv_rope", "pkv_rope.cu", []), ("pkv_kv4_decode", "pkv_kv4_decode.cu", [])]
     for bf in (0, 1):
+        units.append((f"pkv_kv4_{'bf16' if bf else 'f16'}", "pkv_kv4_inst.cu", [f"-DPKV_INST_BF16={bf}"]))
         for mma in (0, 1):
             name = f"pkv_decode_{'bf16' if bf else 'f16'}_{'mma' if mma else 'simt'}"
             units.append((name, "pkv_decode_inst.cu",

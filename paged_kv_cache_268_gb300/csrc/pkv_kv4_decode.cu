@@ -1,90 +1,59 @@
 // Paged single-token decode attention over the 4-bit cache
 // (pkv_kv4_attn_decode, contract in include/pkv.h).
-#include <cuda_fp16.h>
-
-#include "pkv.h"
-#include "pkv_internal.h"
-#include "pkv_kv4.cuh"
-#include "pkv_ptx.cuh"
+#include "pkv_kv4_decode.cuh"
 
 namespace pkv {
 namespace {
 
-struct Kv4Args {
-  DecodeArgs d;
-  const uint8_t* k;
-  const uint8_t* v;
-  int bs;
-};
-
-// One warp per (sequence, query head): lane l owns channels [l * D/32, ...)
-// and the warp walks the tokens one by one with a running maximum and sum.
-template <bool BF, int D>
-__global__ void __launch_bounds__(32) kv4_decode_kernel(const __grid_constant__ Kv4Args p) {
-  constexpr int C = D / 32;
-  pdl_wait();
-  pdl_launch_dependents();
-  const DecodeArgs& a = p.d;
-  const int seq = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq, lane = threadIdx.x;
-  const int L = a.context_lens[seq];
-  const size_t row = static_cast<size_t>(blockIdx.x) * D + lane * C;
-  if (L < 0 || L > a.max_ctx) {
-    if (lane == 0 && h == 0) record_error(a.err, kDevBadContext);
-    return;
-  }
-  float q[C], o[C] = {}, m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < C; i += 2) {
-    const float2 f = unpack2<BF>(*reinterpret_cast<const uint32_t*>(a.q + row + i));
-    q[i] = f.x * a.scale_log2;
-    q[i + 1] = f.y * a.scale_log2;
-  }
-  const int g = lane * C / 32, ch = lane * C % 32;
-  for (int t = 0; t < L; ++t) {
-    const int blk = a.block_tables[static_cast<size_t>(seq) * a.MB + t / p.bs], r = t % p.bs;
-    if (blk < 0 || blk >= a.NB) {
-      if (lane == 0) record_error(a.err, kDevBadBlock);
-      return;
-    }
-    const size_t tile = (static_cast<size_t>(blk) * a.Hkv + h / a.G) * kv4_tile_bytes(D, p.bs);
-    const float2 kp = __half22float2(*reinterpret_cast<const __half2*>(p.k + tile + kv4_k_par_off<D>(p.bs, r, g)));
-    const uint8_t* vp = p.v + tile + kv4_v_par_off<D>(p.bs, r, g);
-    const float vs = __half2float(*reinterpret_cast<const __half*>(vp));
-    const float vz = __half2float(*reinterpret_cast<const __half*>(vp + 4));
-    const uint8_t* kc = p.k + tile + kv4_code_off<D>(r, g) + ch / 2;
-    const uint8_t* vc = p.v + tile + kv4_code_off<D>(r, g) + ch / 2;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < C; ++i)
-      s = fmaf(q[i], kp.x * (static_cast<float>((kc[i / 2] >> (4 * (i & 1))) & 15) + kp.y), s);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    const float mn = fmaxf(m, s), alpha = exp2f(m - mn), w = exp2f(s - mn);
-    m = mn;
-    l = l * alpha + w;
-#pragma unroll
-    for (int i = 0; i < C; ++i)
-      o[i] = fmaf(w, vs * (static_cast<float>((vc[i / 2] >> (4 * (i & 1))) & 15) + vz), o[i] * alpha);
-  }
-  const float inv = L > 0 ? 1.f / l : 0.f;
-#pragma unroll
-  for (int i = 0; i < C; i += 2)
-    *reinterpret_cast<uint32_t*>(a.out + row + i) = pack2<BF>(o[i] * inv, o[i + 1] * inv);
-}
-
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// 8-head tiles of one CTA: groups of up to 8 query heads take one, wider ones
+// two (head_dim 256: one, whose accumulators fill the registers), in as many
+// CTAs as the group needs.
+int kv4_tiles(const pkv_shape* s) {
+  return s->head_dim <= 128 && s->num_q_heads / s->num_kv_heads > 8 ? 2 : 1;
+}
+
 int kv4_plan(const pkv_shape* s, int sms, pkv_plan* plan) {
-  if (s->kernel != 0) return PKV_ERR_UNSUPPORTED;
+  const int nt = kv4_tiles(s), D = s->head_dim, bs = s->block_size;
+  const int G = s->num_q_heads / s->num_kv_heads;
   *plan = pkv_plan{};
   plan->variant = 3;
-  plan->split_tokens = s->max_context_len;
-  plan->num_splits = 1;
-  plan->warps_per_cta = 1;
-  const long long grid = static_cast<long long>(s->num_seqs) * s->num_q_heads;
-  if (grid > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+  plan->warps_per_cta = kKv4Warps;
+  plan->stages_per_warp = kv4_stages(D);
+  const long long units =
+      static_cast<long long>(s->num_seqs) * s->num_kv_heads * ((G + 8 * nt - 1) / (8 * nt));
+  const int maxL = s->max_context_len;
+  const int gran = kKv4Warps * kKv4Tokens;
+  const int cap = kMaxBlocksPerCta * bs;
+  long long P;
+  if (s->split_tokens > 0) {
+    P = (static_cast<long long>(s->split_tokens) + bs - 1) / bs * bs;
+  } else {
+    P = 2048;
+    const long long slots = static_cast<long long>(sms) * ctas_per_sm_for(kv4_smem(D, nt));
+    if (units > 0 && units * ((maxL + P - 1) / P) < 4 * slots) {
+      const long long S = slots / units > 0 ? slots / units : 1;
+      P = (maxL + S - 1) / S;
+    }
+    P = (P + gran - 1) / gran * gran;
+    // at most 1024 partitions per sequence
+    const long long pmin = (static_cast<long long>(maxL) + 1023) / 1024;
+    if (P < pmin) P = (pmin + gran - 1) / gran * gran;
+  }
+  if (P > cap) P = cap;
+  if (P > maxL) P = (maxL + bs - 1) / bs * bs;
+  if (P < bs) P = bs;
+  plan->split_tokens = static_cast<int32_t>(P);
+  plan->num_splits = static_cast<int32_t>((maxL + P - 1) / P);
+  const long long grid = units * plan->num_splits;
+  if (grid > 0x7fffffffLL || static_cast<long long>(s->num_seqs) * s->num_q_heads > 0x7fffffffLL)
+    return PKV_ERR_UNSUPPORTED;
   plan->grid_ctas = static_cast<int32_t>(grid);
-  (void)sms;
+  plan->workspace_bytes =
+      plan->num_splits > 1 ? static_cast<size_t>(s->num_seqs) * s->num_q_heads * plan->num_splits *
+                                 (static_cast<size_t>(D) * 4 + 8)
+                           : 0;
   return PKV_OK;
 }
 
@@ -159,16 +128,22 @@ extern "C" int pkv_kv4_attn_decode(const pkv_shape* s, const void* q, const void
   a.d.scale_log2 = scale * 1.4426950408889634f;  // log2(e)
   a.k = static_cast<const uint8_t*>(k_cache);
   a.v = static_cast<const uint8_t*>(v_cache);
-  a.bs = s->block_size;
+  const int D = s->head_dim, nt = kv4_tiles(s);
+  a.chunks = (a.d.G + 8 * nt - 1) / (8 * nt);
+  if (plan.workspace_bytes > 0) {
+    const size_t rows = static_cast<size_t>(s->num_seqs) * s->num_q_heads * plan.num_splits;
+    a.d.part_o = static_cast<float*>(workspace);
+    a.d.part_ml = reinterpret_cast<float2*>(a.d.part_o + rows * D);
+  }
   const bool bf = s->dtype == PKV_BF16;
-  const int D = s->head_dim;
-  void (*kern)(Kv4Args) = nullptr;
-  if (D == 64) kern = bf ? kv4_decode_kernel<true, 64> : kv4_decode_kernel<false, 64>;
-  if (D == 128) kern = bf ? kv4_decode_kernel<true, 128> : kv4_decode_kernel<false, 128>;
-  if (D == 256) kern = bf ? kv4_decode_kernel<true, 256> : kv4_decode_kernel<false, 256>;
-  if (launch_pdl(kern, dim3(static_cast<unsigned>(plan.grid_ctas)), 32, 0,
-                 reinterpret_cast<cudaStream_t>(stream), a) != cudaSuccess)
-    return PKV_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = (bf ? launch_kv4_bf16 : launch_kv4_f16)(
+      a, D, s->block_size, nt, static_cast<unsigned>(plan.grid_ctas), st);
+  if (e != cudaSuccess) return PKV_ERR_CUDA;
   count_launch();
+  if (plan.num_splits > 1) {
+    if (launch_split_reduce(a.d, bf, D, st) != cudaSuccess) return PKV_ERR_CUDA;
+    count_launch();
+  }
   return PKV_OK;
 }

@@ -1,0 +1,62 @@
+// Instantiates the 4-bit decode kernels for one element type; compiled once
+// per PKV_INST_BF16.
+#include <atomic>
+
+#include "pkv_kv4_decode.cuh"
+
+#ifndef PKV_INST_BF16
+#error "define PKV_INST_BF16 (0 = binary16, 1 = bfloat16)"
+#endif
+
+namespace pkv {
+namespace {
+
+constexpr bool kBF = PKV_INST_BF16 != 0;
+
+template <int D, int BS, int NT>
+cudaError_t launch_one(const Kv4Args& a, unsigned grid, cudaStream_t stream) {
+  constexpr int SMEM = kv4_smem(D, NT);
+  auto kern = kv4_decode_kernel<kBF, D, BS, NT>;
+  // the shared-memory limit is raised once per device (threads that race here
+  // set the same attribute)
+  static std::atomic<unsigned> mask{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned bit = dev < 32 ? 1u << dev : 0u;
+  if (bit == 0 || !(mask.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    mask.fetch_or(bit, std::memory_order_release);
+  }
+  return launch_pdl(kern, dim3(grid), kKv4Warps * 32, SMEM, stream, a);
+}
+
+template <int D>
+cudaError_t launch_bs(const Kv4Args& a, int bs, int nt, unsigned grid, cudaStream_t stream) {
+  if constexpr (D <= 128) {
+    if (nt == 2)
+      return bs == 16 ? launch_one<D, 16, 2>(a, grid, stream) : launch_one<D, 32, 2>(a, grid, stream);
+  }
+  return bs == 16 ? launch_one<D, 16, 1>(a, grid, stream) : launch_one<D, 32, 1>(a, grid, stream);
+}
+
+}  // namespace
+
+#if PKV_INST_BF16
+#define PKV_LAUNCH_NAME launch_kv4_bf16
+#else
+#define PKV_LAUNCH_NAME launch_kv4_f16
+#endif
+
+cudaError_t PKV_LAUNCH_NAME(const Kv4Args& a, int head_dim, int block_size, int nt, unsigned grid,
+                            cudaStream_t stream) {
+  switch (head_dim) {
+    case 64: return launch_bs<64>(a, block_size, nt, grid, stream);
+    case 128: return launch_bs<128>(a, block_size, nt, grid, stream);
+    case 256: return launch_bs<256>(a, block_size, nt, grid, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace pkv

@@ -274,6 +274,28 @@ def test_writes_stay_inside_their_buffers(pkv, split):
     assert torch.equal(caches[0], d["k_cache"]) and torch.equal(caches[1], d["v_cache"])
 
 
+def test_workspace_rules(pkv):
+    b = batch([1000], 8, 1, 128, 16, torch.float16, seed=2)
+    d = device(b)
+    shape = pkv.kv4_decode_shape(d["q"], d["k_cache"], d["block_tables"], 1000, 64)
+    n = pkv.kv4_workspace_bytes(shape)
+    assert n > 0
+    kw = dict(max_context_len=1000, split_tokens=64)
+    want = check(pkv, b, d, **kw)
+    with pytest.raises(pkv.PkvError) as e:
+        pkv.kv4_attn_decode(**d, **kw, workspace=torch.empty(n - 16, dtype=torch.uint8, device="cuda"))
+    assert e.value.code == -5
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    pkv.set_workspace(ws)
+    try:
+        assert torch.equal(pkv.kv4_attn_decode(**d, **kw), want)
+        pkv.set_workspace(ws[:n - 16])
+        with pytest.raises(pkv.PkvError):
+            pkv.kv4_attn_decode(**d, **kw)
+    finally:
+        pkv.set_workspace(None)
+
+
 @pytest.mark.parametrize("split", [0, 128])
 def test_two_graphs_share_a_workspace_and_another_stream(pkv, split):
     """Replayed one after the other, two captured calls may share a workspace."""
