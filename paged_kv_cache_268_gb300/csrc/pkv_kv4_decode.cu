@@ -31,7 +31,7 @@ int kv4_plan(const pkv_shape* s, int sms, pkv_plan* plan) {
     P = (static_cast<long long>(s->split_tokens) + bs - 1) / bs * bs;
   } else {
     P = 2048;
-    const long long slots = static_cast<long long>(sms) * ctas_per_sm_for(kv4_smem(D, nt));
+    const long long slots = static_cast<long long>(sms) * kv4_ctas(D, nt);
     if (units > 0 && units * ((maxL + P - 1) / P) < 4 * slots) {
       const long long S = slots / units > 0 ? slots / units : 1;
       P = (maxL + S - 1) / S;

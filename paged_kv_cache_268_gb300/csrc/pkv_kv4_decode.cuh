@@ -26,11 +26,14 @@
 //     bfloat16 inputs too, which have fewer bits).
 //   O^T[32 ch x 8 heads] += codes^T P': ldmatrix.trans puts two neighbouring
 //     tokens' words side by side; two m16 tiles per group.
-//   z^T P' with z in every row of the A operand: the group's zero-point sum
-//     for each head, in the same lanes as O^T (one more m16 tile).
-// P is scaled by 2^(15-E), E >= 0 the binary exponent of the largest value
-// scale so far, so that neither small weights nor small scales fall out of
-// binary16 and P' stays below 2^15; the running sum carries the same factor.
+//   z^T P' with the pairs (s, z) as they lie in the cache for the A operand:
+//     rows 8 on give the group's zero-point sum for each head, in the same
+//     lanes as O^T (one more m16 tile; its other rows are not used).
+// P is scaled by 2^(9-E), E >= 0 from the largest value scale so far, so that
+// neither small weights nor small scales fall out of binary16; the running sum
+// carries the same factor.  The running maximum follows the true one only when
+// that is more than 2^5 ahead, which spares most rescalings of the
+// accumulators: P stays at most 2^14 and P' below 2^15.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -53,7 +56,9 @@ constexpr int kKv4Warps = 4;
 constexpr int kKv4Tokens = 32;   // per stage
 
 // Stages per warp: about 40-60 KB of ring per CTA.
-constexpr int kv4_stages(int D) { return D == 64 ? 4 : (D == 128 ? 3 : 2); }
+constexpr int kv4_stages(int D) { return D == 64 ? 4 : 2; }
+// Resident CTAs per SM that the registers are budgeted for.
+constexpr int kv4_ctas(int D, int NT) { return NT == 1 && D <= 128 ? 4 : (D == 64 ? 3 : 2); }
 constexpr int kv4_stage_bytes(int D) { return 2 * kv4_tile_bytes(D, kKv4Tokens); }
 constexpr int kv4_merge_bytes(int D, int NT) { return kKv4Warps * 8 * NT * (D + 2) * 4; }
 constexpr int kv4_ring_bytes(int D) { return kKv4Warps * kv4_stages(D) * kv4_stage_bytes(D); }
@@ -99,14 +104,15 @@ struct Kv4Compute {
   static constexpr int TILE = kv4_tile_bytes(D, BS);
   static constexpr int PER = kKv4Tokens / BS;   // blocks per stage
   static constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u;
+  static constexpr float kShift = 9.f, kSlack = 5.f;
 
   uint32_t qf[NG][NT][4];                  // B fragments: k16 step 0 (b0, b1), step 1 (b0, b1)
   float qs[NG][NT][2];                     // 2^-24 sum of the group's q, heads 2c and 2c + 1
   float sc[NT][2];                         // to log2 units, heads 2c and 2c + 1
   float o[2 * NG][NT][4];                  // codes^T P'
-  float oz[NG][NT][4];                     // z^T P' (every row the same)
+  float oz[NG][NT][4];                     // (s, z)^T P': elements 2 and 3 are z's
   float ref[NT][2], l[NT][2];              // running maximum less shift; sum
-  float shift;                             // 15 - E
+  float shift;                             // kShift - E
 
   // Heads g0 + nt * 8 + lane / 4 of the group's q rows at `qg` (zeros past G).
   // A head's row is scaled by the power of two that brings its largest element
@@ -164,7 +170,7 @@ struct Kv4Compute {
   }
 
   __device__ __forceinline__ void reset() {
-    shift = 15.f;
+    shift = kShift;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       ref[nt][0] = ref[nt][1] = -INFINITY;
@@ -200,6 +206,29 @@ struct Kv4Compute {
   }
   static constexpr int row_of(int mt) { return PER == 2 ? 0 : mt * 16; }
 
+  // Clear the parameters of the tokens from `valid` on, so that whatever bytes
+  // lie behind a sequence's end (NaN scales among them) count for nothing.
+  static __device__ __forceinline__ void clear_tail(uint32_t kt, int valid, int lane) {
+    const uint32_t vt = kt + PER * TILE;
+    for (int i = lane; i < kKv4Tokens * NG; i += 32) {
+      const int t = i / NG, g = i % NG;
+      if (t < valid) continue;
+      const int mt = t / 16, r = row_of(mt) + t % 16;
+      const uint32_t kp = block_of(kt, mt) + kv4_k_par_off<D>(BS, r, g);
+      const uint32_t vp = block_of(vt, mt) + kv4_v_par_off<D>(BS, r, g);
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(kp), "r"(0) : "memory");
+      asm volatile("st.shared.b16 [%0], %1;" ::"r"(vp), "h"(static_cast<short>(0)) : "memory");
+      asm volatile("st.shared.b16 [%0], %1;" ::"r"(vp + 4), "h"(static_cast<short>(0)) : "memory");
+    }
+    __syncwarp();
+  }
+
+  // The shift with which weights times a value scale of `top` stay in binary16.
+  static __device__ __forceinline__ float lowered(float top, float shift) {
+    const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;   // top < 2^(e + 1)
+    return fminf(shift, kShift - static_cast<float>(min(max(e, 0), 17)));
+  }
+
   // 32 tokens at `kt` (K) and `kt + PER * TILE` (V), the first `valid` of them real.
   __device__ __forceinline__ void stage(uint32_t kt, int valid, int lane) {
     const uint32_t vt = kt + PER * TILE;
@@ -207,16 +236,19 @@ struct Kv4Compute {
     // codes of (row half * 8 + rr, group hi of a pair): the lane's ldmatrix row
     const uint32_t lrow = (half * 8 + rr) * (D / 2);
     const int sw = rr * NG / 8;
-    const bool ragged = valid < kKv4Tokens;
+    // added to the logits of the lane's tokens: minus infinity past the end
+    float bias[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+    if (valid < kKv4Tokens) {
+      clear_tail(kt, valid, lane);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        bias[i >> 1][i & 1] = i * 8 + (lane >> 2) < valid ? 0.f : -INFINITY;
+    }
 
     float s[2][NT][4];
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
       const uint32_t kb = block_of(kt, mt);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
       uint32_t plo[NG], phi[NG];
       const uint32_t par = kb + BS * (D / 2) + (row_of(mt) + (lane >> 2)) * NG * 4;
       lds_words(par, plo);
@@ -236,40 +268,36 @@ struct Kv4Compute {
                             up.y * qs[g][nt][1]};
             mma_16816<false>(acc, a & M0, b & M0, a8 & M0, b8 & M0, qf[g][nt][0], qf[g][nt][1]);
             mma_16816<false>(acc, a & M1, b & M1, a8 & M1, b8 & M1, qf[g][nt][2], qf[g][nt][3]);
-            s[mt][nt][0] = fmaf(lo.x, acc[0], s[mt][nt][0]);
-            s[mt][nt][1] = fmaf(lo.x, acc[1], s[mt][nt][1]);
-            s[mt][nt][2] = fmaf(up.x, acc[2], s[mt][nt][2]);
-            s[mt][nt][3] = fmaf(up.x, acc[3], s[mt][nt][3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float by = e < 2 ? lo.x : up.x;
+              s[mt][nt][e] = g == 0 ? by * acc[e] : fmaf(by, acc[e], s[mt][nt][e]);
+            }
           }
         }
       }
     }
 
-    // running maximum and sum; tokens past the end are masked
+    // running maximum and sum
     float alpha[NT][2];
     bool grew = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = s[mt][nt][e] * sc[nt][e & 1];
-          if (ragged && mt * 16 + (lane >> 2) + ((e >> 1) << 3) >= valid) x = -INFINITY;
-          s[mt][nt][e] = x;
-          mx[e & 1] = fmaxf(mx[e & 1], x);
-        }
+        for (int e = 0; e < 4; ++e)
+          s[mt][nt][e] = fmaf(s[mt][nt][e], sc[nt][e & 1], bias[mt][e >> 1]);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float v = mx[j];
+        float v = fmaxf(fmaxf(s[0][nt][j], s[0][nt][2 + j]), fmaxf(s[1][nt][j], s[1][nt][2 + j]));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-        const float now = fmaxf(ref[nt][j], v - shift);
-        alpha[nt][j] = fast_exp2(ref[nt][j] - now);
-        grew |= now != ref[nt][j];
-        ref[nt][j] = now;
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16)) - shift;
+        const bool up = v > ref[nt][j] + kSlack;
+        alpha[nt][j] = up ? fast_exp2(ref[nt][j] - v) : 1.f;
+        ref[nt][j] = up ? v : ref[nt][j];
+        grew |= up;
       }
     }
     if (__any_sync(0xffffffffu, grew)) rescale(alpha);
@@ -287,51 +315,46 @@ struct Kv4Compute {
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
       const uint32_t vb = block_of(vt, mt);
-      // parameters of tokens 2c, 2c + 1 and 8 + 2c, 9 + 2c: (s, s), (z, z) per group
-      uint32_t w0[2 * NG], w1[2 * NG];
+      // (s, s), (z, z) of tokens 2c, 2c + 1, then of 8 + 2c, 9 + 2c, per group
+      uint32_t w[NG][4];
       const uint32_t par = vb + BS * (D / 2) + (row_of(mt) / 2 + (lane & 3)) * NG * 8;
-      lds_words(par, w0);
-      lds_words(par + 4 * NG * 8, w1);
-      if (ragged) {
-        const int t = mt * 16 + 2 * (lane & 3);
-        const uint32_t m0 = (t < valid ? 0xffffu : 0u) | (t + 1 < valid ? 0xffff0000u : 0u);
-        const uint32_t m1 = (t + 8 < valid ? 0xffffu : 0u) | (t + 9 < valid ? 0xffff0000u : 0u);
-#pragma unroll
-        for (int i = 0; i < 2 * NG; ++i) {
-          w0[i] &= m0;
-          w1[i] &= m1;
-        }
-      }
-      // a value scale of 2^E or more: lower the shift (rare)
-      __half2 most = *reinterpret_cast<__half2*>(&w0[0]);
+      uint32_t large = 0;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        most = __hmax2(most, *reinterpret_cast<__half2*>(&w0[2 * g]));
-        most = __hmax2(most, *reinterpret_cast<__half2*>(&w1[2 * g]));
+        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[g][0]), "=r"(w[g][1]) : "r"(par + g * 8));
+        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
+                     : "=r"(w[g][2]), "=r"(w[g][3])
+                     : "r"(par + 4 * NG * 8 + g * 8));
+        large |= w[g][0] | w[g][2];
       }
-      float top = fmaxf(__low2float(most), __high2float(most));
-      if (__any_sync(0xffffffffu, top * __int_as_float(static_cast<int>(112.f + shift) << 23) > 1.f)) {
-        // 2^-E = 2^(shift - 15); new E: the exponent above the largest scale
+      if (__any_sync(0xffffffffu, (large & 0x40004000u) != 0)) {   // rare
+        float top = 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const float2 x = unpack2<false>(w[g][0]), y = unpack2<false>(w[g][2]);
+          top = fmaxf(fmaxf(top, fmaxf(x.x, x.y)), fmaxf(y.x, y.y));
+        }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = static_cast<int>(__float_as_uint(top) >> 23) - 126;
-        const float now = 15.f - static_cast<float>(min(e, 17));
-        const float down = fast_exp2(now - shift);
-        float by[NT][2];
+        const float now = lowered(top, shift);
+        if (now < shift) {
+          const float down = fast_exp2(now - shift);
+          float by[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+          for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            by[nt][j] = down;
-            ref[nt][j] += shift - now;
+            for (int j = 0; j < 2; ++j) {
+              by[nt][j] = down;
+              ref[nt][j] += shift - now;
+            }
+#pragma unroll
+            for (int m2 = 0; m2 < 2; ++m2)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) s[m2][nt][x] *= down;
           }
-#pragma unroll
-          for (int m2 = 0; m2 < 2; ++m2)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) s[m2][nt][x] *= down;
+          rescale(by);
+          shift = now;
         }
-        rescale(by);
-        shift = now;
       }
       // P^T as B operands: tokens 2c, 2c + 1 (b0) and 8 on (b1) of head lane / 4
       uint32_t b0[NT], b1[NT];
@@ -351,10 +374,10 @@ struct Kv4Compute {
           const uint32_t a = r[2 * gg], b = r[2 * gg + 1], a8 = a >> 8, b8 = b >> 8;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t p0 = hmul2_bits(b0[nt], w0[2 * g]), p1 = hmul2_bits(b1[nt], w1[2 * g]);
+            const uint32_t p0 = hmul2_bits(b0[nt], w[g][0]), p1 = hmul2_bits(b1[nt], w[g][2]);
             mma_16816<false>(o[2 * g][nt], a & M0, a & M1, b & M0, b & M1, p0, p1);
             mma_16816<false>(o[2 * g + 1][nt], a8 & M0, a8 & M1, b8 & M0, b8 & M1, p0, p1);
-            mma_16816<false>(oz[g][nt], w0[2 * g + 1], w0[2 * g + 1], w1[2 * g + 1], w1[2 * g + 1], p0, p1);
+            mma_16816<false>(oz[g][nt], w[g][0], w[g][1], w[g][2], w[g][3], p0, p1);
           }
         }
       }
@@ -380,7 +403,7 @@ struct Kv4Compute {
 #pragma unroll
         for (int i = 0; i < 2 * NG; ++i) {
           const int d = 32 * (i >> 1) + 4 * (lane >> 2) + 2 * (i & 1);
-          const float z = oz[i >> 1][nt][j];
+          const float z = oz[i >> 1][nt][2 + j];
           *reinterpret_cast<float2*>(co + h * D + d) =
               make_float2(fmaf(o[i][nt][j], 0x1p24f, z), fmaf(o[i][nt][2 + j], 0x1p20f, z));
         }
@@ -390,7 +413,7 @@ struct Kv4Compute {
 };
 
 template <bool BF, int D, int BS, int NT>
-__global__ void __launch_bounds__(kKv4Warps * 32) kv4_decode_kernel(const __grid_constant__ Kv4Args p) {
+__global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas(D, NT)) kv4_decode_kernel(const __grid_constant__ Kv4Args p) {
   using Compute = Kv4Compute<BF, D, BS, NT>;
   constexpr int NW = kKv4Warps, NS = kv4_stages(D), NH = Compute::NH;
   constexpr int TILE = Compute::TILE, PER = Compute::PER, STAGE = kv4_stage_bytes(D);
@@ -454,37 +477,41 @@ __global__ void __launch_bounds__(kKv4Warps * 32) kv4_decode_kernel(const __grid
   const uint32_t wbuf = smem_u32(smem + warp * NS * STAGE);
   const uint32_t wbar = smem_u32(&bars[warp * NS]);
   const uint64_t policy = l2_policy_evict_first();      // the cache is read once
-  auto issue = [&](int k) {
-    const int st = k % NS, b0 = (warp + NW * k) * PER;
-    const int nb = min(PER, nblk - b0);
-    const uint32_t bar = wbar + 8 * st, dst = wbuf + st * STAGE;
-    mbar_arrive_expect_tx(bar, nb * 2 * TILE);
-    for (int b = 0; b < nb; ++b) {
-      const size_t at = (static_cast<size_t>(ids[b0 + b]) * a.Hkv + kvh) * TILE;
-      bulk_load(dst + b * TILE, p.k + at, TILE, bar, policy);
-      bulk_load(dst + (PER + b) * TILE, p.v + at, TILE, bar, policy);
-    }
+  // Stage k of this warp: lane 0 announces the bytes, lane 2b + {0, 1} fetches
+  // block b's K or V tile.
+  const uint8_t* src = ((lane & 1) ? p.v : p.k) + static_cast<size_t>(kvh) * TILE;
+  const size_t pitch = static_cast<size_t>(a.Hkv) * TILE;
+  const uint32_t dst0 = wbuf + ((lane & 1) * PER + (lane >> 1)) * TILE;
+  auto issue = [&](int k, int st) {
+    const int b0 = (warp + NW * k) * PER;
+    const uint32_t bar = wbar + 8 * st;
+    if (lane == 0) mbar_arrive_expect_tx(bar, min(PER, nblk - b0) * 2 * TILE);
+    __syncwarp();
+    if (lane < 2 * PER && b0 + (lane >> 1) < nblk)
+      bulk_load(dst0 + st * STAGE, src + ids[b0 + (lane >> 1)] * pitch, TILE, bar, policy);
   };
-  if (lane == 0) {
-    const int pro = my_n < NS ? my_n : NS;
-    for (int k = 0; k < pro; ++k) issue(k);
-  }
+  const int pro = my_n < NS ? my_n : NS;
+  for (int k = 0; k < pro; ++k) issue(k, k);
 
   Compute cs;
   cs.load_q(a.q + (static_cast<size_t>(seq) * a.Hq + h0) * D, heads, a.scale_log2, lane);
   cs.reset();
   bool ok = true;
-  int k = 0;
+  int k = 0, st = 0;
+  uint32_t phase = 0;
   for (; k < my_n; ++k) {
-    const int st = k % NS;
-    const bool done = mbar_wait(wbar + 8 * st, (k / NS) & 1);
+    const bool done = mbar_wait(wbar + 8 * st, phase);
     if (!__all_sync(0xffffffffu, done)) { ok = false; break; }
     const int left = t1 - t0 - (warp + NW * k) * kKv4Tokens;
     cs.stage(wbuf + st * STAGE, min(left, kKv4Tokens), lane);
     __syncwarp();
-    if (lane == 0 && k + NS < my_n) {
+    if (k + NS < my_n) {
       fence_proxy_async_smem();
-      issue(k + NS);
+      issue(k + NS, st);
+    }
+    if (++st == NS) {
+      st = 0;
+      phase ^= 1;
     }
   }
   if (!ok) {

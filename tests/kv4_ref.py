@@ -106,13 +106,14 @@ def to_np(t: torch.Tensor) -> np.ndarray:
 
 def attention(q: np.ndarray, k_cache: np.ndarray, v_cache: np.ndarray, tables: np.ndarray,
               lens: np.ndarray, scale: float):
-    """softmax(scale q . k) . v in 64 bits over the 4-bit caches; also, per out
-    element, the weighted magnitude sum w |v| and, per row, the largest
-    scale * sum |q| |k|-terms, which the error bound needs."""
+    """softmax(scale q . k) . v in 64 bits over the 4-bit caches; also what the
+    error bound needs: per out element the weighted magnitude sum w |v| and the
+    error of weights held in binary16's subnormals (see attention_bound), per
+    row the largest scale * sum |q| |k|-terms."""
     B, Hq, D = q.shape
     Hkv, bs = k_cache.shape[1:3]
     G = Hq // Hkv
-    out, mag = np.zeros((B, Hq, D)), np.zeros((B, Hq, D))
+    out, mag, low = np.zeros((B, Hq, D)), np.zeros((B, Hq, D)), np.zeros((B, Hq, D))
     smag = np.zeros((B, Hq))
     for i, L in enumerate(lens):
         if L == 0:
@@ -120,42 +121,50 @@ def attention(q: np.ndarray, k_cache: np.ndarray, v_cache: np.ndarray, tables: n
         t = np.arange(L)
         slots = tables[i, t // bs].astype(np.int64) * bs + t % bs
         k, v = load(k_cache, slots, False), load(v_cache, slots, True)
-        par = _par(k_cache, slots)
+        par = _magnitudes(k_cache, slots)
+        top = _params(v_cache, slots, True)[..., 0].max((0, 2))     # largest value scale, per kv head
         for h in range(Hq):
             qh, g = q[i, h].astype(np.float64), h // G
             a = scale * (k[:, g] @ qh)
             w = np.exp(a - a.max())
             w /= w.sum()
             out[i, h], mag[i, h] = w @ v[:, g], w @ np.abs(v[:, g])
+            E = max(0.0, np.floor(np.log2(top[g])))
+            low[i, h] = w.max() * 2.0 ** (E - 34) * np.abs(v[:, g]).sum(0)
             smag[i, h] = abs(scale) * (par[:, g] @ np.abs(qh)).max()
-    return out, mag, smag
+    return out, mag, low, smag
 
 
-def _par(k_cache, slots):
-    """s (15 + |z|) of every channel: no partial sum of a key's products is larger."""
-    NB, Hkv, bs, W = k_cache.shape
+def _params(cache, slots, values):
+    """(s, z) of the rows at the slots, [T, Hkv, D/32, 2] in 64 bits."""
+    NB, Hkv, bs, W = cache.shape
     D = W * 8 // 5
-    off = row_offsets(bs, D, False)[:, D // 2:]
-    tiles = k_cache.reshape(NB, Hkv, bs * W)
+    off = row_offsets(bs, D, values)[:, D // 2:]
+    tiles = cache.reshape(NB, Hkv, bs * W)
     rows = np.take_along_axis(tiles[slots // bs], off[slots % bs][:, None].repeat(Hkv, 1), -1)
-    par = np.ascontiguousarray(rows).view(np.float16).astype(np.float64).reshape(len(slots), Hkv, D // 32, 2)
-    return (par[..., 0] * (15 + np.abs(par[..., 1])))[..., None].repeat(32, -1).reshape(len(slots), Hkv, D)
+    return np.ascontiguousarray(rows).view(np.float16).astype(np.float64).reshape(len(slots), Hkv, D // 32, 2)
 
 
-def attention_bound(out, mag, smag, lens, eps: float, D: int) -> np.ndarray:
+def _magnitudes(k_cache, slots):
+    """s (15 + |z|) of every channel: no partial sum of a key's products is larger."""
+    par = _params(k_cache, slots, False)
+    return (par[..., 0] * (15 + np.abs(par[..., 1])))[..., None].repeat(32, -1).reshape(*par.shape[:2], -1)
+
+
+def attention_bound(out, mag, low, smag, eps: float, D: int) -> np.ndarray:
     """How far a correct result may be off, element by element:
      - the store: half a step, eps / 2 of the value (and half the smallest
        subnormal binary16, 2^-25);
-     - each weight: rounded to binary16 and again after its scale, 2^-11 each,
-       exp2 to 2^-22, the sums in FP32 (at most 2^-24 a term, pairwise within
-       a warp: 2^-14 covers 2^10 terms in a row); weights below 2^-39 of the
-       largest may vanish (one per token);
+     - each weight: rounded to binary16 and again after its scale, 2^-11 each
+       at most, exp2 to 2^-22, the sums in FP32 (at most 2^-24 a term, pairwise
+       within a warp: 2^-14 covers 2^10 terms in a row);
+     - weights below binary16's smallest normal number are off by up to half
+       its smallest step, 2^-25, where the largest weight is at least 2^(9-E)
+       (E: the exponent of the largest value scale, at least 0): 2^(E-34) of
+       the largest weight for each token, times its |v|;
      - each logit: FP32 products and sums of at most D / 8 + 8 steps, of
        magnitude smag (in the exponent, so it counts relative to the weight),
        once in the weight and once in the normaliser."""
     logits = 2 * (D / 8 + 8) * 2.0 ** -24 * smag[..., None]
     weights = 2 * 2.0 ** -11 + 2.0 ** -22 + 2.0 ** -14
-    n = np.asarray(lens, np.float64)[:, None, None]
-    peak = mag.max(-1, keepdims=True)
-    return (eps / 2 * np.abs(out) + 2.0 ** -25 + (weights + logits) * mag
-            + n * 2.0 ** -38 * np.maximum(peak, mag))
+    return eps / 2 * np.abs(out) + 2.0 ** -25 + (weights + logits) * mag + low

@@ -154,11 +154,11 @@ def check(pkv, b, d=None, **kw):
     d = d or device(b)
     out = pkv.kv4_attn_decode(**d, **kw)
     assert pkv.get_device_error() == 0
-    want, mag, smag = R.attention(R.to_np(b["q"]), b["kc"], b["vc"], b["tables"], b["lens"], b["scale"])
+    want, mag, low, smag = R.attention(R.to_np(b["q"]), b["kc"], b["vc"], b["tables"], b["lens"], b["scale"])
     got = R.to_np(out).astype(np.float64)
     assert np.all(np.isfinite(got))
     err = np.abs(got - want)
-    bound = R.attention_bound(want, mag, smag, b["lens"], EPS[b["q"].dtype], b["q"].shape[2])
+    bound = R.attention_bound(want, mag, low, smag, EPS[b["q"].dtype], b["q"].shape[2])
     assert np.all(err <= bound), f"{(err > bound).sum()} out of tolerance, worst {(err / bound).max():.2f} of it"
     return out
 
