@@ -38,6 +38,8 @@
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "pkv_geometry.h"
 #include "pkv_internal.h"
 #include "pkv_kv4.cuh"
@@ -60,13 +62,18 @@ constexpr int kv4_stages(int D) { return D == 64 ? 4 : 2; }
 // Resident CTAs per SM that the registers are budgeted for.
 constexpr int kv4_ctas(int D, int NT) { return NT == 1 && D <= 128 ? 4 : (D == 64 ? 3 : 2); }
 constexpr int kv4_stage_bytes(int D) { return 2 * kv4_tile_bytes(D, kKv4Tokens); }
-constexpr int kv4_merge_bytes(int D, int NT) { return kKv4Warps * 8 * NT * (D + 2) * 4; }
 constexpr int kv4_ring_bytes(int D) { return kKv4Warps * kv4_stages(D) * kv4_stage_bytes(D); }
+// The warps' merge reuses the ring: per warp and head the accumulator row
+// (padded by 8 floats against bank conflicts), the maximum and the sum.
+constexpr int kv4_row(int D) { return D + 8; }
+constexpr int kv4_merge_bytes(int D, int NT) { return kKv4Warps * 8 * NT * (kv4_row(D) + 2) * 4; }
+// Query fragments, per-group sums, scales and maxima, shared by the warps.
+constexpr int kv4_query_bytes(int D, int NT) { return (D / 32) * NT * 512 + (D / 32 + 1 + kKv4Warps) * 8 * NT * 4; }
 constexpr int kv4_tail(int D, int NT) {
   return ((kv4_ring_bytes(D) > kv4_merge_bytes(D, NT) ? kv4_ring_bytes(D) : kv4_merge_bytes(D, NT)) + 127) & ~127;
 }
 constexpr int kv4_smem(int D, int NT) {
-  return kv4_tail(D, NT) + kKv4Warps * kv4_stages(D) * 8 + kMaxBlocksPerCta * 4 + 128;
+  return kv4_tail(D, NT) + kv4_query_bytes(D, NT) + kKv4Warps * kv4_stages(D) * 8 + kMaxBlocksPerCta * 4 + 128;
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar,
@@ -78,17 +85,55 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-template <int N>
+// for (i = 0; i < N; ++i) f(i) with i a constant, so that offsets can be
+// immediates of the shared-memory instructions.
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    static_for<N, I + 1>(f);
+  }
+}
+
+template <int OFF, int N>
 __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
   if constexpr (N == 2) {
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2+%3];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr), "n"(OFF));
   } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 4)
-      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+    static_for<N / 4>([&](auto j) {
+      constexpr int i = 4 * j;
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4+%5];"
                    : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
-                   : "r"(addr + i * 4));
+                   : "r"(addr), "n"(OFF + 4 * i));
+    });
   }
+}
+
+template <int OFF>
+__device__ __forceinline__ void lds_pair(uint32_t addr, uint32_t& a, uint32_t& b) {
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2+%3];" : "=r"(a), "=r"(b) : "r"(addr), "n"(OFF));
+}
+
+template <int OFF, bool TRANS>
+__device__ __forceinline__ void ldm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  if constexpr (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4+%5];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr), "n"(OFF));
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4+%5];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr), "n"(OFF));
+}
+
+// d += A B, binary16 operands, FP32 accumulators (registers only: free to be
+// scheduled between the loads).
+__device__ __forceinline__ void mma_codes(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
@@ -114,57 +159,85 @@ struct Kv4Compute {
   float ref[NT][2], l[NT][2];              // running maximum less shift; sum
   float shift;                             // kShift - E
 
-  // Heads g0 + nt * 8 + lane / 4 of the group's q rows at `qg` (zeros past G).
-  // A head's row is scaled by the power of two that brings its largest element
-  // into [2^14, 2^15): exact in binary16 for either type, but for elements
-  // 2^-28 times the largest or less.
-  __device__ __forceinline__ void load_q(const uint16_t* qg, int heads, float scale_log2, int lane) {
-    const int c = lane & 3;
+  // The queries of the CTA's heads as B fragments, prepared once: warp w does
+  // the channel groups w, w + 4, ... and every warp reads all of them back from
+  // `qsm`.  A head's row is scaled by the power of two that brings its largest
+  // element into [2^14, 2^15): exact in binary16 for either type, but for
+  // elements 2^-28 times the largest or less.
+  __device__ __forceinline__ void load_q(const uint16_t* qg, int heads, float scale_log2, uint8_t* qsm,
+                                         int warp, int lane) {
+    constexpr int NW = kKv4Warps, PG = (NG + NW - 1) / NW;
+    uint4* frag = reinterpret_cast<uint4*>(qsm);                       // [NG][NT][32]
+    float* sums = reinterpret_cast<float*>(qsm + NG * NT * 512);       // [NG][NH]
+    float* scales = sums + NG * NH;                                    // [NH]
+    float* tops = scales + NH;                                         // [NW][NH]
+    const int c = lane & 3, n = lane >> 2;
+    uint4 u[PG][NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int h = nt * 8 + (lane >> 2);
-      float x[NG][8];
       float top = 0.f;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (h < heads) u = __ldg(reinterpret_cast<const uint4*>(qg + h * D + g * 32 + c * 8));
-        const float2 f0 = unpack2<BF>(u.x), f1 = unpack2<BF>(u.y), f2 = unpack2<BF>(u.z),
-                     f3 = unpack2<BF>(u.w);
-        x[g][0] = f0.x; x[g][1] = f0.y; x[g][2] = f1.x; x[g][3] = f1.y;
-        x[g][4] = f2.x; x[g][5] = f2.y; x[g][6] = f3.x; x[g][7] = f3.y;
+      for (int i = 0; i < PG; ++i) {
+        const int g = warp + i * NW, h = nt * 8 + n;
+        u[i][nt] = make_uint4(0, 0, 0, 0);
+        if (g < NG && h < heads)
+          u[i][nt] = __ldg(reinterpret_cast<const uint4*>(qg + h * D + g * 32 + c * 8));
+        const uint32_t x[4] = {u[i][nt].x, u[i][nt].y, u[i][nt].z, u[i][nt].w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[g][i]));
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = unpack2<BF>(x[k]);
+          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
       }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      if (c == 0) tops[warp * NH + nt * 8 + n] = top;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int h = nt * 8 + n;
+      float top = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) top = fmaxf(top, tops[w * NH + h]);
       int e = 14 + 127 - static_cast<int>(__float_as_uint(top) >> 23);   // infinity: a finite factor
       e = top > 0.f ? min(e, 120) : 0;
       const float f = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      const float back = scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * 0x1p24f;
-      sc[nt][0] = __shfl_sync(0xffffffffu, back, 8 * c);
-      sc[nt][1] = __shfl_sync(0xffffffffu, back, 8 * c + 4);
+      if (warp == 0 && c == 0)
+        scales[h] = scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * 0x1p24f;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[g][i] *= f;
-          if (i & 1) x[g][i] *= 0.0625f;
-        }
+      for (int i = 0; i < PG; ++i) {
+        const int g = warp + i * NW;
+        if (g >= NG) break;
+        const float2 x01 = unpack2<BF>(u[i][nt].x), x23 = unpack2<BF>(u[i][nt].y),
+                     x45 = unpack2<BF>(u[i][nt].z), x67 = unpack2<BF>(u[i][nt].w);
+        const float fo = f * 0.0625f;
         // k index 2c + {0, 1} of step 0: channels 0 and 4 of the lane's eight,
         // then 2 and 6; of step 1: 1 and 5, then 3 and 7 (16 times their code)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int i = (b & 1) * 2 + (b >> 1);
-          qf[g][nt][b] = pack2<false>(x[g][i], x[g][i + 4]);
-          const float2 r = unpack2<false>(qf[g][nt][b]);
-          sum += (r.x + r.y) * (b >> 1 ? 0x1p-20f : 0x1p-24f);
-        }
+        const uint32_t r0 = pack2<false>(x01.x * f, x45.x * f), r1 = pack2<false>(x23.x * f, x67.x * f);
+        const uint32_t r2 = pack2<false>(x01.y * fo, x45.y * fo), r3 = pack2<false>(x23.y * fo, x67.y * fo);
+        frag[(g * NT + nt) * 32 + lane] = make_uint4(r0, r1, r2, r3);
+        const float2 s0 = unpack2<false>(r0), s1 = unpack2<false>(r1), s2 = unpack2<false>(r2),
+                     s3 = unpack2<false>(r3);
+        float sum = ((s0.x + s0.y) + (s1.x + s1.y)) * 0x1p-24f + ((s2.x + s2.y) + (s3.x + s3.y)) * 0x1p-20f;
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        qs[g][nt][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
-        qs[g][nt][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+        if (c == 0) sums[g * NH + h] = sum;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float2 x = *reinterpret_cast<const float2*>(scales + nt * 8 + 2 * c);
+      sc[nt][0] = x.x;
+      sc[nt][1] = x.y;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const uint4 v = frag[(g * NT + nt) * 32 + lane];
+        qf[g][nt][0] = v.x; qf[g][nt][1] = v.y; qf[g][nt][2] = v.z; qf[g][nt][3] = v.w;
+        const float2 y = *reinterpret_cast<const float2*>(sums + g * NH + nt * 8 + 2 * c);
+        qs[g][nt][0] = y.x;
+        qs[g][nt][1] = y.y;
       }
     }
   }
@@ -200,22 +273,21 @@ struct Kv4Compute {
     }
   }
 
-  // Address of the 16-token half `mt` of a stage's K or V (block base and row).
-  static __device__ __forceinline__ uint32_t block_of(uint32_t base, int mt) {
-    return PER == 2 ? base + mt * TILE : base;
-  }
-  static constexpr int row_of(int mt) { return PER == 2 ? 0 : mt * 16; }
+  // Offset of the 16-token half `mt` in a stage's K or V: its block, and its row there.
+  static __host__ __device__ constexpr int block_of(int mt) { return PER == 2 ? mt * TILE : 0; }
+  static __host__ __device__ constexpr int row_of(int mt) { return PER == 2 ? 0 : mt * 16; }
+  static constexpr int VT = PER * TILE;           // V behind K
+  static constexpr int PAR = BS * (D / 2);        // parameters behind a tile's codes
 
   // Clear the parameters of the tokens from `valid` on, so that whatever bytes
   // lie behind a sequence's end (NaN scales among them) count for nothing.
   static __device__ __forceinline__ void clear_tail(uint32_t kt, int valid, int lane) {
-    const uint32_t vt = kt + PER * TILE;
     for (int i = lane; i < kKv4Tokens * NG; i += 32) {
       const int t = i / NG, g = i % NG;
       if (t < valid) continue;
       const int mt = t / 16, r = row_of(mt) + t % 16;
-      const uint32_t kp = block_of(kt, mt) + kv4_k_par_off<D>(BS, r, g);
-      const uint32_t vp = block_of(vt, mt) + kv4_v_par_off<D>(BS, r, g);
+      const uint32_t kp = kt + block_of(mt) + kv4_k_par_off<D>(BS, r, g);
+      const uint32_t vp = kt + VT + block_of(mt) + kv4_v_par_off<D>(BS, r, g);
       asm volatile("st.shared.b32 [%0], %1;" ::"r"(kp), "r"(0) : "memory");
       asm volatile("st.shared.b16 [%0], %1;" ::"r"(vp), "h"(static_cast<short>(0)) : "memory");
       asm volatile("st.shared.b16 [%0], %1;" ::"r"(vp + 4), "h"(static_cast<short>(0)) : "memory");
@@ -229,45 +301,37 @@ struct Kv4Compute {
     return fminf(shift, kShift - static_cast<float>(min(max(e, 0), 17)));
   }
 
-  // 32 tokens at `kt` (K) and `kt + PER * TILE` (V), the first `valid` of them real.
-  __device__ __forceinline__ void stage(uint32_t kt, int valid, int lane) {
-    const uint32_t vt = kt + PER * TILE;
-    const int rr = lane & 7, half = (lane >> 3) & 1, hi = lane >> 4;
-    // codes of (row half * 8 + rr, group hi of a pair): the lane's ldmatrix row
-    const uint32_t lrow = (half * 8 + rr) * (D / 2);
-    const int sw = rr * NG / 8;
-    // added to the logits of the lane's tokens: minus infinity past the end
-    float bias[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-    if (valid < kKv4Tokens) {
-      clear_tail(kt, valid, lane);
+  // 32 tokens at `kt` (K) and `kt + VT` (V), the first `valid` of them real.
+  // `lrow[i]`: the lane's ldmatrix row of the group pair i, relative to codes.
+  __device__ __forceinline__ void stage(uint32_t kt, int valid, const uint32_t (&lrow)[NG / 2], int lane) {
+    const bool ragged = valid < kKv4Tokens;
+    if (ragged) clear_tail(kt, valid, lane);
+    uint32_t at[NG / 2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        bias[i >> 1][i & 1] = i * 8 + (lane >> 2) < valid ? 0.f : -INFINITY;
-    }
+    for (int i = 0; i < NG / 2; ++i) at[i] = kt + lrow[i];
+    const uint32_t kpar = kt + (lane >> 2) * NG * 4, vpar = kt + (lane & 3) * NG * 8;
 
     float s[2][NT][4];
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      const uint32_t kb = block_of(kt, mt);
+    static_for<2>([&](auto mt) {
+      constexpr int KB = block_of(mt) + row_of(mt) * (D / 2);
+      constexpr int KP = block_of(mt) + PAR + row_of(mt) * NG * 4;
       uint32_t plo[NG], phi[NG];
-      const uint32_t par = kb + BS * (D / 2) + (row_of(mt) + (lane >> 2)) * NG * 4;
-      lds_words(par, plo);
-      lds_words(par + 8 * NG * 4, phi);
-#pragma unroll
-      for (int g0 = 0; g0 < NG; g0 += 2) {
+      lds_words<KP>(kpar, plo);
+      lds_words<KP + 8 * NG * 4>(kpar, phi);
+      static_for<NG / 2>([&](auto gp) {
         uint32_t r[4];
-        ldmatrix_x4(kb + row_of(mt) * (D / 2) + lrow + (((g0 + hi) ^ sw) << 4), r[0], r[1], r[2], r[3]);
+        ldm_x4<KB, false>(at[gp], r);
 #pragma unroll
         for (int gg = 0; gg < 2; ++gg) {
-          const int g = g0 + gg;
+          const int g = 2 * gp + gg;
           const uint32_t a = r[2 * gg], b = r[2 * gg + 1], a8 = a >> 8, b8 = b >> 8;
           const float2 lo = unpack2<false>(plo[g]), up = unpack2<false>(phi[g]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float acc[4] = {lo.y * qs[g][nt][0], lo.y * qs[g][nt][1], up.y * qs[g][nt][0],
                             up.y * qs[g][nt][1]};
-            mma_16816<false>(acc, a & M0, b & M0, a8 & M0, b8 & M0, qf[g][nt][0], qf[g][nt][1]);
-            mma_16816<false>(acc, a & M1, b & M1, a8 & M1, b8 & M1, qf[g][nt][2], qf[g][nt][3]);
+            mma_codes(acc, a & M0, b & M0, a8 & M0, b8 & M0, qf[g][nt][0], qf[g][nt][1]);
+            mma_codes(acc, a & M1, b & M1, a8 & M1, b8 & M1, qf[g][nt][2], qf[g][nt][3]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float by = e < 2 ? lo.x : up.x;
@@ -275,8 +339,8 @@ struct Kv4Compute {
             }
           }
         }
-      }
-    }
+      });
+    });
 
     // running maximum and sum
     float alpha[NT][2];
@@ -286,8 +350,19 @@ struct Kv4Compute {
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          s[mt][nt][e] = fmaf(s[mt][nt][e], sc[nt][e & 1], bias[mt][e >> 1]);
+        for (int e = 0; e < 4; ++e) s[mt][nt][e] *= sc[nt][e & 1];
+    }
+    if (ragged) {   // minus infinity past the end
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (mt * 16 + (e >> 1) * 8 + (lane >> 2) >= valid) s[mt][nt][e] = -INFINITY;
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         float v = fmaxf(fmaxf(s[0][nt][j], s[0][nt][2 + j]), fmaxf(s[1][nt][j], s[1][nt][2 + j]));
@@ -312,21 +387,17 @@ struct Kv4Compute {
           l[nt][e & 1] += p;
         }
 
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      const uint32_t vb = block_of(vt, mt);
+    static_for<2>([&](auto mt) {
+      constexpr int VB = VT + block_of(mt) + row_of(mt) * (D / 2);
+      constexpr int VP = VT + block_of(mt) + PAR + row_of(mt) / 2 * NG * 8;
       // (s, s), (z, z) of tokens 2c, 2c + 1, then of 8 + 2c, 9 + 2c, per group
       uint32_t w[NG][4];
-      const uint32_t par = vb + BS * (D / 2) + (row_of(mt) / 2 + (lane & 3)) * NG * 8;
       uint32_t large = 0;
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[g][0]), "=r"(w[g][1]) : "r"(par + g * 8));
-        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
-                     : "=r"(w[g][2]), "=r"(w[g][3])
-                     : "r"(par + 4 * NG * 8 + g * 8));
+      static_for<NG>([&](auto g) {
+        lds_pair<VP + g * 8>(vpar, w[g][0], w[g][1]);
+        lds_pair<VP + (4 * NG + g) * 8>(vpar, w[g][2], w[g][3]);
         large |= w[g][0] | w[g][2];
-      }
+      });
       if (__any_sync(0xffffffffu, (large & 0x40004000u) != 0)) {   // rare
         float top = 0.f;
 #pragma unroll
@@ -363,25 +434,23 @@ struct Kv4Compute {
         b0[nt] = movmatrix_trans(pack2<false>(s[mt][nt][0], s[mt][nt][1]));
         b1[nt] = movmatrix_trans(pack2<false>(s[mt][nt][2], s[mt][nt][3]));
       }
-#pragma unroll
-      for (int g0 = 0; g0 < NG; g0 += 2) {
+      static_for<NG / 2>([&](auto gp) {
         uint32_t r[4];
-        ldmatrix_x4_trans(vb + row_of(mt) * (D / 2) + lrow + (((g0 + hi) ^ sw) << 4), r[0], r[1], r[2],
-                          r[3]);
+        ldm_x4<VB, true>(at[gp], r);
 #pragma unroll
         for (int gg = 0; gg < 2; ++gg) {
-          const int g = g0 + gg;
+          const int g = 2 * gp + gg;
           const uint32_t a = r[2 * gg], b = r[2 * gg + 1], a8 = a >> 8, b8 = b >> 8;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const uint32_t p0 = hmul2_bits(b0[nt], w[g][0]), p1 = hmul2_bits(b1[nt], w[g][2]);
-            mma_16816<false>(o[2 * g][nt], a & M0, a & M1, b & M0, b & M1, p0, p1);
-            mma_16816<false>(o[2 * g + 1][nt], a8 & M0, a8 & M1, b8 & M0, b8 & M1, p0, p1);
-            mma_16816<false>(oz[g][nt], w[g][0], w[g][1], w[g][2], w[g][3], p0, p1);
+            mma_codes(o[2 * g][nt], a & M0, a & M1, b & M0, b & M1, p0, p1);
+            mma_codes(o[2 * g + 1][nt], a8 & M0, a8 & M1, b8 & M0, b8 & M1, p0, p1);
+            mma_codes(oz[g][nt], w[g][0], w[g][1], w[g][2], w[g][3], p0, p1);
           }
         }
-      }
-    }
+      });
+    });
   }
 
   // Leave each head's (m, l, o) for the CTA merge.  Rows lane / 4 of tile
@@ -404,7 +473,7 @@ struct Kv4Compute {
         for (int i = 0; i < 2 * NG; ++i) {
           const int d = 32 * (i >> 1) + 4 * (lane >> 2) + 2 * (i & 1);
           const float z = oz[i >> 1][nt][2 + j];
-          *reinterpret_cast<float2*>(co + h * D + d) =
+          *reinterpret_cast<float2*>(co + h * kv4_row(D) + d) =
               make_float2(fmaf(o[i][nt][j], 0x1p24f, z), fmaf(o[i][nt][2 + j], 0x1p20f, z));
         }
       }
@@ -422,7 +491,8 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas(D, NT)) kv4_decode_ke
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kv4_tail(D, NT));
+  uint8_t* qsm = smem + kv4_tail(D, NT);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(qsm + kv4_query_bytes(D, NT));
   int* ids = reinterpret_cast<int*>(bars + NW * NS);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -494,8 +564,12 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas(D, NT)) kv4_decode_ke
   for (int k = 0; k < pro; ++k) issue(k, k);
 
   Compute cs;
-  cs.load_q(a.q + (static_cast<size_t>(seq) * a.Hq + h0) * D, heads, a.scale_log2, lane);
+  cs.load_q(a.q + (static_cast<size_t>(seq) * a.Hq + h0) * D, heads, a.scale_log2, qsm, warp, lane);
   cs.reset();
+  uint32_t lrow[Compute::NG / 2];
+#pragma unroll
+  for (int i = 0; i < Compute::NG / 2; ++i)
+    lrow[i] = kv4_code_off<D>(lane & 15, 2 * i + (lane >> 4));
   bool ok = true;
   int k = 0, st = 0;
   uint32_t phase = 0;
@@ -503,7 +577,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas(D, NT)) kv4_decode_ke
     const bool done = mbar_wait(wbar + 8 * st, phase);
     if (!__all_sync(0xffffffffu, done)) { ok = false; break; }
     const int left = t1 - t0 - (warp + NW * k) * kKv4Tokens;
-    cs.stage(wbuf + st * STAGE, min(left, kKv4Tokens), lane);
+    cs.stage(wbuf + st * STAGE, min(left, kKv4Tokens), lrow, lane);
     __syncwarp();
     if (k + NS < my_n) {
       fence_proxy_async_smem();
@@ -522,30 +596,36 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas(D, NT)) kv4_decode_ke
   }
   if (__syncthreads_or(!ok)) return;   // the ring may still be filling: no result
 
-  float* cm = reinterpret_cast<float*>(smem);
+  float* co = reinterpret_cast<float*>(smem);
+  float* cm = co + NW * NH * kv4_row(D);
   float* cl = cm + NW * NH;
-  float* co = cl + NW * NH;
-  cs.publish(cm + warp * NH, cl + warp * NH, co + warp * NH * D, lane);
+  cs.publish(cm + warp * NH, cl + warp * NH, co + warp * NH * kv4_row(D), lane);
   __syncthreads();
   const bool single = (L + a.P - 1) / a.P == 1;
-  for (int i = threadIdx.x; i < heads * D; i += NW * 32) {
-    const int h = i / D, d = i - h * D;
+  for (int i = threadIdx.x; i < heads * (D / 4); i += NW * 32) {
+    const int h = i / (D / 4), d = i % (D / 4) * 4;
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < NW; ++w) M = fmaxf(M, cm[w * NH + h]);
-    float acc = 0.f, lsum = 0.f;
+    float x[4] = {0.f, 0.f, 0.f, 0.f}, lsum = 0.f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       const float f = fast_exp2(cm[w * NH + h] - M);
-      acc = fmaf(f, co[(w * NH + h) * D + d], acc);
+      const float4 v = *reinterpret_cast<const float4*>(co + (w * NH + h) * kv4_row(D) + d);
+      x[0] = fmaf(f, v.x, x[0]);
+      x[1] = fmaf(f, v.y, x[1]);
+      x[2] = fmaf(f, v.z, x[2]);
+      x[3] = fmaf(f, v.w, x[3]);
       lsum = fmaf(f, cl[w * NH + h], lsum);
     }
     const size_t row = static_cast<size_t>(seq) * a.Hq + h0 + h;
     if (single) {
-      a.out[row * D + d] = to_elem<BF>(acc / lsum);
+      const float r = 1.f / lsum;
+      *reinterpret_cast<uint2*>(a.out + row * D + d) =
+          make_uint2(pack2<BF>(x[0] * r, x[1] * r), pack2<BF>(x[2] * r, x[3] * r));
     } else {
       const size_t pr = row * a.S + split;
-      a.part_o[pr * D + d] = acc;
+      *reinterpret_cast<float4*>(a.part_o + pr * D + d) = make_float4(x[0], x[1], x[2], x[3]);
       if (d == 0) a.part_ml[pr] = make_float2(M, lsum);
     }
   }
