@@ -7,22 +7,22 @@ namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// 8-head tiles of one CTA: groups of up to 8 query heads take one, wider ones
-// two (head_dim 256: one, whose accumulators fill the registers), in as many
-// CTAs as the group needs.
-int kv4_tiles(const pkv_shape* s) {
-  return s->head_dim <= 128 && s->num_q_heads / s->num_kv_heads > 8 ? 2 : 1;
+// CTAs that share the query heads of one kv head.
+int kv4_chunks(const pkv_shape* s) {
+  const int G = s->num_q_heads / s->num_kv_heads;
+  const int heads = kv4_columns(s->head_dim, G) * kv4_tiles(s->head_dim, G);
+  return (G + heads - 1) / heads;
 }
 
 int kv4_plan(const pkv_shape* s, int sms, pkv_plan* plan) {
-  const int nt = kv4_tiles(s), D = s->head_dim, bs = s->block_size;
+  const int D = s->head_dim, bs = s->block_size;
   const int G = s->num_q_heads / s->num_kv_heads;
   *plan = pkv_plan{};
   plan->variant = 3;
   plan->warps_per_cta = kKv4Warps;
   plan->stages_per_warp = kv4_stages(D);
   const long long units =
-      static_cast<long long>(s->num_seqs) * s->num_kv_heads * ((G + 8 * nt - 1) / (8 * nt));
+      static_cast<long long>(s->num_seqs) * s->num_kv_heads * kv4_chunks(s);
   const int maxL = s->max_context_len;
   const int gran = kKv4Warps * kKv4Tokens;
   const int cap = kMaxBlocksPerCta * bs;
@@ -31,7 +31,7 @@ int kv4_plan(const pkv_shape* s, int sms, pkv_plan* plan) {
     P = (static_cast<long long>(s->split_tokens) + bs - 1) / bs * bs;
   } else {
     P = 2048;
-    const long long slots = static_cast<long long>(sms) * kv4_ctas(D, nt);
+    const long long slots = static_cast<long long>(sms) * kv4_ctas(D, kv4_columns(D, G), kv4_tiles(D, G));
     if (units > 0 && units * ((maxL + P - 1) / P) < 4 * slots) {
       const long long S = slots / units > 0 ? slots / units : 1;
       P = (maxL + S - 1) / S;
@@ -128,8 +128,8 @@ extern "C" int pkv_kv4_attn_decode(const pkv_shape* s, const void* q, const void
   a.d.scale_log2 = scale * 1.4426950408889634f;  // log2(e)
   a.k = static_cast<const uint8_t*>(k_cache);
   a.v = static_cast<const uint8_t*>(v_cache);
-  const int D = s->head_dim, nt = kv4_tiles(s);
-  a.chunks = (a.d.G + 8 * nt - 1) / (8 * nt);
+  const int D = s->head_dim;
+  a.chunks = kv4_chunks(s);
   if (plan.workspace_bytes > 0) {
     const size_t rows = static_cast<size_t>(s->num_seqs) * s->num_q_heads * plan.num_splits;
     a.d.part_o = static_cast<float*>(workspace);
@@ -138,7 +138,7 @@ extern "C" int pkv_kv4_attn_decode(const pkv_shape* s, const void* q, const void
   const bool bf = s->dtype == PKV_BF16;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = (bf ? launch_kv4_bf16 : launch_kv4_f16)(
-      a, D, s->block_size, nt, static_cast<unsigned>(plan.grid_ctas), st);
+      a, D, s->block_size, static_cast<unsigned>(plan.grid_ctas), st);
   if (e != cudaSuccess) return PKV_ERR_CUDA;
   count_launch();
   if (plan.num_splits > 1) {

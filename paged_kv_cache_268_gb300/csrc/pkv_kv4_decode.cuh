@@ -9,26 +9,34 @@
 //
 // Codes as operands: a nibble masked into the low bits of a binary16 is the
 // subnormal n * 2^-24 (0x000f) or n * 2^-20 (0x00f0), exactly, and the tensor
-// cores multiply subnormals exactly.  One 32-bit word of codes thus becomes
-// four operand registers with a shift and four ANDs, and the powers of two
-// come out of the results: for the keys through q (scaled to each head's
-// largest element, the odd nibbles' channels by another 2^-4), for the values
-// at the very end (even and odd nibbles are different output rows).
+// cores multiply subnormals exactly and at full rate.  One 32-bit word of codes
+// thus becomes four operand registers with a shift and four ANDs, and the
+// powers of two come out of the results: for the keys through q (each head's
+// row scaled by the power of two that brings its largest element into [2^14,
+// 2^15), the odd nibbles' channels by another 2^-4), for the values at the very
+// end (even and odd nibbles are different output rows).  (A code in the low
+// half of a byte is also n * 2^-9 in e4m3, one AND for four; but this machine
+// has no such mma.sync, the compiler converts every operand: 1.2x slower.)
 //
-// One CTA handles one (sequence, kv head, up to 8 NT query heads, partition).
-// Each warp owns a ring of NS stages of 32 tokens (two 16-token blocks or one
-// of 32), each block's tile a contiguous run of bytes that lane 0 fetches with
-// one untiled bulk copy per block for K and for V.  Per 16 tokens:
-//   S[16 tok x 8 heads]: ldmatrix gives a lane one word (8 channels) of each of
-//     two tokens; two k16 steps per group.
-//   P' = P s in binary16, per group (a weight's rounding, 2^-12 of it at most,
+// Columns: an operand tile has 8 columns.  Where the CTA's query heads HC are
+// fewer, GS = 8 / HC channel groups share it: column (j, h) holds head h, for
+// keys only in the channels of the j-th group (so one accumulator collects
+// the sums of GS groups side by side), for values with that group's scales.
+// A lane then applies one group's parameters instead of GS of them.
+//
+// One CTA handles one (sequence, kv head, chunk of query heads, partition).
+// Each warp owns a ring of stages of 32 tokens (two 16-token blocks or one of
+// 32), each block's tile a contiguous run of bytes fetched with one untiled
+// bulk copy for K and one for V.  Per 16 tokens:
+//   S[16 tok x 8 columns]: ldmatrix gives a lane one word (8 channels) of each
+//     of two tokens; two k16 steps per group.
+//   P' = P s in binary16, per column (a weight's rounding, 2^-12 of it at most,
 //     and its product's are the only ones below FP32; P is binary16 for
 //     bfloat16 inputs too, which have fewer bits).
-//   O^T[32 ch x 8 heads] += codes^T P': ldmatrix.trans puts two neighbouring
+//   O^T[32 ch x 8 columns] += codes^T P': ldmatrix.trans puts two neighbouring
 //     tokens' words side by side; two m16 tiles per group.
 //   z^T P' with the pairs (s, z) as they lie in the cache for the A operand:
-//     rows 8 on give the group's zero-point sum for each head, in the same
-//     lanes as O^T (one more m16 tile; its other rows are not used).
+//     rows 8 on give the zero-point sums (one m16 tile per GS groups).
 // P is scaled by 2^(9-E), E >= 0 from the largest value scale so far, so that
 // neither small weights nor small scales fall out of binary16; the running sum
 // carries the same factor.  The running maximum follows the true one only when
@@ -60,15 +68,22 @@ constexpr int kKv4Tokens = 32;   // per stage
 // Stages per warp: about 40-60 KB of ring per CTA.
 constexpr int kv4_stages(int D) { return D == 64 ? 4 : 2; }
 // Resident CTAs per SM that the registers are budgeted for.
-constexpr int kv4_ctas(int D, int NT) { return NT == 1 && D <= 128 ? 4 : (D == 64 ? 3 : 2); }
+constexpr int kv4_ctas(int D, int HC, int NT) {
+  return D * NT == 64 || (D * NT == 128 && HC < 8) ? 4 : (D * NT == 128 ? 3 : 2);
+}
+// Query heads that share the 8 columns of a tile (HC), and tiles per CTA (NT),
+// for a group of G query heads: as few columns as the group needs; from 9 heads
+// on two tiles (head_dim 256: one, whose accumulators fill the registers).
+constexpr int kv4_columns(int D, int G) { return G <= 2 && D > 64 ? 2 : (G <= 4 ? 4 : 8); }
+constexpr int kv4_tiles(int D, int G) { return D <= 128 && G > 8 ? 2 : 1; }
 constexpr int kv4_stage_bytes(int D) { return 2 * kv4_tile_bytes(D, kKv4Tokens); }
 constexpr int kv4_ring_bytes(int D) { return kKv4Warps * kv4_stages(D) * kv4_stage_bytes(D); }
 // The warps' merge reuses the ring: per warp and head the accumulator row
 // (padded by 8 floats against bank conflicts), the maximum and the sum.
 constexpr int kv4_row(int D) { return D + 8; }
 constexpr int kv4_merge_bytes(int D, int NT) { return kKv4Warps * 8 * NT * (kv4_row(D) + 2) * 4; }
-// Query fragments, per-group sums, scales and maxima, shared by the warps.
-constexpr int kv4_query_bytes(int D, int NT) { return (D / 32) * NT * 512 + (D / 32 + 1 + kKv4Warps) * 8 * NT * 4; }
+// Query fragments, per-group sums and maxima, scales.
+constexpr int kv4_query_bytes(int D, int NT) { return (D / 32) * NT * 512 + (2 * (D / 32) + 1) * 8 * NT * 4; }
 constexpr int kv4_tail(int D, int NT) {
   return ((kv4_ring_bytes(D) > kv4_merge_bytes(D, NT) ? kv4_ring_bytes(D) : kv4_merge_bytes(D, NT)) + 127) & ~127;
 }
@@ -85,6 +100,12 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // for (i = 0; i < N; ++i) f(i) with i a constant, so that offsets can be
 // immediates of the shared-memory instructions.
 template <int N, int I = 0, class F>
@@ -97,7 +118,9 @@ __device__ __forceinline__ void static_for(F&& f) {
 
 template <int OFF, int N>
 __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
-  if constexpr (N == 2) {
+  if constexpr (N == 1) {
+    asm volatile("ld.shared.b32 %0, [%1+%2];" : "=r"(w[0]) : "r"(addr), "n"(OFF));
+  } else if constexpr (N == 2) {
     asm volatile("ld.shared.v2.b32 {%0,%1}, [%2+%3];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr), "n"(OFF));
   } else {
     static_for<N / 4>([&](auto j) {
@@ -142,69 +165,80 @@ __device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) {
 }
 
 // One warp's running state over its tokens and its work on one stage.
-template <bool BF, int D, int BS, int NT>
+template <bool BF, int D, int BS, int HC, int NT>
 struct Kv4Compute {
   static constexpr int NG = D / 32;        // channel groups
-  static constexpr int NH = 8 * NT;        // heads this warp produces
+  static constexpr int GS = 8 / HC;        // groups side by side in a tile's columns
+  static constexpr int NS = NG / GS;       // sets of such groups: group j * NS + i is set i, place j
+  static constexpr int NH = HC * NT;       // heads this warp produces
   static constexpr int TILE = kv4_tile_bytes(D, BS);
   static constexpr int PER = kKv4Tokens / BS;   // blocks per stage
+  static constexpr bool QREG = D * NT <= 128;   // query fragments in registers, else in shared memory
   static constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u;
   static constexpr float kShift = 9.f, kSlack = 5.f;
+  static_assert(NG % GS == 0 && (NT == 1 || HC == 8), "columns");
 
-  uint32_t qf[NG][NT][4];                  // B fragments: k16 step 0 (b0, b1), step 1 (b0, b1)
-  float qs[NG][NT][2];                     // 2^-24 sum of the group's q, heads 2c and 2c + 1
-  float sc[NT][2];                         // to log2 units, heads 2c and 2c + 1
+  // Columns 2c and 2c + 1 (c = lane % 4) are two heads of one group place.
+  uint32_t qf[QREG ? NG : 1][NT][4];       // B fragments: k16 step 0 (b0, b1), step 1 (b0, b1)
+  uint32_t qaddr;                          // or where this lane's lie
+  float qs[NS][NT][2];                     // 2^-24 sum of the group's q
+  float sc[NT][2];                         // to log2 units, not negative
   float o[2 * NG][NT][4];                  // codes^T P'
-  float oz[NG][NT][4];                     // (s, z)^T P': elements 2 and 3 are z's
+  float oz[NS][NT][4];                     // (s, z)^T P': elements 2 and 3 are z's
   float ref[NT][2], l[NT][2];              // running maximum less shift; sum
   float shift;                             // kShift - E
 
+  static __device__ __forceinline__ int place(int column) { return column / HC; }   // j of a column
+
   // The queries of the CTA's heads as B fragments, prepared once: warp w does
   // the channel groups w, w + 4, ... and every warp reads all of them back from
-  // `qsm`.  A head's row is scaled by the power of two that brings its largest
-  // element into [2^14, 2^15): exact in binary16 for either type, but for
-  // elements 2^-28 times the largest or less.
+  // `qsm`.  A negative softmax scale goes into the sign of q.
   __device__ __forceinline__ void load_q(const uint16_t* qg, int heads, float scale_log2, uint8_t* qsm,
                                          int warp, int lane) {
     constexpr int NW = kKv4Warps, PG = (NG + NW - 1) / NW;
     uint4* frag = reinterpret_cast<uint4*>(qsm);                       // [NG][NT][32]
     float* sums = reinterpret_cast<float*>(qsm + NG * NT * 512);       // [NG][NH]
-    float* scales = sums + NG * NH;                                    // [NH]
-    float* tops = scales + NH;                                         // [NW][NH]
+    float* tops = sums + NG * NH;                                      // [NG][NH]
+    float* scales = tops + NG * NH;                                    // [NH]
     const int c = lane & 3, n = lane >> 2;
     uint4 u[PG][NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float top = 0.f;
+      const int h = nt * 8 + n % HC;
 #pragma unroll
       for (int i = 0; i < PG; ++i) {
-        const int g = warp + i * NW, h = nt * 8 + n;
+        const int g = warp + i * NW;
+        if (g >= NG) break;
+        const bool mine = place(n) == g / NS;
         u[i][nt] = make_uint4(0, 0, 0, 0);
-        if (g < NG && h < heads)
-          u[i][nt] = __ldg(reinterpret_cast<const uint4*>(qg + h * D + g * 32 + c * 8));
+        if (mine && h < heads) u[i][nt] = __ldg(reinterpret_cast<const uint4*>(qg + h * D + g * 32 + c * 8));
         const uint32_t x[4] = {u[i][nt].x, u[i][nt].y, u[i][nt].z, u[i][nt].w};
+        float top = 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 f = unpack2<BF>(x[k]);
-          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+          top = max_nan(top, max_nan(fabsf(f.x), fabsf(f.y)));
         }
+        top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        if (mine && c == 0) tops[g * NH + h] = top;
       }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      if (c == 0) tops[warp * NH + nt * 8 + n] = top;
     }
     __syncthreads();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int h = nt * 8 + n;
+      const int h = nt * 8 + n % HC;
       float top = 0.f;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) top = fmaxf(top, tops[w * NH + h]);
-      int e = 14 + 127 - static_cast<int>(__float_as_uint(top) >> 23);   // infinity: a finite factor
+      for (int g = 0; g < NG; ++g) top = max_nan(top, tops[g * NH + h]);
+      int e = 14 + 127 - static_cast<int>(__float_as_uint(top) >> 23);
       e = top > 0.f ? min(e, 120) : 0;
-      const float f = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      if (warp == 0 && c == 0)
-        scales[h] = scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * 0x1p24f;
+      float f = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      if (warp == 0 && n < HC && c == 0)   // an infinite or NaN query gives NaN
+        scales[h] = top < INFINITY
+                        ? fabsf(scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * 0x1p24f
+                        : __uint_as_float(0x7fc00000u);
+      if (scale_log2 < 0.f) f = -f;
 #pragma unroll
       for (int i = 0; i < PG; ++i) {
         const int g = warp + i * NW;
@@ -222,22 +256,29 @@ struct Kv4Compute {
         float sum = ((s0.x + s0.y) + (s1.x + s1.y)) * 0x1p-24f + ((s2.x + s2.y) + (s3.x + s3.y)) * 0x1p-20f;
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        if (c == 0) sums[g * NH + h] = sum;
+        if (place(n) == g / NS && c == 0) sums[g * NH + h] = sum;
       }
     }
     __syncthreads();
+    const int h0 = 2 * c % HC, j = place(2 * c);
+    qaddr = smem_u32(frag + lane);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float2 x = *reinterpret_cast<const float2*>(scales + nt * 8 + 2 * c);
+      const float2 x = *reinterpret_cast<const float2*>(scales + nt * 8 + h0);
       sc[nt][0] = x.x;
       sc[nt][1] = x.y;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const uint4 v = frag[(g * NT + nt) * 32 + lane];
-        qf[g][nt][0] = v.x; qf[g][nt][1] = v.y; qf[g][nt][2] = v.z; qf[g][nt][3] = v.w;
-        const float2 y = *reinterpret_cast<const float2*>(sums + g * NH + nt * 8 + 2 * c);
-        qs[g][nt][0] = y.x;
-        qs[g][nt][1] = y.y;
+      for (int i = 0; i < NS; ++i) {
+        const float2 y = *reinterpret_cast<const float2*>(sums + (j * NS + i) * NH + nt * 8 + h0);
+        qs[i][nt][0] = y.x;
+        qs[i][nt][1] = y.y;
+      }
+      if constexpr (QREG) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const uint4 v = frag[(g * NT + nt) * 32 + lane];
+          qf[g][nt][0] = v.x; qf[g][nt][1] = v.y; qf[g][nt][2] = v.z; qf[g][nt][3] = v.w;
+        }
       }
     }
   }
@@ -253,7 +294,7 @@ struct Kv4Compute {
 #pragma unroll
         for (int i = 0; i < 2 * NG; ++i) o[i][nt][e] = 0.f;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) oz[g][nt][e] = 0.f;
+        for (int i = 0; i < NS; ++i) oz[i][nt][e] = 0.f;
       }
     }
   }
@@ -268,7 +309,7 @@ struct Kv4Compute {
 #pragma unroll
         for (int i = 0; i < 2 * NG; ++i) o[i][nt][e] *= by[nt][e & 1];
 #pragma unroll
-        for (int g = 0; g < NG; ++g) oz[g][nt][e] *= by[nt][e & 1];
+        for (int i = 0; i < NS; ++i) oz[i][nt][e] *= by[nt][e & 1];
       }
     }
   }
@@ -309,50 +350,61 @@ struct Kv4Compute {
     uint32_t at[NG / 2];
 #pragma unroll
     for (int i = 0; i < NG / 2; ++i) at[i] = kt + lrow[i];
-    const uint32_t kpar = kt + (lane >> 2) * NG * 4, vpar = kt + (lane & 3) * NG * 8;
+    // the lane's parameters: keys of tokens lane / 4 and 8 on for the group
+    // place of its columns 2c, 2c + 1; values of tokens 2c, 2c + 1 and 8 on for
+    // that of column lane / 4
+    const uint32_t kpar = kt + ((lane >> 2) * NG + place(2 * (lane & 3)) * NS) * 4;
+    const uint32_t vpar = kt + ((lane & 3) * NG + place(lane >> 2) * NS) * 8;
 
     float s[2][NT][4];
     static_for<2>([&](auto mt) {
       constexpr int KB = block_of(mt) + row_of(mt) * (D / 2);
       constexpr int KP = block_of(mt) + PAR + row_of(mt) * NG * 4;
-      uint32_t plo[NG], phi[NG];
+      uint32_t plo[NS], phi[NS];
       lds_words<KP>(kpar, plo);
       lds_words<KP + 8 * NG * 4>(kpar, phi);
-      static_for<NG / 2>([&](auto gp) {
-        uint32_t r[4];
-        ldm_x4<KB, false>(at[gp], r);
+      uint32_t r[NG / 2][4];
+      static_for<NG / 2>([&](auto gp) { ldm_x4<KB, false>(at[gp], r[gp]); });
+      static_for<NS>([&](auto i) {
+        const float2 lo = unpack2<false>(plo[i]), up = unpack2<false>(phi[i]);
 #pragma unroll
-        for (int gg = 0; gg < 2; ++gg) {
-          const int g = 2 * gp + gg;
-          const uint32_t a = r[2 * gg], b = r[2 * gg + 1], a8 = a >> 8, b8 = b >> 8;
-          const float2 lo = unpack2<false>(plo[g]), up = unpack2<false>(phi[g]);
+        for (int nt = 0; nt < NT; ++nt) {
+          float acc[4] = {lo.y * qs[i][nt][0], lo.y * qs[i][nt][1], up.y * qs[i][nt][0],
+                          up.y * qs[i][nt][1]};
+          static_for<GS>([&](auto j) {
+            constexpr int g = j * NS + i;
+            const uint32_t a = r[g / 2][2 * (g & 1)], b = r[g / 2][2 * (g & 1) + 1];
+            const uint32_t a8 = a >> 8, b8 = b >> 8;
+            uint32_t q[4];
+            if constexpr (QREG) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float acc[4] = {lo.y * qs[g][nt][0], lo.y * qs[g][nt][1], up.y * qs[g][nt][0],
-                            up.y * qs[g][nt][1]};
-            mma_codes(acc, a & M0, b & M0, a8 & M0, b8 & M0, qf[g][nt][0], qf[g][nt][1]);
-            mma_codes(acc, a & M1, b & M1, a8 & M1, b8 & M1, qf[g][nt][2], qf[g][nt][3]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float by = e < 2 ? lo.x : up.x;
-              s[mt][nt][e] = g == 0 ? by * acc[e] : fmaf(by, acc[e], s[mt][nt][e]);
+              for (int k = 0; k < 4; ++k) q[k] = qf[g][nt][k];
+            } else {
+              lds_words<g * NT * 512>(qaddr + nt * 512, q);
             }
+            mma_codes(acc, a & M0, b & M0, a8 & M0, b8 & M0, q[0], q[1]);
+            mma_codes(acc, a & M1, b & M1, a8 & M1, b8 & M1, q[2], q[3]);
+          });
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float by = e < 2 ? lo.x : up.x;
+            s[mt][nt][e] = i == 0 ? by * acc[e] : fmaf(by, acc[e], s[mt][nt][e]);
           }
         }
       });
+      // the group places of a head lie in lanes 4 / GS apart
+#pragma unroll
+      for (int m = 4 / GS; m < 4; m <<= 1)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[mt][nt][e] += __shfl_xor_sync(0xffffffffu, s[mt][nt][e], m);
     });
 
-    // running maximum and sum
+    // running maximum and sum; s stays in its own units (sc is not negative)
     float alpha[NT][2];
     bool grew = false;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[mt][nt][e] *= sc[nt][e & 1];
-    }
-    if (ragged) {   // minus infinity past the end
+    if (ragged) {   // out of the maximum past the end
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -368,7 +420,8 @@ struct Kv4Compute {
         float v = fmaxf(fmaxf(s[0][nt][j], s[0][nt][2 + j]), fmaxf(s[1][nt][j], s[1][nt][2 + j]));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16)) - shift;
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+        v = fmaf(v, sc[nt][j], -shift);
         const bool up = v > ref[nt][j] + kSlack;
         alpha[nt][j] = up ? fast_exp2(ref[nt][j] - v) : 1.f;
         ref[nt][j] = up ? v : ref[nt][j];
@@ -381,32 +434,44 @@ struct Kv4Compute {
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float p = fast_exp2(s[mt][nt][e] - ref[nt][e & 1]);
-          s[mt][nt][e] = p;
-          l[nt][e & 1] += p;
-        }
+        for (int e = 0; e < 4; ++e)
+          s[mt][nt][e] = fast_exp2(fmaf(s[mt][nt][e], sc[nt][e & 1], -ref[nt][e & 1]));
+    if (ragged) {   // (a scale of zero times minus infinity is no number)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (mt * 16 + (e >> 1) * 8 + (lane >> 2) >= valid) s[mt][nt][e] = 0.f;
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) l[nt][e & 1] += s[mt][nt][e];
 
     static_for<2>([&](auto mt) {
       constexpr int VB = VT + block_of(mt) + row_of(mt) * (D / 2);
       constexpr int VP = VT + block_of(mt) + PAR + row_of(mt) / 2 * NG * 8;
-      // (s, s), (z, z) of tokens 2c, 2c + 1, then of 8 + 2c, 9 + 2c, per group
-      uint32_t w[NG][4];
+      // (s, s), (z, z) of tokens 2c, 2c + 1, then of 8 + 2c, 9 + 2c, per set
+      uint32_t w[NS][4];
       uint32_t large = 0;
-      static_for<NG>([&](auto g) {
-        lds_pair<VP + g * 8>(vpar, w[g][0], w[g][1]);
-        lds_pair<VP + (4 * NG + g) * 8>(vpar, w[g][2], w[g][3]);
-        large |= w[g][0] | w[g][2];
+      static_for<NS>([&](auto i) {
+        lds_pair<VP + i * 8>(vpar, w[i][0], w[i][1]);
+        lds_pair<VP + (4 * NG + i) * 8>(vpar, w[i][2], w[i][3]);
+        large |= w[i][0] | w[i][2];
       });
       if (__any_sync(0xffffffffu, (large & 0x40004000u) != 0)) {   // rare
         float top = 0.f;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          const float2 x = unpack2<false>(w[g][0]), y = unpack2<false>(w[g][2]);
+        for (int i = 0; i < NS; ++i) {
+          const float2 x = unpack2<false>(w[i][0]), y = unpack2<false>(w[i][2]);
           top = fmaxf(fmaxf(top, fmaxf(x.x, x.y)), fmaxf(y.x, y.y));
         }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
         const float now = lowered(top, shift);
         if (now < shift) {
           const float down = fast_exp2(now - shift);
@@ -427,13 +492,22 @@ struct Kv4Compute {
           shift = now;
         }
       }
-      // P^T as B operands: tokens 2c, 2c + 1 (b0) and 8 on (b1) of head lane / 4
+      // P^T as B operands: tokens 2c, 2c + 1 (b0) and 8 on (b1) of column lane / 4
       uint32_t b0[NT], b1[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         b0[nt] = movmatrix_trans(pack2<false>(s[mt][nt][0], s[mt][nt][1]));
         b1[nt] = movmatrix_trans(pack2<false>(s[mt][nt][2], s[mt][nt][3]));
       }
+      uint32_t p0[NS][NT], p1[NS][NT];
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          p0[i][nt] = hmul2_bits(b0[nt], w[i][0]);
+          p1[i][nt] = hmul2_bits(b1[nt], w[i][2]);
+          mma_codes(oz[i][nt], w[i][0], w[i][1], w[i][2], w[i][3], p0[i][nt], p1[i][nt]);
+        }
       static_for<NG / 2>([&](auto gp) {
         uint32_t r[4];
         ldm_x4<VB, true>(at[gp], r);
@@ -443,10 +517,9 @@ struct Kv4Compute {
           const uint32_t a = r[2 * gg], b = r[2 * gg + 1], a8 = a >> 8, b8 = b >> 8;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t p0 = hmul2_bits(b0[nt], w[g][0]), p1 = hmul2_bits(b1[nt], w[g][2]);
-            mma_codes(o[2 * g][nt], a & M0, a & M1, b & M0, b & M1, p0, p1);
-            mma_codes(o[2 * g + 1][nt], a8 & M0, a8 & M1, b8 & M0, b8 & M1, p0, p1);
-            mma_codes(oz[g][nt], w[g][0], w[g][1], w[g][2], w[g][3], p0, p1);
+            mma_codes(o[2 * g][nt], a & M0, a & M1, b & M0, b & M1, p0[g % NS][nt], p1[g % NS][nt]);
+            mma_codes(o[2 * g + 1][nt], a8 & M0, a8 & M1, b8 & M0, b8 & M1, p0[g % NS][nt],
+                      p1[g % NS][nt]);
           }
         }
       });
@@ -454,36 +527,47 @@ struct Kv4Compute {
   }
 
   // Leave each head's (m, l, o) for the CTA merge.  Rows lane / 4 of tile
-  // (g, a) are channels 32 g + 4 (lane / 4) + 2 a, rows 8 on the next channel.
+  // (g, a) are channels 32 g + 4 (lane / 4) + 2 a, rows 8 on the next channel;
+  // columns 2c, 2c + 1 hold group g only where it has their place.
   __device__ __forceinline__ void publish(float* cm, float* cl, float* co, int lane) {
+    const int c = lane & 3, j = place(2 * c), h0 = 2 * c % HC;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float lt = l[nt][j];
+      for (int k = 0; k < 2; ++k) {
+        float lt = l[nt][k];
         lt += __shfl_xor_sync(0xffffffffu, lt, 4);
         lt += __shfl_xor_sync(0xffffffffu, lt, 8);
         lt += __shfl_xor_sync(0xffffffffu, lt, 16);
-        const int h = nt * 8 + 2 * (lane & 3) + j;
-        if (lane < 4) {
-          cm[h] = ref[nt][j];
+        const int h = nt * 8 + h0 + k;
+        if (lane < HC / 2) {
+          cm[h] = ref[nt][k];
           cl[h] = lt;
         }
 #pragma unroll
-        for (int i = 0; i < 2 * NG; ++i) {
-          const int d = 32 * (i >> 1) + 4 * (lane >> 2) + 2 * (i & 1);
-          const float z = oz[i >> 1][nt][2 + j];
-          *reinterpret_cast<float2*>(co + h * kv4_row(D) + d) =
-              make_float2(fmaf(o[i][nt][j], 0x1p24f, z), fmaf(o[i][nt][2 + j], 0x1p20f, z));
+        for (int i = 0; i < NS; ++i) {
+          // the zero-point sum of this place's group lies in its own rows
+          const float z = __shfl_sync(0xffffffffu, oz[i][nt][2 + k], j * HC * 4 + c);
+#pragma unroll
+          for (int x = 0; x < GS; ++x) {
+            if (x != j) continue;
+            const int g = x * NS + i;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int d = 32 * g + 4 * (lane >> 2) + 2 * t;
+              *reinterpret_cast<float2*>(co + h * kv4_row(D) + d) =
+                  make_float2(fmaf(o[2 * g + t][nt][k], 0x1p24f, z), fmaf(o[2 * g + t][nt][2 + k], 0x1p20f, z));
+            }
+          }
         }
       }
     }
   }
 };
 
-template <bool BF, int D, int BS, int NT>
-__global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas(D, NT)) kv4_decode_kernel(const __grid_constant__ Kv4Args p) {
-  using Compute = Kv4Compute<BF, D, BS, NT>;
+template <bool BF, int D, int BS, int HC, int NT>
+__global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas(D, HC, NT)) kv4_decode_kernel(const __grid_constant__ Kv4Args p) {
+  using Compute = Kv4Compute<BF, D, BS, HC, NT>;
   constexpr int NW = kKv4Warps, NS = kv4_stages(D), NH = Compute::NH;
   constexpr int TILE = Compute::TILE, PER = Compute::PER, STAGE = kv4_stage_bytes(D);
   static_assert(STAGE == 2 * PER * TILE, "stage");
@@ -632,7 +716,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas(D, NT)) kv4_decode_ke
 }
 
 // Launch for one element type (pkv_kv4_inst.cu, compiled once per type).
-cudaError_t launch_kv4_f16(const Kv4Args&, int head_dim, int block_size, int nt, unsigned grid, cudaStream_t);
-cudaError_t launch_kv4_bf16(const Kv4Args&, int head_dim, int block_size, int nt, unsigned grid, cudaStream_t);
+cudaError_t launch_kv4_f16(const Kv4Args&, int head_dim, int block_size, unsigned grid, cudaStream_t);
+cudaError_t launch_kv4_bf16(const Kv4Args&, int head_dim, int block_size, unsigned grid, cudaStream_t);
 
 }  // namespace pkv

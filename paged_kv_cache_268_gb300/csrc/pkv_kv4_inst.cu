@@ -13,10 +13,10 @@ namespace {
 
 constexpr bool kBF = PKV_INST_BF16 != 0;
 
-template <int D, int BS, int NT>
+template <int D, int BS, int HC, int NT>
 cudaError_t launch_one(const Kv4Args& a, unsigned grid, cudaStream_t stream) {
   constexpr int SMEM = kv4_smem(D, NT);
-  auto kern = kv4_decode_kernel<kBF, D, BS, NT>;
+  auto kern = kv4_decode_kernel<kBF, D, BS, HC, NT>;
   // the shared-memory limit is raised once per device (threads that race here
   // set the same attribute)
   static std::atomic<unsigned> mask{0};
@@ -32,13 +32,21 @@ cudaError_t launch_one(const Kv4Args& a, unsigned grid, cudaStream_t stream) {
   return launch_pdl(kern, dim3(grid), kKv4Warps * 32, SMEM, stream, a);
 }
 
-template <int D>
-cudaError_t launch_bs(const Kv4Args& a, int bs, int nt, unsigned grid, cudaStream_t stream) {
+template <int D, int BS>
+cudaError_t launch_heads(const Kv4Args& a, unsigned grid, cudaStream_t stream) {
   if constexpr (D <= 128) {
-    if (nt == 2)
-      return bs == 16 ? launch_one<D, 16, 2>(a, grid, stream) : launch_one<D, 32, 2>(a, grid, stream);
+    if (kv4_tiles(D, a.d.G) == 2) return launch_one<D, BS, 8, 2>(a, grid, stream);
   }
-  return bs == 16 ? launch_one<D, 16, 1>(a, grid, stream) : launch_one<D, 32, 1>(a, grid, stream);
+  if constexpr (D > 64) {
+    if (kv4_columns(D, a.d.G) == 2) return launch_one<D, BS, 2, 1>(a, grid, stream);
+  }
+  return kv4_columns(D, a.d.G) == 4 ? launch_one<D, BS, 4, 1>(a, grid, stream)
+                                    : launch_one<D, BS, 8, 1>(a, grid, stream);
+}
+
+template <int D>
+cudaError_t launch_bs(const Kv4Args& a, int bs, unsigned grid, cudaStream_t stream) {
+  return bs == 16 ? launch_heads<D, 16>(a, grid, stream) : launch_heads<D, 32>(a, grid, stream);
 }
 
 }  // namespace
@@ -49,12 +57,12 @@ cudaError_t launch_bs(const Kv4Args& a, int bs, int nt, unsigned grid, cudaStrea
 #define PKV_LAUNCH_NAME launch_kv4_f16
 #endif
 
-cudaError_t PKV_LAUNCH_NAME(const Kv4Args& a, int head_dim, int block_size, int nt, unsigned grid,
+cudaError_t PKV_LAUNCH_NAME(const Kv4Args& a, int head_dim, int block_size, unsigned grid,
                             cudaStream_t stream) {
   switch (head_dim) {
-    case 64: return launch_bs<64>(a, block_size, nt, grid, stream);
-    case 128: return launch_bs<128>(a, block_size, nt, grid, stream);
-    case 256: return launch_bs<256>(a, block_size, nt, grid, stream);
+    case 64: return launch_bs<64>(a, block_size, grid, stream);
+    case 128: return launch_bs<128>(a, block_size, grid, stream);
+    case 256: return launch_bs<256>(a, block_size, grid, stream);
     default: return cudaErrorInvalidValue;
   }
 }

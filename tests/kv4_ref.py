@@ -108,8 +108,8 @@ def attention(q: np.ndarray, k_cache: np.ndarray, v_cache: np.ndarray, tables: n
               lens: np.ndarray, scale: float):
     """softmax(scale q . k) . v in 64 bits over the 4-bit caches; also what the
     error bound needs: per out element the weighted magnitude sum w |v| and the
-    error of weights held in binary16's subnormals (see attention_bound), per
-    row the largest scale * sum |q| |k|-terms."""
+    error of weights held in binary16's subnormals, per row the error of a logit
+    (see attention_bound)."""
     B, Hq, D = q.shape
     Hkv, bs = k_cache.shape[1:3]
     G = Hq // Hkv
@@ -131,7 +131,11 @@ def attention(q: np.ndarray, k_cache: np.ndarray, v_cache: np.ndarray, tables: n
             out[i, h], mag[i, h] = w @ v[:, g], w @ np.abs(v[:, g])
             E = max(0.0, np.floor(np.log2(top[g])))
             low[i, h] = w.max() * 2.0 ** (E - 34) * np.abs(v[:, g]).sum(0)
-            smag[i, h] = abs(scale) * (par[:, g] @ np.abs(qh)).max()
+            # in units of the largest step count: D / 8 + 8 FP32 roundings of the
+            # largest partial sum, and what q loses in binary16's subnormals
+            steps, rest = (D / 8 + 8) * 2.0 ** -24, 2.0 ** -35 * np.abs(qh).max()
+            smag[i, h] = abs(scale) * (steps * (par[:, g] @ np.abs(qh)).max()
+                                       + rest * np.abs(k[:, g]).sum(-1).max())
     return out, mag, low, smag
 
 
@@ -151,7 +155,7 @@ def _magnitudes(k_cache, slots):
     return (par[..., 0] * (15 + np.abs(par[..., 1])))[..., None].repeat(32, -1).reshape(*par.shape[:2], -1)
 
 
-def attention_bound(out, mag, low, smag, eps: float, D: int) -> np.ndarray:
+def attention_bound(out, mag, low, smag, eps: float) -> np.ndarray:
     """How far a correct result may be off, element by element:
      - the store: half a step, eps / 2 of the value (and half the smallest
        subnormal binary16, 2^-25);
@@ -162,9 +166,11 @@ def attention_bound(out, mag, low, smag, eps: float, D: int) -> np.ndarray:
        its smallest step, 2^-25, where the largest weight is at least 2^(9-E)
        (E: the exponent of the largest value scale, at least 0): 2^(E-34) of
        the largest weight for each token, times its |v|;
-     - each logit: FP32 products and sums of at most D / 8 + 8 steps, of
-       magnitude smag (in the exponent, so it counts relative to the weight),
-       once in the weight and once in the normaliser."""
-    logits = 2 * (D / 8 + 8) * 2.0 ** -24 * smag[..., None]
+     - each logit: FP32 products and sums of at most D / 8 + 8 steps, 2^-24 of
+       the largest partial sum each, and the queries' rounding (half of
+       binary16's smallest step, 2^-25, times 16, for a row of at least 2^14:
+       2^-35 of the row's largest element) (smag; in the exponent, so it counts relative to
+       the weight), once in the weight and once in the normaliser."""
+    logits = 2 * smag[..., None]
     weights = 2 * 2.0 ** -11 + 2.0 ** -22 + 2.0 ** -14
     return eps / 2 * np.abs(out) + 2.0 ** -25 + (weights + logits) * mag + low

@@ -158,7 +158,7 @@ def check(pkv, b, d=None, **kw):
     got = R.to_np(out).astype(np.float64)
     assert np.all(np.isfinite(got))
     err = np.abs(got - want)
-    bound = R.attention_bound(want, mag, low, smag, EPS[b["q"].dtype], b["q"].shape[2])
+    bound = R.attention_bound(want, mag, low, smag, EPS[b["q"].dtype])
     assert np.all(err <= bound), f"{(err > bound).sum()} out of tolerance, worst {(err / bound).max():.2f} of it"
     return out
 
