@@ -421,11 +421,30 @@ def _kv4_dims(k_cache: torch.Tensor, v_cache: torch.Tensor) -> tuple[int, int, i
 @functools.lru_cache(maxsize=256)
 def _sized(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
            max_blocks_per_seq, max_context_len, dtype, split_tokens=0) -> Shape:
-    """A Shape, made once for the same sizes.  Read only."""
-    return make_shape(num_seqs=num_seqs, num_q_heads=num_q_heads, num_kv_heads=num_kv_heads,
-                      head_dim=head_dim, block_size=block_size, num_blocks=num_blocks,
-                      max_blocks_per_seq=max_blocks_per_seq, max_context_len=max_context_len,
-                      dtype=dtype, split_tokens=split_tokens)
+    """A Shape, made once for the same sizes.  Read only.  It carries a reference
+    to itself for calls and, per device, the 4-bit decode's workspace size."""
+    shape = make_shape(num_seqs=num_seqs, num_q_heads=num_q_heads, num_kv_heads=num_kv_heads,
+                       head_dim=head_dim, block_size=block_size, num_blocks=num_blocks,
+                       max_blocks_per_seq=max_blocks_per_seq, max_context_len=max_context_len,
+                       dtype=dtype, split_tokens=split_tokens)
+    shape.ref, shape.kv4_workspace = ctypes.byref(shape), {}
+    return shape
+
+
+@functools.lru_cache(maxsize=256)
+def _rope(*fields):
+    """A reference to the Rope of these fields, made once."""
+    return ctypes.byref(Rope(*fields))
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _launch_stream(stream, dev: torch.device) -> int:
+    """_stream_ptr, without making a Stream object where none is given."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev.index)
+    return _stream_ptr(stream, dev)
 
 
 def _on(dev: torch.device):
@@ -459,10 +478,35 @@ def _token_stride(t: torch.Tensor, name: str, heads: int, D: int, T: int, dtype)
     return t.stride(0) if T > 1 else 0
 
 
-def _append(fn: str, dims, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out,
-            interleaved, stream, dtype):
+def _append_plain(dims, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, dtype):
+    """Whether a call is the usual one (everything dense, on one GPU, as the
+    caches say): _check_append would find nothing.  A decode step makes this
+    call for every layer, so it looks at each tensor once."""
+    _, Hkv, _, D = dims
+    dev = k_cache.get_device()
+    if q is None or cos_sin is None or positions is None or dev < 0 or dtype not in _DT:
+        return False
+    ks, qs, cs = k.shape, q.shape, cos_sin.shape
+    if len(ks) != 3 or len(qs) != 3 or len(cs) != 2:
+        return False
+    T = ks[0]
+    return (ks[1] == Hkv and ks[2] == D and v.shape == ks and qs[0] == T and qs[2] == D and qs[1] > 0
+            and slot_mapping.shape == (T,) and positions.shape == (T,)
+            and q.dtype is dtype and k.dtype is dtype and v.dtype is dtype
+            and slot_mapping.dtype is torch.int32 and positions.dtype is torch.int32
+            and cos_sin.dtype is torch.float32
+            and q.get_device() == dev and k.get_device() == dev and v.get_device() == dev
+            and v_cache.get_device() == dev and slot_mapping.get_device() == dev
+            and positions.get_device() == dev and cos_sin.get_device() == dev
+            and q.is_contiguous() and k.is_contiguous() and v.is_contiguous()
+            and slot_mapping.is_contiguous() and positions.is_contiguous()
+            and cos_sin.is_contiguous())
+
+
+def _check_append(dims, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out, dtype):
+    """Refuse what does not fit together; the token strides of q, k and v."""
     NB, Hkv, bs, D = dims
-    code = _dtype_code(dtype)
+    _dtype_code(dtype)
     if k.dim() != 3:
         raise ValueError("k must be [T, Hkv, D]")
     T = k.shape[0]
@@ -471,12 +515,11 @@ def _append(fn: str, dims, q, k, v, positions, cos_sin, slot_mapping, k_cache, v
     _dense(slot_mapping, "slot_mapping", torch.int32)
     if slot_mapping.shape != (T,):
         raise ValueError("slot_mapping must be [T]")
-    Hq = qs = rot = rows = 0
+    qs = 0
     if q is not None:
         if q.dim() != 3:
             raise ValueError("q must be [T, Hq, D]")
-        Hq = q.shape[1]
-        qs = _token_stride(q, "q", Hq, D, T, dtype)
+        qs = _token_stride(q, "q", q.shape[1], D, T, dtype)
         if q_out is not None:
             _dense(q_out, "q_out", dtype)
             if q_out.shape != q.shape:
@@ -490,20 +533,35 @@ def _append(fn: str, dims, q, k, v, positions, cos_sin, slot_mapping, k_cache, v
         _dense(cos_sin, "cos_sin", torch.float32)
         if positions.shape != (T,) or cos_sin.dim() != 2:
             raise ValueError("positions must be [T], cos_sin [max_position, rot_dim]")
-        rows, rot = cos_sin.shape
-    dev = _one_device(q=q, k=k, v=v, positions=positions, cos_sin=cos_sin,
-                      slot_mapping=slot_mapping, k_cache=k_cache, v_cache=v_cache, q_out=q_out)
-    ptr = _stream_ptr(stream, dev)
-    shape = _sized(0, max(Hq, 1), Hkv, D, bs, NB, 1, 1, code)
-    rope = Rope(rot, 1 if interleaved else 0, rows, qs, ks, vs)
-    if q is not None and q_out is None:
-        with _allocating_on(stream):
-            q_out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
+    _one_device(q=q, k=k, v=v, positions=positions, cos_sin=cos_sin, slot_mapping=slot_mapping,
+                k_cache=k_cache, v_cache=v_cache, q_out=q_out)
+    return qs, ks, vs
+
+
+def _append(fn: str, dims, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out,
+            interleaved, stream, dtype):
+    NB, Hkv, bs, D = dims
+    qs = ks = vs = 0
+    if q_out is not None or not _append_plain(dims, q, k, v, positions, cos_sin, slot_mapping,
+                                              k_cache, v_cache, dtype):
+        qs, ks, vs = _check_append(dims, q, k, v, positions, cos_sin, slot_mapping, k_cache,
+                                   v_cache, q_out, dtype)
+    T, dev = k.shape[0], k_cache.device
+    Hq = 0 if q is None else q.shape[1]
+    rows, rot = (0, 0) if cos_sin is None else cos_sin.shape
+    ptr = _launch_stream(stream, dev)
+    shape = _sized(0, max(Hq, 1), Hkv, D, bs, NB, 1, 1, _DT[dtype])
+    rope = _rope(rot, 1 if interleaved else 0, rows, qs, ks, vs)
     with _on(dev):
-        _check(fn, getattr(load_library(), fn)(
-            ctypes.byref(shape), ctypes.byref(rope), _ptr(q) if Hq else None, _ptr(k), _ptr(v),
-            _ptr(positions), _ptr(cos_sin), _ptr(slot_mapping), T, _ptr(q_out) if Hq else None,
-            _ptr(k_cache), _ptr(v_cache), ptr))
+        if q is not None and q_out is None:
+            with _allocating_on(stream):
+                q_out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
+        rc = getattr(load_library(), fn)(
+            shape.ref, rope, q.data_ptr() if Hq else None, k.data_ptr(), v.data_ptr(),
+            positions.data_ptr() if rot else None, cos_sin.data_ptr() if rot else None,
+            slot_mapping.data_ptr(), T, q_out.data_ptr() if Hq else None, k_cache.data_ptr(),
+            v_cache.data_ptr(), ptr)
+    _check(fn, rc)
     return q_out
 
 
@@ -526,7 +584,7 @@ def rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
     dims = _cache_shape(k_cache)
     _dense(k_cache, "k_cache")
     _dense(v_cache, "v_cache", k_cache.dtype)
-    if v_cache.shape != k_cache.shape:
+    if v_cache.shape != dims:
         raise ValueError("caches must have one shape")
     return _append("pkv_rope_append", dims, q, k, v, positions, cos_sin, slot_mapping, k_cache,
                    v_cache, q_out, interleaved, stream, k_cache.dtype)
@@ -560,24 +618,27 @@ def kv4_gather(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch
             if t.shape != (T, Hkv, D):
                 raise ValueError(f"{n} must be [T, Hkv, D]")
     dev = _one_device(k_cache=k_cache, v_cache=v_cache, slot_mapping=slot_mapping, k=k, v=v)
-    ptr = _stream_ptr(stream, dev)
-    with _allocating_on(stream):
-        k = torch.empty((T, Hkv, D), dtype=dtype, device=dev) if k is None else k
-        v = torch.empty((T, Hkv, D), dtype=dtype, device=dev) if v is None else v
+    ptr = _launch_stream(stream, dev)
     shape = _sized(0, 1, Hkv, D, bs, NB, 1, 1, code)
     with _on(dev):
-        _check("pkv_kv4_gather",
-               load_library().pkv_kv4_gather(ctypes.byref(shape), _ptr(k_cache), _ptr(v_cache),
-                                             _ptr(slot_mapping), T, _ptr(k), _ptr(v), ptr))
+        with _allocating_on(stream):
+            k = torch.empty((T, Hkv, D), dtype=dtype, device=dev) if k is None else k
+            v = torch.empty((T, Hkv, D), dtype=dtype, device=dev) if v is None else v
+        rc = load_library().pkv_kv4_gather(shape.ref, k_cache.data_ptr(), v_cache.data_ptr(),
+                                           slot_mapping.data_ptr(), T, k.data_ptr(), v.data_ptr(), ptr)
+    _check("pkv_kv4_gather", rc)
     return k, v
 
 
 def kv4_decode_shape(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tensor,
                      max_context_len: int | None = None, split_tokens: int = 0) -> Shape:
     """decode_shape for a 4-bit cache."""
-    NB, Hkv, bs, W = k_cache.shape
-    MB = block_tables.shape[1]
-    return _sized(q.shape[0], q.shape[1], Hkv, W * 8 // 5, bs, NB, MB,
+    return Shape.from_buffer_copy(_kv4_sized(q, k_cache, block_tables, max_context_len, split_tokens))
+
+
+def _kv4_sized(q, k_cache, block_tables, max_context_len, split_tokens) -> Shape:
+    (B, Hq, _), (NB, Hkv, bs, W), (_, MB) = q.shape, k_cache.shape, block_tables.shape
+    return _sized(B, Hq, Hkv, W * 8 // 5, bs, NB, MB,
                   MB * bs if max_context_len is None else int(max_context_len),
                   _dtype_code(q.dtype), int(split_tokens))
 
@@ -628,20 +689,23 @@ def kv4_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         _dense(workspace, "workspace")
     dev = _one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
                       context_lens=context_lens, out=out, workspace=workspace)
-    ptr = _stream_ptr(stream, dev)
-    shape = kv4_decode_shape(q, k_cache, block_tables, max_context_len, split_tokens)
-    with _on(dev), _allocating_on(stream):
-        if workspace is None and dev.index not in _SET_WS:
-            n = kv4_workspace_bytes(shape)
-            if n:
-                workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-        if out is None:
-            out = torch.empty_like(q)
-        _check("pkv_kv4_attn_decode",
-               load_library().pkv_kv4_attn_decode(
-                   ctypes.byref(shape), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-                   _ptr(context_lens), float(scale), _ptr(out), _ptr(workspace),
-                   _nbytes(workspace), ptr))
+    ptr = _launch_stream(stream, dev)
+    shape = _kv4_sized(q, k_cache, block_tables, max_context_len, split_tokens)
+    with _on(dev):
+        with _allocating_on(stream):
+            if workspace is None and dev.index not in _SET_WS:
+                n = shape.kv4_workspace.get(dev.index)
+                if n is None:
+                    n = shape.kv4_workspace[dev.index] = kv4_workspace_bytes(shape)
+                if n:
+                    workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+            if out is None:
+                out = torch.empty_like(q)
+        rc = load_library().pkv_kv4_attn_decode(
+            shape.ref, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_tables.data_ptr(), context_lens.data_ptr(), float(scale), out.data_ptr(),
+            _ptr(workspace), _nbytes(workspace), ptr)
+    _check("pkv_kv4_attn_decode", rc)
     return out
 
 

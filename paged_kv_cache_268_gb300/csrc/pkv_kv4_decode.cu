@@ -30,12 +30,28 @@ int kv4_plan(const pkv_shape* s, int sms, pkv_plan* plan) {
   if (s->split_tokens > 0) {
     P = (static_cast<long long>(s->split_tokens) + bs - 1) / bs * bs;
   } else {
-    P = 2048;
-    const long long slots = static_cast<long long>(sms) * kv4_ctas(D, kv4_columns(D, G), kv4_tiles(D, G));
-    if (units > 0 && units * ((maxL + P - 1) / P) < 4 * slots) {
-      const long long S = slots / units > 0 ? slots / units : 1;
+    // Tokens per resident CTA if every sequence were of the largest length.
+    // Measured on one GB300 over batches of 1 to 128 sequences (uniform and
+    // log-normal lengths, 8 and 32 kv heads, head_dim 64 to 256):
+    //  - from 6000 on, 2048-token partitions (64 x 512-4096 tokens, 32 heads:
+    //    123 us, 126 at 1024), from 1000 on, 1024 (64 x 1-4096, 8 heads: 40 us,
+    //    43 at 2048 or 512), below, half of it;
+    //  - up to four sequences, whose lengths are mostly near the largest: one
+    //    wave of equal partitions (4 x 32768 tokens: 36 us, 42-45 at 768-2048);
+    //  - at least 256 tokens, 128 where a sequence has at most 2048, since
+    //    start-up and merge cost a CTA as much as about that many (1 x 8192: 8.1
+    //    us at 256, 10.4 at 128; 1 x 500: 5.2 us at 128, 6.2 at 256); no split of
+    //    up to 256 tokens (4.2 us, 4.5 in two).
+    const long long slots =
+        static_cast<long long>(sms) * kv4_ctas(D, kv4_columns(D, G), kv4_tiles(D, G));
+    const long long per_slot = units * maxL / slots;
+    P = per_slot >= 6000 ? 2048 : (per_slot >= 1000 ? 1024 : per_slot / 2);
+    if (s->num_seqs <= 4 && units > 0 && units < slots) {
+      const long long S = slots / units;
       P = (maxL + S - 1) / S;
     }
+    const long long least = maxL <= 256 ? 256 : (maxL <= 2048 ? 128 : 256);
+    if (P < least) P = least;
     P = (P + gran - 1) / gran * gran;
     // at most 1024 partitions per sequence
     const long long pmin = (static_cast<long long>(maxL) + 1023) / 1024;

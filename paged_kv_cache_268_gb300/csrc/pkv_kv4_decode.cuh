@@ -299,21 +299,6 @@ struct Kv4Compute {
     }
   }
 
-  __device__ __forceinline__ void rescale(const float (&by)[NT][2]) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) l[nt][j] *= by[nt][j];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-#pragma unroll
-        for (int i = 0; i < 2 * NG; ++i) o[i][nt][e] *= by[nt][e & 1];
-#pragma unroll
-        for (int i = 0; i < NS; ++i) oz[i][nt][e] *= by[nt][e & 1];
-      }
-    }
-  }
-
   // Offset of the 16-token half `mt` in a stage's K or V: its block, and its row there.
   static __host__ __device__ constexpr int block_of(int mt) { return PER == 2 ? mt * TILE : 0; }
   static __host__ __device__ constexpr int row_of(int mt) { return PER == 2 ? 0 : mt * 16; }
@@ -336,17 +321,68 @@ struct Kv4Compute {
     __syncwarp();
   }
 
-  // The shift with which weights times a value scale of `top` stay in binary16.
-  static __device__ __forceinline__ float lowered(float top, float shift) {
-    const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;   // top < 2^(e + 1)
-    return fminf(shift, kShift - static_cast<float>(min(max(e, 0), 17)));
+  // The running maximum is more than the slack behind `top`, or a value scale
+  // of 2 or more is in the stage: set the reference (and the shift, so that
+  // weights times the largest scale stay in binary16) and rescale the sums.
+  __device__ __forceinline__ void catch_up(const float (&top)[NT][2], uint32_t kt, int lane) {
+    float most = 0.f;
+    for (int i = lane; i < 16 * NG; i += 32) {
+      const int half = i / (8 * NG), rest = i % (8 * NG);
+      uint32_t x;
+      asm volatile("ld.shared.b32 %0, [%1];"
+                   : "=r"(x)
+                   : "r"(kt + VT + PAR + (half ? block_of(1) + row_of(1) / 2 * NG * 8 : 0) + rest * 8));
+      const float2 f = unpack2<false>(x);
+      most = fmaxf(most, fmaxf(f.x, f.y));
+    }
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
+    const int e = static_cast<int>(__float_as_uint(most) >> 23) - 127;   // most < 2^(e + 1)
+    const float now = fminf(shift, kShift - static_cast<float>(min(max(e, 0), 17)));
+    float by[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float old = ref[nt][j];
+        const float keep = old + (shift - now);          // the same maximum, the new shift
+        ref[nt][j] = top[nt][j] > keep + (now + kSlack) ? top[nt][j] - now : keep;
+        by[nt][j] = old == ref[nt][j] ? 1.f : fast_exp2(old - ref[nt][j]);
+      }
+    shift = now;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) l[nt][j] *= by[nt][j];
+#pragma unroll
+      for (int e4 = 0; e4 < 4; ++e4) {
+#pragma unroll
+        for (int i = 0; i < 2 * NG; ++i) o[i][nt][e4] *= by[nt][e4 & 1];
+#pragma unroll
+        for (int i = 0; i < NS; ++i) oz[i][nt][e4] *= by[nt][e4 & 1];
+      }
+    }
   }
 
-  // 32 tokens at `kt` (K) and `kt + VT` (V), the first `valid` of them real.
-  // `lrow[i]`: the lane's ldmatrix row of the group pair i, relative to codes.
+  // 32 tokens at `kt` (K) and `kt + VT` (V); RAGGED: only the first `valid` of
+  // them are real.  `lrow[i]`: the lane's ldmatrix row of the group pair i,
+  // relative to codes.  Apart from one rare branch this is straight code, so
+  // that loads, logic, matrix and exponential instructions can be interleaved.
+  template <bool RAGGED>
   __device__ __forceinline__ void stage(uint32_t kt, int valid, const uint32_t (&lrow)[NG / 2], int lane) {
-    const bool ragged = valid < kKv4Tokens;
-    if (ragged) clear_tail(kt, valid, lane);
+    if constexpr (RAGGED) clear_tail(kt, valid, lane);
+    // Is a value scale of 2 or more among the stage's?  Every lane looks at its
+    // share of the scales' pairs.
+    uint32_t large = 0;
+#pragma unroll
+    for (int i = 0; i < NG / 2; ++i) {
+      const int k = i * 32 + lane, half = k / (8 * NG), rest = k % (8 * NG);
+      uint32_t x;
+      asm volatile("ld.shared.b32 %0, [%1];"
+                   : "=r"(x)
+                   : "r"(kt + VT + PAR + (half ? block_of(1) + row_of(1) / 2 * NG * 8 : 0) + rest * 8));
+      large |= x;
+    }
     uint32_t at[NG / 2];
 #pragma unroll
     for (int i = 0; i < NG / 2; ++i) at[i] = kt + lrow[i];
@@ -356,25 +392,38 @@ struct Kv4Compute {
     const uint32_t kpar = kt + ((lane >> 2) * NG + place(2 * (lane & 3)) * NS) * 4;
     const uint32_t vpar = kt + ((lane & 3) * NG + place(lane >> 2) * NS) * 8;
 
+    // Logits.  Both halves go side by side, so that one's matrix instructions
+    // fill the other's latency.
     float s[2][NT][4];
+    uint32_t plo[2][NS], phi[2][NS], r[2][NG / 2][4];
     static_for<2>([&](auto mt) {
-      constexpr int KB = block_of(mt) + row_of(mt) * (D / 2);
       constexpr int KP = block_of(mt) + PAR + row_of(mt) * NG * 4;
-      uint32_t plo[NS], phi[NS];
-      lds_words<KP>(kpar, plo);
-      lds_words<KP + 8 * NG * 4>(kpar, phi);
-      uint32_t r[NG / 2][4];
-      static_for<NG / 2>([&](auto gp) { ldm_x4<KB, false>(at[gp], r[gp]); });
-      static_for<NS>([&](auto i) {
-        const float2 lo = unpack2<false>(plo[i]), up = unpack2<false>(phi[i]);
+      lds_words<KP>(kpar, plo[mt]);
+      lds_words<KP + 8 * NG * 4>(kpar, phi[mt]);
+    });
+    static_for<NG / 2>([&](auto gp) {
+      static_for<2>([&](auto mt) {
+        constexpr int KB = block_of(mt) + row_of(mt) * (D / 2);
+        ldm_x4<KB, false>(at[gp], r[mt][gp]);
+      });
+    });
+    static_for<NS>([&](auto i) {
+      float acc[2][NT][4];
+      static_for<GS>([&](auto j) {
+        constexpr int g = j * NS + i;
+        static_for<2>([&](auto mt) {
+          const uint32_t a = r[mt][g / 2][2 * (g & 1)], b = r[mt][g / 2][2 * (g & 1) + 1];
+          const uint32_t a8 = a >> 8, b8 = b >> 8;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float acc[4] = {lo.y * qs[i][nt][0], lo.y * qs[i][nt][1], up.y * qs[i][nt][0],
-                          up.y * qs[i][nt][1]};
-          static_for<GS>([&](auto j) {
-            constexpr int g = j * NS + i;
-            const uint32_t a = r[g / 2][2 * (g & 1)], b = r[g / 2][2 * (g & 1) + 1];
-            const uint32_t a8 = a >> 8, b8 = b >> 8;
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (j == 0) {
+              const float zl = __high2float(*reinterpret_cast<const __half2*>(&plo[mt][i]));
+              const float zu = __high2float(*reinterpret_cast<const __half2*>(&phi[mt][i]));
+              acc[mt][nt][0] = zl * qs[i][nt][0];
+              acc[mt][nt][1] = zl * qs[i][nt][1];
+              acc[mt][nt][2] = zu * qs[i][nt][0];
+              acc[mt][nt][3] = zu * qs[i][nt][1];
+            }
             uint32_t q[4];
             if constexpr (QREG) {
 #pragma unroll
@@ -382,29 +431,38 @@ struct Kv4Compute {
             } else {
               lds_words<g * NT * 512>(qaddr + nt * 512, q);
             }
-            mma_codes(acc, a & M0, b & M0, a8 & M0, b8 & M0, q[0], q[1]);
-            mma_codes(acc, a & M1, b & M1, a8 & M1, b8 & M1, q[2], q[3]);
-          });
+            mma_codes(acc[mt][nt], a & M0, b & M0, a8 & M0, b8 & M0, q[0], q[1]);
+            mma_codes(acc[mt][nt], a & M1, b & M1, a8 & M1, b8 & M1, q[2], q[3]);
+          }
+        });
+      });
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const float sl = __low2float(*reinterpret_cast<const __half2*>(&plo[mt][i]));
+        const float su = __low2float(*reinterpret_cast<const __half2*>(&phi[mt][i]));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float by = e < 2 ? lo.x : up.x;
-            s[mt][nt][e] = i == 0 ? by * acc[e] : fmaf(by, acc[e], s[mt][nt][e]);
+            const float by = e < 2 ? sl : su;
+            s[mt][nt][e] = i == 0 ? by * acc[mt][nt][e] : fmaf(by, acc[mt][nt][e], s[mt][nt][e]);
           }
-        }
-      });
-      // the group places of a head lie in lanes 4 / GS apart
+      }
+    });
+    // the group places of a head lie in lanes 4 / GS apart
 #pragma unroll
-      for (int m = 4 / GS; m < 4; m <<= 1)
+    for (int m = 4 / GS; m < 4; m <<= 1)
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[mt][nt][e] += __shfl_xor_sync(0xffffffffu, s[mt][nt][e], m);
-    });
 
-    // running maximum and sum; s stays in its own units (sc is not negative)
-    float alpha[NT][2];
-    bool grew = false;
-    if (ragged) {   // out of the maximum past the end
+    // Running maximum and sum; s stays in its own units (sc is not negative).
+    float top[NT][2];
+    bool rare = (large & 0x40004000u) != 0;
+    if constexpr (RAGGED) {   // out of the maximum past the end
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -421,77 +479,33 @@ struct Kv4Compute {
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-        v = fmaf(v, sc[nt][j], -shift);
-        const bool up = v > ref[nt][j] + kSlack;
-        alpha[nt][j] = up ? fast_exp2(ref[nt][j] - v) : 1.f;
-        ref[nt][j] = up ? v : ref[nt][j];
-        grew |= up;
+        top[nt][j] = v * sc[nt][j];
+        rare |= top[nt][j] > ref[nt][j] + (shift + kSlack);
       }
     }
-    if (__any_sync(0xffffffffu, grew)) rescale(alpha);
+    if (__any_sync(0xffffffffu, rare)) catch_up(top, kt, lane);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          s[mt][nt][e] = fast_exp2(fmaf(s[mt][nt][e], sc[nt][e & 1], -ref[nt][e & 1]));
-    if (ragged) {   // (a scale of zero times minus infinity is no number)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (mt * 16 + (e >> 1) * 8 + (lane >> 2) >= valid) s[mt][nt][e] = 0.f;
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) l[nt][e & 1] += s[mt][nt][e];
+        for (int e = 0; e < 4; ++e) {
+          float p = fast_exp2(fmaf(s[mt][nt][e], sc[nt][e & 1], -ref[nt][e & 1]));
+          // (a scale of zero times minus infinity is no number)
+          if (RAGGED && mt * 16 + (e >> 1) * 8 + (lane >> 2) >= valid) p = 0.f;
+          s[mt][nt][e] = p;
+          l[nt][e & 1] += p;
+        }
 
     static_for<2>([&](auto mt) {
       constexpr int VB = VT + block_of(mt) + row_of(mt) * (D / 2);
       constexpr int VP = VT + block_of(mt) + PAR + row_of(mt) / 2 * NG * 8;
       // (s, s), (z, z) of tokens 2c, 2c + 1, then of 8 + 2c, 9 + 2c, per set
       uint32_t w[NS][4];
-      uint32_t large = 0;
       static_for<NS>([&](auto i) {
         lds_pair<VP + i * 8>(vpar, w[i][0], w[i][1]);
         lds_pair<VP + (4 * NG + i) * 8>(vpar, w[i][2], w[i][3]);
-        large |= w[i][0] | w[i][2];
       });
-      if (__any_sync(0xffffffffu, (large & 0x40004000u) != 0)) {   // rare
-        float top = 0.f;
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          const float2 x = unpack2<false>(w[i][0]), y = unpack2<false>(w[i][2]);
-          top = fmaxf(fmaxf(top, fmaxf(x.x, x.y)), fmaxf(y.x, y.y));
-        }
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-        const float now = lowered(top, shift);
-        if (now < shift) {
-          const float down = fast_exp2(now - shift);
-          float by[NT][2];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              by[nt][j] = down;
-              ref[nt][j] += shift - now;
-            }
-#pragma unroll
-            for (int m2 = 0; m2 < 2; ++m2)
-#pragma unroll
-              for (int x = 0; x < 4; ++x) s[m2][nt][x] *= down;
-          }
-          rescale(by);
-          shift = now;
-        }
-      }
       // P^T as B operands: tokens 2c, 2c + 1 (b0) and 8 on (b1) of column lane / 4
       uint32_t b0[NT], b1[NT];
 #pragma unroll
@@ -661,7 +675,10 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas(D, HC, NT)) kv4_decod
     const bool done = mbar_wait(wbar + 8 * st, phase);
     if (!__all_sync(0xffffffffu, done)) { ok = false; break; }
     const int left = t1 - t0 - (warp + NW * k) * kKv4Tokens;
-    cs.stage(wbuf + st * STAGE, min(left, kKv4Tokens), lrow, lane);
+    if (left >= kKv4Tokens)
+      cs.template stage<false>(wbuf + st * STAGE, kKv4Tokens, lrow, lane);
+    else
+      cs.template stage<true>(wbuf + st * STAGE, left, lrow, lane);
     __syncwarp();
     if (k + NS < my_n) {
       fence_proxy_async_smem();
