@@ -105,7 +105,10 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], __half* scale
 // lane keeps the cosines and sines of its chunk in registers for every head
 // that it visits.  The half-split partner of a chunk comes from the lane that
 // holds it, so queries may be rotated in place.  The four lanes of 32
-// channels agree on the scale by shuffles.
+// channels agree on the scale by shuffles.  Bound by memory: a lane asks for
+// its chunks of up to kAhead heads before it works on the first.
+constexpr int kAhead = 3;
+
 template <bool BF, int D, bool KV4>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int LPR = D / 8;              // lanes per row
@@ -115,7 +118,24 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
   const int t = blockIdx.x;
   const int c = threadIdx.x % LPR;
   const int lane = threadIdx.x & 31;
+  const int all = a.Hq + 2 * a.Hkv, step = R * gridDim.y;
+  int u = R * blockIdx.y + threadIdx.x / LPR;
+  auto load = [&](int v) {
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (v < all) {
+      const uint16_t* row = v < a.Hq ? a.q + t * a.q_stride + v * D
+                                     : (v < a.Hq + a.Hkv ? a.k + t * a.k_stride + (v - a.Hq) * D
+                                                         : a.v + t * a.v_stride + (v - a.Hq - a.Hkv) * D);
+      x = *reinterpret_cast<const uint4*>(row + c * 8);
+    }
+    return x;
+  };
+  uint4 raw[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) raw[i] = load(u + i * step);
+
   int slot = a.slots[t];
+  const bool turned = c * 8 < a.rot;
   float cs[8], sn[8];
   if (a.rot > 0) {
     const int pos = a.positions[t];
@@ -125,16 +145,16 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
     }
     const float* row = a.cos_sin + static_cast<size_t>(pos) * a.rot;
     const int half = a.rot / 2;
-    if (c * 8 < a.rot) {
+    if (turned) {
       const int i0 = a.inter ? c * 4 : (c * 8 < half ? c * 8 : c * 8 - half);
       const int n = a.inter ? 4 : 8;
 #pragma unroll
       for (int i = 0; i < 8; i += 4) {
         if (i < n) {
-          const float4 u = __ldg(reinterpret_cast<const float4*>(row + i0 + i));
-          const float4 w = __ldg(reinterpret_cast<const float4*>(row + half + i0 + i));
-          cs[i] = u.x; cs[i + 1] = u.y; cs[i + 2] = u.z; cs[i + 3] = u.w;
-          sn[i] = w.x; sn[i + 1] = w.y; sn[i + 2] = w.z; sn[i + 3] = w.w;
+          const float4 x = __ldg(reinterpret_cast<const float4*>(row + i0 + i));
+          const float4 y = __ldg(reinterpret_cast<const float4*>(row + half + i0 + i));
+          cs[i] = x.x; cs[i + 1] = x.y; cs[i + 2] = x.z; cs[i + 3] = x.w;
+          sn[i] = y.x; sn[i + 1] = y.y; sn[i + 2] = y.z; sn[i + 3] = y.w;
         }
       }
     }
@@ -143,21 +163,16 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
     if (threadIdx.x == 0 && blockIdx.y == 0) record_error(a.err, kDevBadSlot);
     slot = -1;
   }
-  const int units = slot >= 0 ? a.Hq + 2 * a.Hkv : a.Hq;
-  const int step = R * gridDim.y;
-  const bool turned = c * 8 < a.rot;
+  const int units = slot >= 0 ? all : a.Hq;
+  const size_t block = slot >= 0 ? static_cast<size_t>(slot / a.bs) * a.Hkv : 0;
+  const int r = slot >= 0 ? slot % a.bs : 0;
   const bool first = c * 16 < a.rot;                       // chunk of the first half
   const int partner = a.inter || !turned ? lane : (first ? lane + a.rot / 16 : lane - a.rot / 16);
-  for (int u0 = R * blockIdx.y; u0 < units; u0 += step) {
-    const int u = u0 + threadIdx.x / LPR;
-    const bool live = u < units;
-    const bool is_q = u < a.Hq, is_v = u >= a.Hq + a.Hkv;
-    const int h = is_q ? u : (is_v ? u - a.Hq - a.Hkv : u - a.Hq);
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (live) {
-      const uint16_t* src = is_q ? a.q + t * a.q_stride : (is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride);
-      raw = *reinterpret_cast<const uint4*>(src + static_cast<size_t>(h) * D + c * 8);
-    }
+
+  auto work = [&](int v, const uint4& raw) {
+    const bool live = v < units;
+    const bool is_q = v < a.Hq, is_v = v >= a.Hq + a.Hkv;
+    const int h = is_q ? v : (is_v ? v - a.Hq - a.Hkv : v - a.Hq);
     float x[8];
     unpack8<BF>(raw, x);
     if (a.rot > 0) {
@@ -165,9 +180,9 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
         if (turned && !is_v) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float p = x[2 * i], r = x[2 * i + 1];
-            x[2 * i] = __fsub_rn(__fmul_rn(p, cs[i]), __fmul_rn(r, sn[i]));
-            x[2 * i + 1] = __fadd_rn(__fmul_rn(r, cs[i]), __fmul_rn(p, sn[i]));
+            const float p = x[2 * i], q = x[2 * i + 1];
+            x[2 * i] = __fsub_rn(__fmul_rn(p, cs[i]), __fmul_rn(q, sn[i]));
+            x[2 * i + 1] = __fadd_rn(__fmul_rn(q, cs[i]), __fmul_rn(p, sn[i]));
           }
         }
       } else {
@@ -181,24 +196,24 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
         if (turned && !is_v) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float p = __fmul_rn(x[i], cs[i]), r = __fmul_rn(y[i], sn[i]);
-            x[i] = first ? __fsub_rn(p, r) : __fadd_rn(p, r);
+            const float p = __fmul_rn(x[i], cs[i]), q = __fmul_rn(y[i], sn[i]);
+            x[i] = first ? __fsub_rn(p, q) : __fadd_rn(p, q);
           }
         }
       }
     }
     __half s, z;
     uint32_t w = 0;
-    if constexpr (KV4) w = quantise8(x, &s, &z);   // every lane: the shuffles want whole warps
-    if (!live) continue;
+    if constexpr (KV4) {   // whole warps: the shuffles want them; none where all rows are queries
+      if (__any_sync(0xffffffffu, live && !is_q)) w = quantise8(x, &s, &z);
+    }
+    if (!live) return;
     if (is_q) {
       *reinterpret_cast<uint4*>(a.q_out + (static_cast<size_t>(t) * a.Hq + h) * D + c * 8) = pack8<BF>(x);
-      continue;
+      return;
     }
-    const size_t tile = static_cast<size_t>(slot / a.bs) * a.Hkv + h;
-    const int r = slot % a.bs;
     if constexpr (KV4) {
-      uint8_t* base = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + tile * kv4_tile_bytes(D, a.bs);
+      uint8_t* base = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + (block + h) * kv4_tile_bytes(D, a.bs);
       const int g = c >> 2;
       *reinterpret_cast<uint32_t*>(base + kv4_code_off<D>(r, g) + (c & 3) * 4) = w;
       if ((c & 3) == 0) {
@@ -211,15 +226,34 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
         }
       }
     } else {
-      uint16_t* dst = static_cast<uint16_t*>(is_v ? a.v_cache : a.k_cache) + (tile * a.bs + r) * D + c * 8;
+      uint16_t* dst = static_cast<uint16_t*>(is_v ? a.v_cache : a.k_cache) + ((block + h) * a.bs + r) * D + c * 8;
       *reinterpret_cast<uint4*>(dst) = is_v ? raw : pack8<BF>(x);
     }
+  };
+
+  // the same number of rounds for every lane of a warp
+  for (int base = R * blockIdx.y; base < units; base += kAhead * step, u += kAhead * step) {
+    uint4 now[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) now[i] = raw[i];
+    if (base + kAhead * step < units) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) raw[i] = load(u + (kAhead + i) * step);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (base + i * step < units) work(u + i * step, now[i]);
   }
 }
 
 // Rows of the 4-bit cache back in 16 bits: the D/8 lanes of a row hold one
 // chunk each.  value = scale * (code + zero) in FP32 (the sum is exact), one
-// rounding at the store.  Rows of a negative or bad slot become zeros.
+// rounding at the store.  Rows of a negative or bad slot become zeros.  A CTA
+// takes kTokens tokens; a lane asks for the same head's chunk of all of them
+// before it works on the first (bound by memory: three of its four bytes are
+// written).
+constexpr int kTokens = 4;
+
 template <bool BF, int D>
 __global__ void __launch_bounds__(kThreads)
     kv4_gather_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
@@ -229,38 +263,52 @@ __global__ void __launch_bounds__(kThreads)
   constexpr int R = kThreads / LPR;
   pdl_wait();
   pdl_launch_dependents();
-  const long long row = static_cast<long long>(blockIdx.x) * R + threadIdx.x / LPR;
-  const int c = threadIdx.x % LPR;
-  if (row >= static_cast<long long>(T) * Hkv * 2) return;
-  const int t = static_cast<int>(row / (2 * Hkv));
-  const int u = static_cast<int>(row - static_cast<long long>(t) * 2 * Hkv);
-  const bool is_v = u >= Hkv;
-  const int h = is_v ? u - Hkv : u;
-  uint16_t* dst = (is_v ? v : k) + (static_cast<size_t>(t) * Hkv + h) * D + c * 8;
-  const int slot = slots[t];
-  if (slot < 0 || static_cast<long long>(slot) >= static_cast<long long>(NB) * bs) {
-    if (slot >= 0 && c == 0 && u == 0) record_error(err, kDevBadSlot);
-    *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
-    return;
-  }
-  const uint8_t* base = (is_v ? v_cache : k_cache) +
-                        (static_cast<size_t>(slot / bs) * Hkv + h) * kv4_tile_bytes(D, bs);
-  const int r = slot % bs, g = c >> 2;
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(base + kv4_code_off<D>(r, g) + (c & 3) * 4);
-  float s, z;
-  if (is_v) {
-    const uint8_t* p = base + kv4_v_par_off<D>(bs, r, g);
-    s = __half2float(*reinterpret_cast<const __half*>(p));
-    z = __half2float(*reinterpret_cast<const __half*>(p + 4));
-  } else {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(base + kv4_k_par_off<D>(bs, r, g)));
-    s = f.x;
-    z = f.y;
-  }
-  float x[8];
+  const int t0 = blockIdx.x * kTokens;
+  const int c = threadIdx.x % LPR, g = c >> 2;
+  size_t block[kTokens];
+  int row[kTokens];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = s * (static_cast<float>((w >> (4 * i)) & 15u) + z);
-  *reinterpret_cast<uint4*>(dst) = pack8<BF>(x);
+  for (int i = 0; i < kTokens; ++i) {
+    row[i] = -1;
+    if (t0 + i < T) {
+      const int slot = slots[t0 + i];
+      if (slot >= 0 && static_cast<long long>(slot) < static_cast<long long>(NB) * bs) {
+        block[i] = static_cast<size_t>(slot / bs) * Hkv;
+        row[i] = slot % bs;
+      } else if (slot >= 0 && threadIdx.x == 0 && blockIdx.y == 0) {
+        record_error(err, kDevBadSlot);
+      }
+    }
+  }
+  for (int u = R * blockIdx.y + threadIdx.x / LPR; u < 2 * Hkv; u += R * gridDim.y) {
+    const bool is_v = u >= Hkv;
+    const int h = is_v ? u - Hkv : u;
+    uint32_t w[kTokens], par[kTokens];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+      w[i] = par[i] = 0;
+      if (row[i] < 0) continue;
+      const uint8_t* base = (is_v ? v_cache : k_cache) + (block[i] + h) * kv4_tile_bytes(D, bs);
+      w[i] = *reinterpret_cast<const uint32_t*>(base + kv4_code_off<D>(row[i], g) + (c & 3) * 4);
+      if (is_v) {
+        const uint8_t* p = base + kv4_v_par_off<D>(bs, row[i], g);
+        par[i] = *reinterpret_cast<const uint16_t*>(p) |
+                 static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p + 4)) << 16;
+      } else {
+        par[i] = *reinterpret_cast<const uint32_t*>(base + kv4_k_par_off<D>(bs, row[i], g));
+      }
+    }
+    uint16_t* dst = (is_v ? v : k) + (static_cast<size_t>(t0) * Hkv + h) * D + c * 8;
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+      if (t0 + i >= T) break;
+      const float2 p = unpack2<false>(par[i]);   // a padding row: scale 0, all zeros
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = p.x * (static_cast<float>((w[i] >> (4 * j)) & 15u) + p.y);
+      *reinterpret_cast<uint4*>(dst + static_cast<size_t>(i) * Hkv * D) = pack8<BF>(x);
+    }
+  }
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -361,8 +409,10 @@ extern "C" int pkv_kv4_gather(const pkv_shape* s, const void* k_cache, const voi
       !aligned(slot_mapping, 4))
     return PKV_ERR_ALIGN;
   const int D = s->head_dim, rows = kThreads / (D / 8);
-  const long long grid = (static_cast<long long>(num_tokens) * s->num_kv_heads * 2 + rows - 1) / rows;
-  if (grid > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+  if (s->num_kv_heads > (1 << 29)) return PKV_ERR_UNSUPPORTED;
+  const int tiles = (num_tokens - 1) / kTokens + 1, passes = (2 * s->num_kv_heads - 1) / rows + 1;
+  // few tokens: the heads' passes on CTAs of their own
+  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(tiles < 1024 ? (passes < 65535 ? passes : 65535) : 1));
   int* err = device_error_word();
   if (!err) return PKV_ERR_CUDA;
   const bool bf = s->dtype == PKV_BF16;
@@ -370,7 +420,7 @@ extern "C" int pkv_kv4_gather(const pkv_shape* s, const void* k_cache, const voi
   if (D == 64) kern = bf ? kv4_gather_kernel<true, 64> : kv4_gather_kernel<false, 64>;
   if (D == 128) kern = bf ? kv4_gather_kernel<true, 128> : kv4_gather_kernel<false, 128>;
   if (D == 256) kern = bf ? kv4_gather_kernel<true, 256> : kv4_gather_kernel<false, 256>;
-  cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(grid)), kThreads, 0,
+  cudaError_t e = launch_pdl(kern, grid, kThreads, 0,
                              reinterpret_cast<cudaStream_t>(stream), static_cast<const uint8_t*>(k_cache),
                              static_cast<const uint8_t*>(v_cache), slot_mapping,
                              static_cast<uint16_t*>(k), static_cast<uint16_t*>(v), num_tokens,
