@@ -3,6 +3,7 @@
 // the read-back of 4-bit rows (pkv_kv4_gather).  Contracts in include/pkv.h.
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cfloat>
 
 #include "pkv.h"
@@ -27,9 +28,18 @@ struct RopeArgs {
   void* v_cache;
   int* err;
   long long q_stride, k_stride, v_stride;   // elements between tokens
-  int Hq, Hkv, bs, NB;
+  int T, Hq, Hkv, bs, NB;
+  int rows;                                 // head rows of one slice
   int rot, inter, max_pos;
 };
+
+// Untiled bulk copy to shared memory, completing on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
 
 __device__ __forceinline__ float min_nan(float a, float b) {
   float r;
@@ -57,11 +67,18 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 
 // Scale and zero point of the 32 channels that four neighbouring lanes hold
 // eight each of, and this lane's eight codes (channel i in bits 4i .. 4i + 3).
-// Every quotient is a true division: 16-bit inputs often fall exactly on a
-// border between two codes, where a product with a reciprocal would decide by
-// its own rounding.  The scale is rounded up so that 15 steps always span the
-// group, and is at least 1/1024 of its largest magnitude so that the zero
-// point keeps a fraction of a step in binary16.
+// Quotients are true divisions: 16-bit inputs often fall exactly on a border
+// between two codes, where a product with a reciprocal would decide by its own
+// rounding.  The scale is rounded up so that 15 steps always span the group,
+// and is at least 1/1024 of its largest magnitude so that the zero point keeps
+// a fraction of a step in binary16.
+//
+// A division per channel would cost more than all the rest, so the codes come
+// from x * (1 / s) - z, which is within 5 (|z| + 16) 2^-24 of the rounded
+// quotient less z wherever that is near 0 .. 15 (the reciprocal, the product,
+// the quotient and the two differences are off by 2^-24 of their values each,
+// and |x / s| < |z| + 16); where one of a warp's values lies within
+// 8 (|z| + 16) 2^-24 of a border, all are divided.
 __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], __half* scale, __half* zero) {
   float lo = x[0], hi = x[0];
 #pragma unroll
@@ -74,10 +91,7 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], __half* scale
     lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, m));
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, m));
   }
-  if (!(lo >= -FLT_MAX && hi <= FLT_MAX)) {   // an infinity or NaN: the group reads as NaN
-    *scale = *zero = __ushort_as_half(0x7e00);
-    return 0;
-  }
+  const bool finite = lo >= -FLT_MAX && hi <= FLT_MAX;
   const float want = fmaxf(fmaxf(__fdiv_rn(__fsub_rn(hi, lo), 15.f),
                                  __fmul_rn(fmaxf(fabsf(lo), fabsf(hi)), 0x1p-10f)),
                            0x1p-24f);
@@ -88,161 +102,227 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], __half* scale
     h = __float2half_rn(s);
   }
   const __half z = __float2half_rn(fminf(fmaxf(__fdiv_rn(lo, s), -65504.f), 65504.f));
-  const float zf = __half2float(z);
-  uint32_t w = 0;
+  const float zf = __half2float(z), inv = __frcp_rn(s);
+  constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: adding it rounds to a whole number, ties to even
+  const float safe = 0.5f - (fabsf(zf) + 16.f) * 0x1p-21f;
+  float n[8], off = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float n = fminf(fmaxf(rintf(__fsub_rn(__fdiv_rn(x[i], s), zf)), 0.f), 15.f);
-    w |= static_cast<uint32_t>(n) << (4 * i);
+    const float v = fminf(fmaxf(__fsub_rn(__fmul_rn(x[i], inv), zf), 0.f), 15.f);
+    n[i] = __fsub_rn(__fadd_rn(v, kMagic), kMagic);
+    off = fmaxf(off, fabsf(v - n[i]));
   }
-  *scale = h;
-  *zero = z;
-  return w;
+  if (__any_sync(0xffffffffu, !(off <= safe))) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float v = fminf(fmaxf(__fsub_rn(__fdiv_rn(x[i], s), zf), 0.f), 15.f);
+      n[i] = __fsub_rn(__fadd_rn(v, kMagic), kMagic);
+    }
+  }
+  // four codes side by side are exact in FP32, and 2^23 more leaves them in the low bits
+  const float w0 = fmaf(4096.f, n[3], fmaf(256.f, n[2], fmaf(16.f, n[1], n[0])));
+  const float w1 = fmaf(4096.f, n[7], fmaf(256.f, n[6], fmaf(16.f, n[5], n[4])));
+  const uint32_t w = (__float_as_uint(w0 + 8388608.f) & 0xffffu) | (__float_as_uint(w1 + 8388608.f) << 16);
+  *scale = finite ? h : __ushort_as_half(0x7e00);   // an infinity or NaN: the group reads as NaN
+  *zero = finite ? z : __ushort_as_half(0x7e00);
+  return finite ? w : 0u;
 }
 
-// One CTA per token (and slice of its heads).  A lane owns one 16-byte chunk
-// (eight channels) of a head row, the D/8 lanes of a row the whole row; the
-// lane keeps the cosines and sines of its chunk in registers for every head
-// that it visits.  The half-split partner of a chunk comes from the lane that
-// holds it, so queries may be rotated in place.  The four lanes of 32
-// channels agree on the scale by shuffles.  Bound by memory: a lane asks for
-// its chunks of up to kAhead heads before it works on the first.
-constexpr int kAhead = 3;
+// Rotation and append.  Work is (token, slice of its head rows); a CTA walks
+// tokens blockIdx.x, + gridDim.x, ... of slice blockIdx.y.  Thread 0 stages a
+// token's rows of the slice (a contiguous run each of q, k and v) and its
+// table row in shared memory with bulk copies, kStages tokens ahead, so that
+// the memory system always has tens of KB per SM to fetch and the lanes spend
+// no instructions on it; bound by memory.  A lane owns one 16-byte chunk (eight
+// channels) of a head row, the D/8 lanes of a row the whole row; it keeps the
+// cosines and sines of its chunk for every head of the token and reads the
+// half-split partner chunk from shared memory (so queries may be rotated in
+// place).  The four lanes of 32 channels agree on the scale by shuffles.
+// Measured on one GB300, 8192 tokens of 32 + 2 x 8 heads of 128: see the host
+// code for the choice of the grid.
+constexpr int kStages = 4;
+
+struct TokenMeta {
+  int slot;    // where k and v go, -1: nowhere
+  int known;   // the position has a table row
+};
 
 template <bool BF, int D, bool KV4>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) rope_append_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int LPR = D / 8;              // lanes per row
   constexpr int R = kThreads / LPR;       // rows per pass
+  constexpr int ROW = D * 2;              // bytes
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t bars[kStages];
+  __shared__ TokenMeta meta[kStages];
+  const int all = a.Hq + 2 * a.Hkv;
+  const int ua = a.rows * blockIdx.y, n = min(a.rows, all - ua);   // rows of the slice
+  const int stage_bytes = a.rows * ROW + a.rot * 4;
+  const uint32_t base = smem_u32(smem);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&bars[i]), 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
-  const int t = blockIdx.x;
+
+  // Thread 0: stage token `t`, whose position and slot are given.
+  auto issue = [&](int t, int pos, int slot, int st) {
+    const uint32_t bar = smem_u32(&bars[st]);
+    const bool known = a.rot == 0 || (pos >= 0 && pos < a.max_pos);
+    const bool beyond = slot >= 0 && static_cast<long long>(slot) >= static_cast<long long>(a.NB) * a.bs;
+    if (blockIdx.y == 0) {
+      if (!known) record_error(a.err, kDevBadPosition);
+      else if (beyond) record_error(a.err, kDevBadSlot);
+    }
+    meta[st].slot = beyond || slot < 0 ? -1 : slot;
+    meta[st].known = known;
+    if (!known) {
+      mbar_arrive(bar);
+      return;
+    }
+    const int end = meta[st].slot >= 0 ? ua + n : min(ua + n, a.Hq);   // rows to fetch: [ua, end)
+    mbar_arrive_expect_tx(bar, max(end - ua, 0) * ROW + a.rot * 4);
+    const uint32_t dst = base + st * stage_bytes;
+    // rows [from, to) of one tensor whose first row is row `zero` of the token
+    auto rows = [&](const uint16_t* x, long long stride, int zero, int heads) {
+      const int from = max(ua, zero), to = min(end, zero + heads);
+      if (from < to)
+        bulk_load(dst + (from - ua) * ROW, x + t * stride + (from - zero) * D, (to - from) * ROW, bar);
+    };
+    rows(a.q, a.q_stride, 0, a.Hq);
+    rows(a.k, a.k_stride, a.Hq, a.Hkv);
+    rows(a.v, a.v_stride, a.Hq + a.Hkv, a.Hkv);
+    if (a.rot > 0)
+      bulk_load(dst + a.rows * ROW, a.cos_sin + static_cast<size_t>(pos) * a.rot, a.rot * 4, bar);
+  };
+  const int gx = gridDim.x;
+  int npos = 0, nslot = 0;                // of the next token to stage (thread 0)
+  auto look = [&](int t) {
+    if (t < a.T) {
+      npos = a.rot > 0 ? a.positions[t] : 0;
+      nslot = a.slots[t];
+    }
+  };
+  if (threadIdx.x == 0) {
+    look(blockIdx.x);
+    for (int i = 0; i < kStages; ++i) {
+      const int t = blockIdx.x + i * gx;
+      if (t >= a.T) break;
+      const int pos = npos, slot = nslot;
+      look(t + gx);
+      issue(t, pos, slot, i);
+    }
+  }
+
   const int c = threadIdx.x % LPR;
-  const int lane = threadIdx.x & 31;
-  const int all = a.Hq + 2 * a.Hkv, step = R * gridDim.y;
-  int u = R * blockIdx.y + threadIdx.x / LPR;
-  auto load = [&](int v) {
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (v < all) {
-      const uint16_t* row = v < a.Hq ? a.q + t * a.q_stride + v * D
-                                     : (v < a.Hq + a.Hkv ? a.k + t * a.k_stride + (v - a.Hq) * D
-                                                         : a.v + t * a.v_stride + (v - a.Hq - a.Hkv) * D);
-      x = *reinterpret_cast<const uint4*>(row + c * 8);
-    }
-    return x;
-  };
-  uint4 raw[kAhead];
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) raw[i] = load(u + i * step);
-
-  int slot = a.slots[t];
-  const bool turned = c * 8 < a.rot;
-  float cs[8], sn[8];
-  if (a.rot > 0) {
-    const int pos = a.positions[t];
-    if (pos < 0 || pos >= a.max_pos) {
-      if (threadIdx.x == 0 && blockIdx.y == 0) record_error(a.err, kDevBadPosition);
-      return;
-    }
-    const float* row = a.cos_sin + static_cast<size_t>(pos) * a.rot;
-    const int half = a.rot / 2;
-    if (turned) {
-      const int i0 = a.inter ? c * 4 : (c * 8 < half ? c * 8 : c * 8 - half);
-      const int n = a.inter ? 4 : 8;
-#pragma unroll
-      for (int i = 0; i < 8; i += 4) {
-        if (i < n) {
-          const float4 x = __ldg(reinterpret_cast<const float4*>(row + i0 + i));
-          const float4 y = __ldg(reinterpret_cast<const float4*>(row + half + i0 + i));
-          cs[i] = x.x; cs[i + 1] = x.y; cs[i + 2] = x.z; cs[i + 3] = x.w;
-          sn[i] = y.x; sn[i + 1] = y.y; sn[i + 2] = y.z; sn[i + 3] = y.w;
+  const bool turned = c * 8 < a.rot, first = c * 16 < a.rot;       // in the rotated part; in its first half
+  const int partner = (first ? c * 8 + a.rot / 2 : c * 8 - a.rot / 2) * 2;   // byte of the other half's chunk
+  const int i0 = a.inter ? c * 4 : (first ? c * 8 : c * 8 - a.rot / 2);
+  const int g = c >> 2;
+  int st = 0;
+  uint32_t phase = 0;
+  bool failed = false;
+  for (int t = blockIdx.x; t < a.T; t += gx) {
+    const bool ok = mbar_wait(smem_u32(&bars[st]), phase);
+    if (ok && meta[st].known) {
+      const uint8_t* stage = smem + st * stage_bytes;
+      const int slot = meta[st].slot;
+      const int units = slot >= 0 ? n : min(n, a.Hq - ua);         // rows to work on
+      const size_t block = slot >= 0 ? static_cast<size_t>(slot / a.bs) * a.Hkv : 0;
+      const int r = slot >= 0 ? slot % a.bs : 0;
+      float cs[8], sn[8];
+      if (turned) {
+        const float* row = reinterpret_cast<const float*>(stage + a.rows * ROW) + i0;
+        const float4 c0 = *reinterpret_cast<const float4*>(row);
+        const float4 s0 = *reinterpret_cast<const float4*>(row + a.rot / 2);
+        cs[0] = c0.x; cs[1] = c0.y; cs[2] = c0.z; cs[3] = c0.w;
+        sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w;
+        if (!a.inter) {
+          const float4 c1 = *reinterpret_cast<const float4*>(row + 4);
+          const float4 s1 = *reinterpret_cast<const float4*>(row + a.rot / 2 + 4);
+          cs[4] = c1.x; cs[5] = c1.y; cs[6] = c1.z; cs[7] = c1.w;
+          sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
         }
       }
-    }
-  }
-  if (slot >= 0 && static_cast<long long>(slot) >= static_cast<long long>(a.NB) * a.bs) {
-    if (threadIdx.x == 0 && blockIdx.y == 0) record_error(a.err, kDevBadSlot);
-    slot = -1;
-  }
-  const int units = slot >= 0 ? all : a.Hq;
-  const size_t block = slot >= 0 ? static_cast<size_t>(slot / a.bs) * a.Hkv : 0;
-  const int r = slot >= 0 ? slot % a.bs : 0;
-  const bool first = c * 16 < a.rot;                       // chunk of the first half
-  const int partner = a.inter || !turned ? lane : (first ? lane + a.rot / 16 : lane - a.rot / 16);
-
-  auto work = [&](int v, const uint4& raw) {
-    const bool live = v < units;
-    const bool is_q = v < a.Hq, is_v = v >= a.Hq + a.Hkv;
-    const int h = is_q ? v : (is_v ? v - a.Hq - a.Hkv : v - a.Hq);
-    float x[8];
-    unpack8<BF>(raw, x);
-    if (a.rot > 0) {
-      if (a.inter) {
+      uint16_t* q_out = a.q_out + static_cast<size_t>(t) * a.Hq * D + c * 8;
+      // the same number of rounds for every lane of a warp (its shuffles want whole warps)
+      for (int b = 0; b < units; b += R) {
+        const int i = b + threadIdx.x / LPR, u = ua + i;
+        const bool live = i < units;
+        const bool is_q = u < a.Hq, is_v = u >= a.Hq + a.Hkv;
+        const uint8_t* row = stage + (live ? i : 0) * ROW;
+        const uint4 raw = *reinterpret_cast<const uint4*>(row + c * 16);
+        float x[8];
+        unpack8<BF>(raw, x);
         if (turned && !is_v) {
+          if (a.inter) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float p = x[2 * i], q = x[2 * i + 1];
-            x[2 * i] = __fsub_rn(__fmul_rn(p, cs[i]), __fmul_rn(q, sn[i]));
-            x[2 * i + 1] = __fadd_rn(__fmul_rn(q, cs[i]), __fmul_rn(p, sn[i]));
+            for (int j = 0; j < 4; ++j) {
+              const float p0 = x[2 * j], p1 = x[2 * j + 1];
+              x[2 * j] = __fsub_rn(__fmul_rn(p0, cs[j]), __fmul_rn(p1, sn[j]));
+              x[2 * j + 1] = __fadd_rn(__fmul_rn(p1, cs[j]), __fmul_rn(p0, sn[j]));
+            }
+          } else {
+            float y[8];
+            unpack8<BF>(*reinterpret_cast<const uint4*>(row + partner), y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float p0 = __fmul_rn(x[j], cs[j]), p1 = __fmul_rn(y[j], sn[j]);
+              x[j] = first ? __fsub_rn(p0, p1) : __fadd_rn(p0, p1);
+            }
           }
         }
-      } else {
-        uint4 other;
-        other.x = __shfl_sync(0xffffffffu, raw.x, partner);
-        other.y = __shfl_sync(0xffffffffu, raw.y, partner);
-        other.z = __shfl_sync(0xffffffffu, raw.z, partner);
-        other.w = __shfl_sync(0xffffffffu, raw.w, partner);
-        float y[8];
-        unpack8<BF>(other, y);
-        if (turned && !is_v) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float p = __fmul_rn(x[i], cs[i]), q = __fmul_rn(y[i], sn[i]);
-            x[i] = first ? __fsub_rn(p, q) : __fadd_rn(p, q);
-          }
+        __half s, z;
+        uint32_t w = 0;
+        if constexpr (KV4) {   // not where all rows are queries
+          if (__any_sync(0xffffffffu, live && !is_q)) w = quantise8(x, &s, &z);
         }
-      }
-    }
-    __half s, z;
-    uint32_t w = 0;
-    if constexpr (KV4) {   // whole warps: the shuffles want them; none where all rows are queries
-      if (__any_sync(0xffffffffu, live && !is_q)) w = quantise8(x, &s, &z);
-    }
-    if (!live) return;
-    if (is_q) {
-      *reinterpret_cast<uint4*>(a.q_out + (static_cast<size_t>(t) * a.Hq + h) * D + c * 8) = pack8<BF>(x);
-      return;
-    }
-    if constexpr (KV4) {
-      uint8_t* base = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + (block + h) * kv4_tile_bytes(D, a.bs);
-      const int g = c >> 2;
-      *reinterpret_cast<uint32_t*>(base + kv4_code_off<D>(r, g) + (c & 3) * 4) = w;
-      if ((c & 3) == 0) {
-        if (is_v) {
-          uint8_t* p = base + kv4_v_par_off<D>(a.bs, r, g);
-          *reinterpret_cast<__half*>(p) = s;
-          *reinterpret_cast<__half*>(p + 4) = z;
+        if (!live) continue;
+        if (is_q) {
+          *reinterpret_cast<uint4*>(q_out + u * D) = pack8<BF>(x);
+          continue;
+        }
+        const int h = u - a.Hq - (is_v ? a.Hkv : 0);
+        if constexpr (KV4) {
+          uint8_t* tile = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + (block + h) * kv4_tile_bytes(D, a.bs);
+          *reinterpret_cast<uint32_t*>(tile + kv4_code_off<D>(r, g) + (c & 3) * 4) = w;
+          if ((c & 3) == 0) {
+            if (is_v) {
+              uint8_t* par = tile + kv4_v_par_off<D>(a.bs, r, g);
+              *reinterpret_cast<__half*>(par) = s;
+              *reinterpret_cast<__half*>(par + 4) = z;
+            } else {
+              *reinterpret_cast<__half2*>(tile + kv4_k_par_off<D>(a.bs, r, g)) = __halves2half2(s, z);
+            }
+          }
         } else {
-          *reinterpret_cast<__half2*>(base + kv4_k_par_off<D>(a.bs, r, g)) = __halves2half2(s, z);
+          uint16_t* dst = static_cast<uint16_t*>(is_v ? a.v_cache : a.k_cache) + ((block + h) * a.bs + r) * D + c * 8;
+          *reinterpret_cast<uint4*>(dst) = is_v ? raw : pack8<BF>(x);
         }
       }
-    } else {
-      uint16_t* dst = static_cast<uint16_t*>(is_v ? a.v_cache : a.k_cache) + ((block + h) * a.bs + r) * D + c * 8;
-      *reinterpret_cast<uint4*>(dst) = is_v ? raw : pack8<BF>(x);
     }
-  };
-
-  // the same number of rounds for every lane of a warp
-  for (int base = R * blockIdx.y; base < units; base += kAhead * step, u += kAhead * step) {
-    uint4 now[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) now[i] = raw[i];
-    if (base + kAhead * step < units) {
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) raw[i] = load(u + (kAhead + i) * step);
+    failed = __syncthreads_or(!ok);       // every lane is done with the stage
+    if (failed) break;
+    if (threadIdx.x == 0) {
+      const int next = t + kStages * gx;
+      if (next < a.T) {
+        const int pos = npos, slot = nslot;
+        look(next + gx);
+        fence_proxy_async_smem();
+        issue(next, pos, slot, st);
+      }
     }
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (base + i * step < units) work(u + i * step, now[i]);
+    if (++st == kStages) {
+      st = 0;
+      phase ^= 1;
+    }
+  }
+  if (failed && threadIdx.x == 0) {
+    // a copy did not come in time: give all that are in flight a bounded chance to land
+    for (int i = 0; i < kStages; ++i) mbar_wait(smem_u32(&bars[i]), i >= st ? phase : phase ^ 1, 100000000ull);
+    record_error(a.err, kDevTimeout);
   }
 }
 
@@ -313,6 +393,21 @@ __global__ void __launch_bounds__(kThreads)
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// The kernels' shared-memory limit, raised once per device and kernel (threads
+// that race here set the same attribute).
+cudaError_t raise_smem(const void* kern, bool kv4, bool bf, int D) {
+  static std::atomic<unsigned> masks[12];
+  std::atomic<unsigned>& mask = masks[(D == 64 ? 0 : (D == 128 ? 1 : 2)) * 4 + kv4 * 2 + bf];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned bit = dev < 32 ? 1u << dev : 0u;
+  if (bit != 0 && (mask.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kStages * (16384 + 1024));
+  if (e == cudaSuccess) mask.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 template <bool KV4>
 int append(const pkv_shape* s, const pkv_rope* rope, const void* q, const void* k, const void* v,
            const int32_t* positions, const float* cos_sin, const int32_t* slots, int32_t num_tokens,
@@ -355,6 +450,7 @@ int append(const pkv_shape* s, const pkv_rope* rope, const void* q, const void* 
   a.q_out = static_cast<uint16_t*>(q_out);
   a.k_cache = k_cache;
   a.v_cache = v_cache;
+  a.T = num_tokens;
   a.Hq = q ? s->num_q_heads : 0;
   a.Hkv = s->num_kv_heads;
   a.bs = s->block_size;
@@ -367,10 +463,32 @@ int append(const pkv_shape* s, const pkv_rope* rope, const void* q, const void* 
   if (D == 64) kern = bf ? rope_append_kernel<true, 64, KV4> : rope_append_kernel<false, 64, KV4>;
   if (D == 128) kern = bf ? rope_append_kernel<true, 128, KV4> : rope_append_kernel<false, 128, KV4>;
   if (D == 256) kern = bf ? rope_append_kernel<true, 256, KV4> : rope_append_kernel<false, 256, KV4>;
-  const int rows = kThreads / (D / 8);
-  const int passes = (a.Hq + 2 * a.Hkv + rows - 1) / rows;
-  const dim3 grid(static_cast<unsigned>(num_tokens), static_cast<unsigned>(num_tokens < 1024 ? (passes < 65535 ? passes : 65535) : 1));
-  cudaError_t e = launch_pdl(kern, grid, kThreads, 0, reinterpret_cast<cudaStream_t>(stream), a);
+  int sms = 0;
+  rc = device_sms(&sms);
+  if (rc != PKV_OK) return rc;
+  // Three CTAs per SM walk the tokens.  A slice has at most 16 KB of rows (three
+  // CTAs of four stages fit an SM's shared memory), and fewer where there are
+  // not tokens enough for every CTA: down to one pass of the CTA's threads.
+  const int pass = kThreads / (D / 8), all = a.Hq + 2 * a.Hkv, most = 16384 / (D * 2);
+  const int resident = 3 * sms;
+  long long slices = (all + most - 1) / most;
+  if (num_tokens * slices < resident) {
+    slices = resident / num_tokens;
+    if (slices > (all + pass - 1) / pass) slices = (all + pass - 1) / pass;
+  }
+  a.rows = static_cast<int>((all + slices - 1) / slices);
+  a.rows = (a.rows + pass - 1) / pass * pass;
+  if (a.rows > most) a.rows = most;
+  slices = (all + a.rows - 1) / a.rows;
+  if (slices > 65535) return PKV_ERR_UNSUPPORTED;
+  long long walkers = resident / slices;
+  if (walkers < 1) walkers = 1;
+  const dim3 grid(static_cast<unsigned>(num_tokens < walkers ? num_tokens : walkers),
+                  static_cast<unsigned>(slices));
+  const size_t smem = static_cast<size_t>(kStages) * (static_cast<size_t>(a.rows) * D * 2 + a.rot * 4);
+  cudaError_t e = raise_smem(reinterpret_cast<const void*>(kern), KV4, bf, D);
+  if (e != cudaSuccess) return PKV_ERR_CUDA;
+  e = launch_pdl(kern, grid, kThreads, smem, reinterpret_cast<cudaStream_t>(stream), a);
   if (e != cudaSuccess) return PKV_ERR_CUDA;
   count_launch();
   return PKV_OK;
