@@ -28,7 +28,7 @@ struct RopeArgs {
   void* v_cache;
   int* err;
   long long q_stride, k_stride, v_stride;   // elements between tokens
-  int T, Hq, Hkv, bs, NB;
+  int T, Hq, Hkv, bs, bs_log2, NB;
   int rows;                                 // head rows of one slice
   int rot, inter, max_pos;
 };
@@ -65,20 +65,25 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     pack2<BF>(x[6], x[7]));
 }
 
+// The IEEE quotient a / b for b with at most 11 significant bits, y = 1 / b to
+// within 2^-23 of it.  q = a y, corrected by its exact remainder: before its
+// last rounding the result is within 2^-22 half-steps of a / b.  That decides
+// the rounding, as a / b is never that near a border between two floats: the
+// border c has 25 bits, a - b c is a multiple of 2^-36 of a, and not zero, so
+// a / b is at least 2^-12 steps away from c.  (Quotients below 2^-70 may be
+// off by more: their remainder is not exact.  They are never told from zero.)
+__device__ __forceinline__ float quotient(float a, float b, float y) {
+  const float q = __fmul_rn(a, y);
+  return fmaf(fmaf(-q, b, a), y, q);
+}
+
 // Scale and zero point of the 32 channels that four neighbouring lanes hold
 // eight each of, and this lane's eight codes (channel i in bits 4i .. 4i + 3).
-// Quotients are true divisions: 16-bit inputs often fall exactly on a border
+// Quotients are true ones: 16-bit inputs often fall exactly on a border
 // between two codes, where a product with a reciprocal would decide by its own
 // rounding.  The scale is rounded up so that 15 steps always span the group,
 // and is at least 1/1024 of its largest magnitude so that the zero point keeps
 // a fraction of a step in binary16.
-//
-// A division per channel would cost more than all the rest, so the codes come
-// from x * (1 / s) - z, which is within 5 (|z| + 16) 2^-24 of the rounded
-// quotient less z wherever that is near 0 .. 15 (the reciprocal, the product,
-// the quotient and the two differences are off by 2^-24 of their values each,
-// and |x / s| < |z| + 16); where one of a warp's values lies within
-// 8 (|z| + 16) 2^-24 of a border, all are divided.
 __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], __half* scale, __half* zero) {
   float lo = x[0], hi = x[0];
 #pragma unroll
@@ -92,37 +97,24 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], __half* scale
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, m));
   }
   const bool finite = lo >= -FLT_MAX && hi <= FLT_MAX;
-  const float want = fmaxf(fmaxf(__fdiv_rn(__fsub_rn(hi, lo), 15.f),
-                                 __fmul_rn(fmaxf(fabsf(lo), fabsf(hi)), 0x1p-10f)),
-                           0x1p-24f);
-  __half h = __float2half_ru(want);
-  float s = __half2float(h);
-  if (s > 65504.f) {
-    s = 65504.f;
-    h = __float2half_rn(s);
-  }
-  const __half z = __float2half_rn(fminf(fmaxf(__fdiv_rn(lo, s), -65504.f), 65504.f));
-  const float zf = __half2float(z), inv = __frcp_rn(s);
-  constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: adding it rounds to a whole number, ties to even
-  const float safe = 0.5f - (fabsf(zf) + 16.f) * 0x1p-21f;
-  float n[8], off = 0.f;
+  // (a span past FLT_MAX gives no number here, and the magnitude decides)
+  const float span = quotient(__fsub_rn(hi, lo), 15.f, 1.f / 15.f);
+  const float want =
+      fmaxf(fmaxf(span, __fmul_rn(fmaxf(fabsf(lo), fabsf(hi)), 0x1p-10f)), 0x1p-24f);
+  const __half h = __hmin(__float2half_ru(want), __ushort_as_half(0x7bff));   // at most 65504
+  const float s = __half2float(h);
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
+  y = fmaf(fmaf(-s, y, 1.f), y, y);
+  const __half z = __float2half_rn(fminf(fmaxf(quotient(lo, s, y), -65504.f), 65504.f));
+  const float zf = __half2float(z);
+  uint32_t w = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float v = fminf(fmaxf(__fsub_rn(__fmul_rn(x[i], inv), zf), 0.f), 15.f);
-    n[i] = __fsub_rn(__fadd_rn(v, kMagic), kMagic);
-    off = fmaxf(off, fabsf(v - n[i]));
+  for (int i = 7; i >= 0; --i) {
+    const float v = fminf(fmaxf(__fsub_rn(quotient(x[i], s, y), zf), 0.f), 15.f);
+    // 1.5 * 2^23 more rounds to a whole number, ties to even, in the low bits
+    w = w * 16u + (__float_as_uint(__fadd_rn(v, 12582912.f)) - 0x4b400000u);
   }
-  if (__any_sync(0xffffffffu, !(off <= safe))) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float v = fminf(fmaxf(__fsub_rn(__fdiv_rn(x[i], s), zf), 0.f), 15.f);
-      n[i] = __fsub_rn(__fadd_rn(v, kMagic), kMagic);
-    }
-  }
-  // four codes side by side are exact in FP32, and 2^23 more leaves them in the low bits
-  const float w0 = fmaf(4096.f, n[3], fmaf(256.f, n[2], fmaf(16.f, n[1], n[0])));
-  const float w1 = fmaf(4096.f, n[7], fmaf(256.f, n[6], fmaf(16.f, n[5], n[4])));
-  const uint32_t w = (__float_as_uint(w0 + 8388608.f) & 0xffffu) | (__float_as_uint(w1 + 8388608.f) << 16);
   *scale = finite ? h : __ushort_as_half(0x7e00);   // an infinity or NaN: the group reads as NaN
   *zero = finite ? z : __ushort_as_half(0x7e00);
   return finite ? w : 0u;
@@ -140,7 +132,7 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], __half* scale
 // place).  The four lanes of 32 channels agree on the scale by shuffles.
 // Measured on one GB300, 8192 tokens of 32 + 2 x 8 heads of 128: see the host
 // code for the choice of the grid.
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 
 struct TokenMeta {
   int slot;    // where k and v go, -1: nowhere
@@ -230,8 +222,8 @@ __global__ void __launch_bounds__(kThreads, 3) rope_append_kernel(const __grid_c
       const uint8_t* stage = smem + st * stage_bytes;
       const int slot = meta[st].slot;
       const int units = slot >= 0 ? n : min(n, a.Hq - ua);         // rows to work on
-      const size_t block = slot >= 0 ? static_cast<size_t>(slot / a.bs) * a.Hkv : 0;
-      const int r = slot >= 0 ? slot % a.bs : 0;
+      const uint32_t block = slot >= 0 ? static_cast<uint32_t>(slot >> a.bs_log2) * a.Hkv : 0;   // first tile
+      const int r = slot & (a.bs - 1);
       float cs[8], sn[8];
       if (turned) {
         const float* row = reinterpret_cast<const float*>(stage + a.rows * ROW) + i0;
@@ -286,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_append_kernel(const __grid_c
         }
         const int h = u - a.Hq - (is_v ? a.Hkv : 0);
         if constexpr (KV4) {
-          uint8_t* tile = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + (block + h) * kv4_tile_bytes(D, a.bs);
+          uint8_t* tile = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + static_cast<size_t>(block + h) * static_cast<uint32_t>(kv4_tile_bytes(D, a.bs));
           *reinterpret_cast<uint32_t*>(tile + kv4_code_off<D>(r, g) + (c & 3) * 4) = w;
           if ((c & 3) == 0) {
             if (is_v) {
@@ -298,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 3) rope_append_kernel(const __grid_c
             }
           }
         } else {
-          uint16_t* dst = static_cast<uint16_t*>(is_v ? a.v_cache : a.k_cache) + ((block + h) * a.bs + r) * D + c * 8;
+          uint16_t* dst = static_cast<uint16_t*>(is_v ? a.v_cache : a.k_cache) + static_cast<size_t>((block + h) * a.bs + r) * D + c * 8;
           *reinterpret_cast<uint4*>(dst) = is_v ? raw : pack8<BF>(x);
         }
       }
@@ -326,69 +318,83 @@ __global__ void __launch_bounds__(kThreads, 3) rope_append_kernel(const __grid_c
   }
 }
 
-// Rows of the 4-bit cache back in 16 bits: the D/8 lanes of a row hold one
-// chunk each.  value = scale * (code + zero) in FP32 (the sum is exact), one
-// rounding at the store.  Rows of a negative or bad slot become zeros.  A CTA
-// takes kTokens tokens; a lane asks for the same head's chunk of all of them
-// before it works on the first (bound by memory: three of its four bytes are
-// written).
-constexpr int kTokens = 4;
+// Rows of the 4-bit cache back in 16 bits.  value = scale * (code + zero) in
+// FP32 (the sum is exact), one rounding at the store.  Rows of a negative or
+// bad slot become zeros.  The D/8 lanes of a row hold one chunk each; a CTA
+// takes two tokens (whose value parameters share bytes) and kLoops passes over
+// their head rows.  Bound by memory: three of its four bytes are written.
+constexpr int kGatherThreads = 128;
+constexpr int kTokens = 2;
+constexpr int kLoops = 2;
 
-template <bool BF, int D>
-__global__ void __launch_bounds__(kThreads)
+template <bool BF, int D, int BS>
+__global__ void __launch_bounds__(kGatherThreads)
     kv4_gather_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
                       const int32_t* __restrict__ slots, uint16_t* __restrict__ k,
-                      uint16_t* __restrict__ v, int T, int Hkv, int bs, int NB, int* err) {
+                      uint16_t* __restrict__ v, int T, int Hkv, int NB, int* err) {
   constexpr int LPR = D / 8;
-  constexpr int R = kThreads / LPR;
+  constexpr int R = kGatherThreads / LPR;
+  constexpr uint32_t TILE = kv4_tile_bytes(D, BS);
   pdl_wait();
   pdl_launch_dependents();
   const int t0 = blockIdx.x * kTokens;
   const int c = threadIdx.x % LPR, g = c >> 2;
-  size_t block[kTokens];
+  uint32_t block[kTokens];   // first tile of the slot's block
   int row[kTokens];
 #pragma unroll
   for (int i = 0; i < kTokens; ++i) {
     row[i] = -1;
     if (t0 + i < T) {
-      const int slot = slots[t0 + i];
-      if (slot >= 0 && static_cast<long long>(slot) < static_cast<long long>(NB) * bs) {
-        block[i] = static_cast<size_t>(slot / bs) * Hkv;
-        row[i] = slot % bs;
+      const int slot = __ldg(slots + t0 + i);
+      if (slot >= 0 && static_cast<long long>(slot) < static_cast<long long>(NB) * BS) {
+        block[i] = static_cast<uint32_t>(slot / BS) * Hkv;
+        row[i] = slot % BS;
       } else if (slot >= 0 && threadIdx.x == 0 && blockIdx.y == 0) {
         record_error(err, kDevBadSlot);
       }
     }
   }
-  for (int u = R * blockIdx.y + threadIdx.x / LPR; u < 2 * Hkv; u += R * gridDim.y) {
+  const int last = min(2 * Hkv, R * kLoops * static_cast<int>(blockIdx.y + 1));
+  for (int u = R * kLoops * blockIdx.y + threadIdx.x / LPR; u < last; u += R) {
     const bool is_v = u >= Hkv;
     const int h = is_v ? u - Hkv : u;
+    const uint8_t* cache = is_v ? v_cache : k_cache;
     uint32_t w[kTokens], par[kTokens];
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
-      w[i] = par[i] = 0;
+      w[i] = par[i] = 0;                         // a padding row: scale 0, all zeros
       if (row[i] < 0) continue;
-      const uint8_t* base = (is_v ? v_cache : k_cache) + (block[i] + h) * kv4_tile_bytes(D, bs);
-      w[i] = *reinterpret_cast<const uint32_t*>(base + kv4_code_off<D>(row[i], g) + (c & 3) * 4);
+      const uint8_t* base = cache + static_cast<size_t>(block[i] + h) * TILE;
+      w[i] = __ldg(reinterpret_cast<const uint32_t*>(base + kv4_code_off<D>(row[i], g) + (c & 3) * 4));
       if (is_v) {
-        const uint8_t* p = base + kv4_v_par_off<D>(bs, row[i], g);
-        par[i] = *reinterpret_cast<const uint16_t*>(p) |
-                 static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p + 4)) << 16;
+        const uint8_t* p = base + kv4_v_par_off<D>(BS, row[i], g);
+        par[i] = __ldg(reinterpret_cast<const uint16_t*>(p)) |
+                 static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p + 4))) << 16;
       } else {
-        par[i] = *reinterpret_cast<const uint32_t*>(base + kv4_k_par_off<D>(bs, row[i], g));
+        par[i] = __ldg(reinterpret_cast<const uint32_t*>(base + kv4_k_par_off<D>(BS, row[i], g)));
       }
     }
     uint16_t* dst = (is_v ? v : k) + (static_cast<size_t>(t0) * Hkv + h) * D + c * 8;
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
       if (t0 + i >= T) break;
-      const float2 p = unpack2<false>(par[i]);   // a padding row: scale 0, all zeros
+      const float2 p = unpack2<false>(par[i]);
       float x[8];
+      // nibbles j and j + 4 as binary16 subnormals, n * 2^-24; n + z and 2^24 (n 2^-24) are exact
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = p.x * (static_cast<float>((w[i] >> (4 * j)) & 15u) + p.y);
+      for (int j = 0; j < 4; ++j) {
+        const float2 n = unpack2<false>((w[i] >> (4 * j)) & 0x000f000fu);
+        x[j] = p.x * fmaf(n.x, 0x1p24f, p.y);
+        x[j + 4] = p.x * fmaf(n.y, 0x1p24f, p.y);
+      }
       *reinterpret_cast<uint4*>(dst + static_cast<size_t>(i) * Hkv * D) = pack8<BF>(x);
     }
   }
+}
+
+template <bool BF, int D>
+auto gather_kernel(int bs) {
+  return bs == 32 ? kv4_gather_kernel<BF, D, 32> : kv4_gather_kernel<BF, D, 16>;
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -454,6 +460,7 @@ int append(const pkv_shape* s, const pkv_rope* rope, const void* q, const void* 
   a.Hq = q ? s->num_q_heads : 0;
   a.Hkv = s->num_kv_heads;
   a.bs = s->block_size;
+  a.bs_log2 = s->block_size == 32 ? 5 : 4;
   a.NB = s->num_blocks;
   a.rot = rope->rot_dim;
   a.inter = rope->interleaved != 0;
@@ -526,23 +533,24 @@ extern "C" int pkv_kv4_gather(const pkv_shape* s, const void* k_cache, const voi
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
       !aligned(slot_mapping, 4))
     return PKV_ERR_ALIGN;
-  const int D = s->head_dim, rows = kThreads / (D / 8);
+  const int D = s->head_dim;
   if (s->num_kv_heads > (1 << 29)) return PKV_ERR_UNSUPPORTED;
-  const int tiles = (num_tokens - 1) / kTokens + 1, passes = (2 * s->num_kv_heads - 1) / rows + 1;
-  // few tokens: the heads' passes on CTAs of their own
-  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(tiles < 1024 ? (passes < 65535 ? passes : 65535) : 1));
+  const int rows = kGatherThreads / (D / 8), passes = (2 * s->num_kv_heads - 1) / rows + 1;
+  if (passes > 65535) return PKV_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>((num_tokens - 1) / kTokens + 1),
+                  static_cast<unsigned>((passes - 1) / kLoops + 1));
   int* err = device_error_word();
   if (!err) return PKV_ERR_CUDA;
   const bool bf = s->dtype == PKV_BF16;
-  auto kern = kv4_gather_kernel<false, 64>;
-  if (D == 64) kern = bf ? kv4_gather_kernel<true, 64> : kv4_gather_kernel<false, 64>;
-  if (D == 128) kern = bf ? kv4_gather_kernel<true, 128> : kv4_gather_kernel<false, 128>;
-  if (D == 256) kern = bf ? kv4_gather_kernel<true, 256> : kv4_gather_kernel<false, 256>;
-  cudaError_t e = launch_pdl(kern, grid, kThreads, 0,
+  const int bs = s->block_size;
+  auto kern = bf ? gather_kernel<true, 64>(bs) : gather_kernel<false, 64>(bs);
+  if (D == 128) kern = bf ? gather_kernel<true, 128>(bs) : gather_kernel<false, 128>(bs);
+  if (D == 256) kern = bf ? gather_kernel<true, 256>(bs) : gather_kernel<false, 256>(bs);
+  cudaError_t e = launch_pdl(kern, grid, kGatherThreads, 0,
                              reinterpret_cast<cudaStream_t>(stream), static_cast<const uint8_t*>(k_cache),
                              static_cast<const uint8_t*>(v_cache), slot_mapping,
                              static_cast<uint16_t*>(k), static_cast<uint16_t*>(v), num_tokens,
-                             s->num_kv_heads, s->block_size, s->num_blocks, err);
+                             s->num_kv_heads, s->num_blocks, err);
   if (e != cudaSuccess) return PKV_ERR_CUDA;
   count_launch();
   return PKV_OK;
