@@ -447,11 +447,6 @@ def _launch_stream(stream, dev: torch.device) -> int:
     return _stream_ptr(stream, dev)
 
 
-def _on(dev: torch.device):
-    """Make `dev` current, where it is not."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-
-
 def _allocating_on(stream):
     """Allocate for work on `stream`: memory that the caller drops is then not
     handed out again before that work has run."""
@@ -547,21 +542,27 @@ def _append(fn: str, dims, q, k, v, positions, cos_sin, slot_mapping, k_cache, v
         qs, ks, vs = _check_append(dims, q, k, v, positions, cos_sin, slot_mapping, k_cache,
                                    v_cache, q_out, dtype)
     T, dev = k.shape[0], k_cache.device
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _append(fn, dims, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache,
+                           q_out, interleaved, stream, dtype)
     Hq = 0 if q is None else q.shape[1]
     rows, rot = (0, 0) if cos_sin is None else cos_sin.shape
     ptr = _launch_stream(stream, dev)
-    shape = _sized(0, max(Hq, 1), Hkv, D, bs, NB, 1, 1, _DT[dtype])
-    rope = _rope(rot, 1 if interleaved else 0, rows, qs, ks, vs)
-    with _on(dev):
-        if q is not None and q_out is None:
-            with _allocating_on(stream):
+    if q is not None and q_out is None:
+        if stream is None:
+            q_out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
+        else:
+            with torch.cuda.stream(stream):
                 q_out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
-        rc = getattr(load_library(), fn)(
-            shape.ref, rope, q.data_ptr() if Hq else None, k.data_ptr(), v.data_ptr(),
-            positions.data_ptr() if rot else None, cos_sin.data_ptr() if rot else None,
-            slot_mapping.data_ptr(), T, q_out.data_ptr() if Hq else None, k_cache.data_ptr(),
-            v_cache.data_ptr(), ptr)
-    _check(fn, rc)
+    rc = getattr(_LIB or load_library(), fn)(
+        _sized(0, Hq or 1, Hkv, D, bs, NB, 1, 1, _DT[dtype]).ref,
+        _rope(rot, 1 if interleaved else 0, rows, qs, ks, vs), q.data_ptr() if Hq else None,
+        k.data_ptr(), v.data_ptr(), positions.data_ptr() if rot else None,
+        cos_sin.data_ptr() if rot else None, slot_mapping.data_ptr(), T,
+        q_out.data_ptr() if Hq else None, k_cache.data_ptr(), v_cache.data_ptr(), ptr)
+    if rc:
+        raise PkvError(fn, rc)
     return q_out
 
 
@@ -618,15 +619,19 @@ def kv4_gather(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch
             if t.shape != (T, Hkv, D):
                 raise ValueError(f"{n} must be [T, Hkv, D]")
     dev = _one_device(k_cache=k_cache, v_cache=v_cache, slot_mapping=slot_mapping, k=k, v=v)
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return kv4_gather(k_cache, v_cache, slot_mapping, dtype, k, v, stream)
     ptr = _launch_stream(stream, dev)
-    shape = _sized(0, 1, Hkv, D, bs, NB, 1, 1, code)
-    with _on(dev):
+    if k is None or v is None:
         with _allocating_on(stream):
             k = torch.empty((T, Hkv, D), dtype=dtype, device=dev) if k is None else k
             v = torch.empty((T, Hkv, D), dtype=dtype, device=dev) if v is None else v
-        rc = load_library().pkv_kv4_gather(shape.ref, k_cache.data_ptr(), v_cache.data_ptr(),
-                                           slot_mapping.data_ptr(), T, k.data_ptr(), v.data_ptr(), ptr)
-    _check("pkv_kv4_gather", rc)
+    rc = (_LIB or load_library()).pkv_kv4_gather(
+        _sized(0, 1, Hkv, D, bs, NB, 1, 1, code).ref, k_cache.data_ptr(), v_cache.data_ptr(),
+        slot_mapping.data_ptr(), T, k.data_ptr(), v.data_ptr(), ptr)
+    if rc:
+        raise PkvError("pkv_kv4_gather", rc)
     return k, v
 
 
@@ -662,15 +667,23 @@ def kv4_workspace_bytes(shape: Shape) -> int:
     return int(n.value)
 
 
-def kv4_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
-                    block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
-                    out: torch.Tensor | None = None, *, max_context_len: int | None = None,
-                    split_tokens: int = 0, workspace: torch.Tensor | None = None,
-                    stream=None) -> torch.Tensor:
-    """paged_attn_decode over 4-bit caches (kv4_cache): q [B, Hq, D] fp16 or
-    bf16, out of q's type.  A length of 0 marks a padding row, whose out rows
-    are set to zero.  workspace as for paged_attn_decode
-    (kv4_workspace_bytes)."""
+def _kv4_decode_plain(q, k_cache, v_cache, block_tables, context_lens) -> bool:
+    """Whether a call is the usual one: _check_kv4_decode would find nothing.
+    Looks at each tensor once (a decode step makes this call for every layer)."""
+    dev, qs, ks, bt = q.get_device(), q.shape, k_cache.shape, block_tables.shape
+    return (dev >= 0 and len(qs) == 3 and len(ks) == 4 and len(bt) == 2 and q.dtype in _DT
+            and ks[3] * 8 == qs[2] * 5 and v_cache.shape == ks and bt[0] == qs[0]
+            and context_lens.shape == (qs[0],) and k_cache.dtype is torch.uint8
+            and v_cache.dtype is torch.uint8 and block_tables.dtype is torch.int32
+            and context_lens.dtype is torch.int32 and k_cache.get_device() == dev
+            and v_cache.get_device() == dev and block_tables.get_device() == dev
+            and context_lens.get_device() == dev and q.is_contiguous() and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and block_tables.is_contiguous()
+            and context_lens.is_contiguous())
+
+
+def _check_kv4_decode(q, k_cache, v_cache, block_tables, context_lens, out, workspace):
+    """Refuse what does not fit together."""
     NB, Hkv, bs, D = _kv4_dims(k_cache, v_cache)
     _dense(q, "q")
     _dtype_code(q.dtype)
@@ -687,25 +700,45 @@ def kv4_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
             raise ValueError("out must have q's shape [B, Hq, D]")
     if workspace is not None:
         _dense(workspace, "workspace")
-    dev = _one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                      context_lens=context_lens, out=out, workspace=workspace)
+    _one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                context_lens=context_lens, out=out, workspace=workspace)
+
+
+def kv4_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                    out: torch.Tensor | None = None, *, max_context_len: int | None = None,
+                    split_tokens: int = 0, workspace: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """paged_attn_decode over 4-bit caches (kv4_cache): q [B, Hq, D] fp16 or
+    bf16, out of q's type.  A length of 0 marks a padding row, whose out rows
+    are set to zero.  workspace as for paged_attn_decode
+    (kv4_workspace_bytes)."""
+    if out is not None or workspace is not None or not _kv4_decode_plain(
+            q, k_cache, v_cache, block_tables, context_lens):
+        _check_kv4_decode(q, k_cache, v_cache, block_tables, context_lens, out, workspace)
+    dev = q.device
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return kv4_attn_decode(q, k_cache, v_cache, block_tables, context_lens, scale, out,
+                                   max_context_len=max_context_len, split_tokens=split_tokens,
+                                   workspace=workspace, stream=stream)
     ptr = _launch_stream(stream, dev)
     shape = _kv4_sized(q, k_cache, block_tables, max_context_len, split_tokens)
-    with _on(dev):
+    n = 0
+    if workspace is None and dev.index not in _SET_WS:
+        n = shape.kv4_workspace.get(dev.index)
+        if n is None:
+            n = shape.kv4_workspace[dev.index] = kv4_workspace_bytes(shape)
+    if n or out is None:
         with _allocating_on(stream):
-            if workspace is None and dev.index not in _SET_WS:
-                n = shape.kv4_workspace.get(dev.index)
-                if n is None:
-                    n = shape.kv4_workspace[dev.index] = kv4_workspace_bytes(shape)
-                if n:
-                    workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-            if out is None:
-                out = torch.empty_like(q)
-        rc = load_library().pkv_kv4_attn_decode(
-            shape.ref, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            block_tables.data_ptr(), context_lens.data_ptr(), float(scale), out.data_ptr(),
-            _ptr(workspace), _nbytes(workspace), ptr)
-    _check("pkv_kv4_attn_decode", rc)
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else workspace
+            out = torch.empty_like(q) if out is None else out
+    rc = (_LIB or load_library()).pkv_kv4_attn_decode(
+        shape.ref, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+        context_lens.data_ptr(), float(scale), out.data_ptr(),
+        None if workspace is None else workspace.data_ptr(), _nbytes(workspace), ptr)
+    if rc:
+        raise PkvError("pkv_kv4_attn_decode", rc)
     return out
 
 
