@@ -37,11 +37,16 @@
 //     tokens' words side by side; two m16 tiles per group.
 //   z^T P' with the pairs (s, z) as they lie in the cache for the A operand:
 //     rows 8 on give the zero-point sums (one m16 tile per GS groups).
-// P is scaled by 2^(9-E), E >= 0 from the largest value scale so far, so that
-// neither small weights nor small scales fall out of binary16; the running sum
-// carries the same factor.  The running maximum follows the true one only when
-// that is more than 2^5 ahead, which spares most rescalings of the
-// accumulators: P stays at most 2^14 and P' below 2^15.
+// P is scaled by 2^(12-E), E >= 0 the exponent of the largest value scale so
+// far, so that neither small weights nor small scales fall out of binary16; the
+// running sum carries the same factor.  The reference follows the running
+// maximum only when that is more than a factor of 2 ahead, which spares the
+// rescalings for small gains: P stays at most 2^13 and P' below 2^14.
+// (Following at once makes the largest weight a power of two, which rounds to
+// itself: binary16 results are then off by 2.7e-4 of their size in all, 2.8e-4
+// as it is, 3.3e-4 at a factor of 32; their own rounding is 2.1e-4.  The 64
+// sequences of 512-4096 tokens take 123 us in all three; 256 of 1-2048, four
+// query heads a key head, 72.9, 71.7 and 71 us.)
 #pragma once
 
 #include <cuda_fp16.h>
@@ -178,7 +183,7 @@ struct Kv4Compute {
   // tokens: 121 us, 123 with fragments in registers).
   static constexpr bool QREG = D * NT < 128;
   static constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u;
-  static constexpr float kShift = 9.f, kSlack = 5.f;
+  static constexpr float kShift = 12.f, kSlack = 1.f;
   static_assert(NG % GS == 0 && (NT == 1 || HC == 8), "columns");
 
   // Columns 2c and 2c + 1 (c = lane % 4) are two heads of one group place.
@@ -324,24 +329,27 @@ struct Kv4Compute {
     __syncwarp();
   }
 
-  // The running maximum is more than the slack behind `top`, or a value scale
-  // of 2 or more is in the stage: set the reference (and the shift, so that
-  // weights times the largest scale stay in binary16) and rescale the sums.
-  __device__ __forceinline__ void catch_up(const float (&top)[NT][2], uint32_t kt, int lane) {
-    float most = 0.f;
-    for (int i = lane; i < 16 * NG; i += 32) {
-      const int half = i / (8 * NG), rest = i % (8 * NG);
-      uint32_t x;
-      asm volatile("ld.shared.b32 %0, [%1];"
-                   : "=r"(x)
-                   : "r"(kt + VT + PAR + (half ? block_of(1) + row_of(1) / 2 * NG * 8 : 0) + rest * 8));
-      const float2 f = unpack2<false>(x);
-      most = fmaxf(most, fmaxf(f.x, f.y));
-    }
+  // The running maximum is more than the slack behind `top`, or (large) a value
+  // scale of 2 or more is in the stage: set the reference (and the shift, so
+  // that weights times the largest scale stay in binary16) and rescale the sums.
+  __device__ __forceinline__ void catch_up(const float (&top)[NT][2], bool large, uint32_t kt, int lane) {
+    float now = shift;
+    if (__any_sync(0xffffffffu, large)) {
+      float most = 0.f;
+      for (int i = lane; i < 16 * NG; i += 32) {
+        const int half = i / (8 * NG), rest = i % (8 * NG);
+        uint32_t x;
+        asm volatile("ld.shared.b32 %0, [%1];"
+                     : "=r"(x)
+                     : "r"(kt + VT + PAR + (half ? block_of(1) + row_of(1) / 2 * NG * 8 : 0) + rest * 8));
+        const float2 f = unpack2<false>(x);
+        most = fmaxf(most, fmaxf(f.x, f.y));
+      }
 #pragma unroll
-    for (int m = 1; m < 32; m <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
-    const int e = static_cast<int>(__float_as_uint(most) >> 23) - 127;   // most < 2^(e + 1)
-    const float now = fminf(shift, kShift - static_cast<float>(min(max(e, 0), 17)));
+      for (int m = 1; m < 32; m <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
+      const int e = static_cast<int>(__float_as_uint(most) >> 23) - 127;   // most < 2^(e + 1)
+      now = fminf(now, kShift - static_cast<float>(min(max(e, 0), 17)));
+    }
     float by[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -464,7 +472,8 @@ struct Kv4Compute {
 
     // Running maximum and sum; s stays in its own units (sc is not negative).
     float top[NT][2];
-    bool rare = (large & 0x40004000u) != 0;
+    const bool big = (large & 0x40004000u) != 0;
+    bool rare = big;
     if constexpr (RAGGED) {   // out of the maximum past the end
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -486,7 +495,7 @@ struct Kv4Compute {
         rare |= top[nt][j] > ref[nt][j] + (shift + kSlack);
       }
     }
-    if (__any_sync(0xffffffffu, rare)) catch_up(top, kt, lane);
+    if (__any_sync(0xffffffffu, rare)) catch_up(top, big, kt, lane);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

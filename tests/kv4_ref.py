@@ -130,7 +130,7 @@ def attention(q: np.ndarray, k_cache: np.ndarray, v_cache: np.ndarray, tables: n
             w /= w.sum()
             out[i, h], mag[i, h] = w @ v[:, g], w @ np.abs(v[:, g])
             E = max(0.0, np.floor(np.log2(top[g])))
-            low[i, h] = w.max() * 2.0 ** (E - 34) * np.abs(v[:, g]).sum(0)
+            low[i, h] = w.max() * 2.0 ** (E - 37) * np.abs(v[:, g]).sum(0)
             # in units of the largest step count: D / 8 + 8 FP32 roundings of the
             # largest partial sum, and what q loses in binary16's subnormals
             steps, rest = (D / 8 + 8) * 2.0 ** -24, 2.0 ** -35 * np.abs(qh).max()
@@ -163,8 +163,8 @@ def attention_bound(out, mag, low, smag, eps: float) -> np.ndarray:
        at most, exp2 to 2^-22, the sums in FP32 (at most 2^-24 a term, pairwise
        within a warp: 2^-14 covers 2^10 terms in a row);
      - weights below binary16's smallest normal number are off by up to half
-       its smallest step, 2^-25, where the largest weight is at least 2^(9-E)
-       (E: the exponent of the largest value scale, at least 0): 2^(E-34) of
+       its smallest step, 2^-25, where the largest weight is at least 2^(12-E)
+       (E: the exponent of the largest value scale, at least 0): 2^(E-37) of
        the largest weight for each token, times its |v|;
      - each logit: FP32 products and sums of at most D / 8 + 8 steps, 2^-24 of
        the largest partial sum each, and the queries' rounding (half of
