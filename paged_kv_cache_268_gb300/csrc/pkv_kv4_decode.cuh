@@ -47,6 +47,14 @@
 // as it is, 3.3e-4 at a factor of 32; their own rounding is 2.1e-4.  The 64
 // sequences of 512-4096 tokens take 123 us in all three; 256 of 1-2048, four
 // query heads a key head, 72.9, 71.7 and 71 us.)
+// What bounds it (one GB300, graph-timed; floor: K and V bytes at the measured
+// copy rate): 128 sequences of 8192 tokens, 8 kv heads, 205 us of a 201 us
+// floor, so in the steady state memory does.  A tile's instructions alone (no
+// loads) take nearly as long as its bytes (64 x 512-4096 tokens, 32 kv heads:
+// 96 us and 108; both together 121, floor 111), so what start-up and the tail
+// of unequal lengths leave idle is not caught up: 256 x 1-2048 72 us of 54,
+// 128 log-normal 62 of 40, 4 x 32768 36 of 25.  Half of the instructions are
+// the shift and ANDs of the codes, at two cycles each per SM quarter.
 #pragma once
 
 #include <cuda_fp16.h>

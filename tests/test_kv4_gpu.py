@@ -211,6 +211,29 @@ def test_decode_zero_query_averages_the_values(pkv):
     check(pkv, b)
 
 
+@pytest.mark.parametrize("scale", [-0.125, 0.0, 3.0])
+@pytest.mark.parametrize("Hq", [2, 6, 14])
+def test_decode_any_scale(pkv, scale, Hq):
+    b = batch([50, 1, 700], Hq, 2, 128, 16, torch.float16, seed=8)
+    b["scale"] = scale
+    check(pkv, b)
+
+
+@pytest.mark.parametrize("Hq,D", [(2, 64), (2, 128), (6, 128), (16, 128), (24, 64), (4, 256)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_decode_queries_that_are_no_numbers(pkv, Hq, D, bad):
+    """A NaN or infinity in one head's query makes that head NaN and no other."""
+    b = batch([50, 3], Hq, 2, D, 16, torch.float16, seed=8)
+    d = device(b)
+    good = pkv.kv4_attn_decode(**d)
+    d["q"][0, 1, D // 2 + 5] = bad
+    out = pkv.kv4_attn_decode(**d)
+    assert bool(out[0, 1].isnan().all())
+    rest = torch.ones((2, Hq), dtype=torch.bool, device="cuda")
+    rest[0, 1] = False
+    assert torch.equal(out[rest], good[rest])
+
+
 def test_decode_nan_rows_stay_in_their_sequence(pkv):
     """A cached NaN reaches its own sequence's heads and no other; a NaN past
     a sequence's end reaches nothing."""

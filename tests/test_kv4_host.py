@@ -178,6 +178,91 @@ def test_plan_refusals(lib):
         B.kv4_decode_plan(s, num_sms=0)
 
 
+def test_sizes_past_the_counters_are_refused(lib):
+    big = (1 << 30) + 1
+    assert _append(lib, "pkv_rope_append", T=big) == -3
+    assert _append(lib, "pkv_kv4_append", T=big) == -3
+    s = _shape()
+    assert lib.pkv_kv4_gather(ctypes.byref(s), FAKE, FAKE, FAKE, big, FAKE, FAKE, None) == -3
+    heads = _shape(num_kv_heads=1 << 26, num_blocks=1)
+    assert lib.pkv_kv4_gather(ctypes.byref(heads), FAKE, FAKE, FAKE, 1, FAKE, FAKE, None) == -3
+    many = _shape(num_seqs=1 << 30, num_q_heads=8, num_kv_heads=8)
+    p = B.Plan()
+    assert lib.pkv_kv4_decode_plan(ctypes.byref(many), 152, ctypes.byref(p)) == -3
+
+
+# ---------------------------------------------------------------- the planner
+def columns(D, G):
+    return 2 if G <= 2 and D > 64 else (4 if G <= 4 else 8)
+
+
+def tiles(D, G):
+    return 2 if D <= 128 and G > 8 else 1
+
+
+def resident(D, G):
+    nt = tiles(D, G)
+    if D * nt == 64 or (D * nt == 128 and columns(D, G) < 8):
+        return 4
+    return 3 if D * nt == 128 else 2
+
+
+def restated_plan(B_, Hq, Hkv, D, bs, maxL, split, sms):
+    G = Hq // Hkv
+    heads = columns(D, G) * tiles(D, G)
+    units = B_ * Hkv * -(-G // heads)
+    if split > 0:
+        P = -(-split // bs) * bs
+    else:
+        slots = sms * resident(D, G)
+        per_slot = units * maxL // slots
+        P = 2048 if per_slot >= 6000 else (1024 if per_slot >= 1000 else per_slot // 2)
+        if B_ <= 4 and 0 < units < slots:
+            S = slots // units
+            P = -(-maxL // S)
+        P = max(P, 128 if 256 < maxL <= 2048 else 256)
+        P = -(-P // 128) * 128
+        least = -(-maxL // 1024)
+        if P < least:
+            P = -(-least // 128) * 128
+    P = min(P, 256 * bs)
+    if P > maxL:
+        P = -(-maxL // bs) * bs
+    P = max(P, bs)
+    S = -(-maxL // P)
+    return P, S, units * S, (B_ * Hq * S * (4 * D + 8) if S > 1 else 0)
+
+
+@pytest.mark.parametrize("sms", [1, 16, 152])
+@pytest.mark.parametrize("D,bs", [(64, 16), (128, 32), (128, 16), (256, 16)])
+def test_plan_follows_its_rule(lib, sms, D, bs):
+    for B_ in (0, 1, 3, 4, 5, 64, 300):
+        for Hkv, G in ((1, 1), (8, 4), (32, 1), (2, 8), (8, 16), (3, 5), (1, 32)):
+            for maxL in (1, 16, 200, 256, 257, 2048, 5000, 40000):
+                for split in (0, 1, 100, 4096, 100000):
+                    s = B.make_shape(num_seqs=B_, num_q_heads=Hkv * G, num_kv_heads=Hkv, head_dim=D, block_size=bs,
+                                     num_blocks=4096, max_blocks_per_seq=-(-maxL // bs), max_context_len=maxL,
+                                     dtype=1, split_tokens=split)
+                    p = B.kv4_decode_plan(s, num_sms=sms)
+                    P, S, grid, ws = restated_plan(B_, Hkv * G, Hkv, D, bs, maxL, split, sms)
+                    assert (p.split_tokens, p.num_splits, p.grid_ctas, p.workspace_bytes) == (P, S, grid, ws)
+                    assert p.split_tokens % bs == 0 and (p.num_splits - 1) * p.split_tokens < maxL
+                    assert p.variant == 3 and p.schedule == 0 and p.warps_per_cta == 4
+
+
+def test_plan_worked_examples(lib):
+    def plan(B_, Hq, Hkv, D, bs, maxL):
+        s = B.make_shape(num_seqs=B_, num_q_heads=Hq, num_kv_heads=Hkv, head_dim=D, block_size=bs, num_blocks=65536,
+                         max_blocks_per_seq=-(-maxL // bs), max_context_len=maxL, dtype=1)
+        p = B.kv4_decode_plan(s, num_sms=152)
+        return p.split_tokens, p.num_splits, p.grid_ctas
+
+    assert plan(64, 32, 32, 128, 16, 4096) == (2048, 2, 4096)
+    assert plan(4, 64, 8, 128, 32, 32768) == (2432, 14, 448)        # one wave of three CTAs per SM
+    assert plan(256, 32, 8, 128, 16, 2048) == (2048, 1, 2048)
+    assert plan(4, 8, 8, 64, 16, 200) == (208, 1, 32)                # no split of up to 256 tokens
+
+
 # ---------------------------------------------------------------- binding refusals
 class _Cuda(torch.Tensor):
     """A host tensor that says it is on a GPU: reaches the binding's checks."""
