@@ -473,29 +473,38 @@ def _token_stride(t: torch.Tensor, name: str, heads: int, D: int, T: int, dtype)
     return t.stride(0) if T > 1 else 0
 
 
-def _append_plain(dims, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, dtype):
-    """Whether a call is the usual one (everything dense, on one GPU, as the
-    caches say): _check_append would find nothing.  A decode step makes this
-    call for every layer, so it looks at each tensor once."""
-    _, Hkv, _, D = dims
-    dev = k_cache.get_device()
-    if q is None or cos_sin is None or positions is None or dev < 0 or dtype not in _DT:
-        return False
-    ks, qs, cs = k.shape, q.shape, cos_sin.shape
-    if len(ks) != 3 or len(qs) != 3 or len(cs) != 2:
-        return False
-    T = ks[0]
-    return (ks[1] == Hkv and ks[2] == D and v.shape == ks and qs[0] == T and qs[2] == D and qs[1] > 0
-            and slot_mapping.shape == (T,) and positions.shape == (T,)
-            and q.dtype is dtype and k.dtype is dtype and v.dtype is dtype
-            and slot_mapping.dtype is torch.int32 and positions.dtype is torch.int32
-            and cos_sin.dtype is torch.float32
+_I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
+
+
+def _append_plain(kv4: bool, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache):
+    """(NB, Hkv, bs, D) of the usual call (everything dense, on one GPU, of
+    fitting sizes), of which _check_append would find nothing to refuse; else
+    None.  A decode step makes this call for every layer, so it looks at each
+    tensor once."""
+    if q is None or cos_sin is None or positions is None:
+        return None
+    dtype, dev = k.dtype, k_cache.get_device()
+    cache, ks, qs, cs = k_cache.shape, k.shape, q.shape, cos_sin.shape
+    if len(cache) != 4 or len(ks) != 3 or len(qs) != 3 or len(cs) != 2 or dev < 0 or dtype not in _DT:
+        return None
+    NB, Hkv, bs, W = cache
+    T, _, D = ks
+    one = (T,)
+    if (ks[1] == Hkv and W * 8 == D * 5 if kv4 else ks[1] == Hkv and W == D) and (
+            v_cache.shape == cache and v.shape == ks and qs[0] == T and qs[2] == D and qs[1] > 0
+            and slot_mapping.shape == one and positions.shape == one
+            and k_cache.dtype is (_U8 if kv4 else dtype) and v_cache.dtype is k_cache.dtype
+            and q.dtype is dtype and v.dtype is dtype and slot_mapping.dtype is _I32
+            and positions.dtype is _I32 and cos_sin.dtype is _F32
             and q.get_device() == dev and k.get_device() == dev and v.get_device() == dev
             and v_cache.get_device() == dev and slot_mapping.get_device() == dev
             and positions.get_device() == dev and cos_sin.get_device() == dev
             and q.is_contiguous() and k.is_contiguous() and v.is_contiguous()
+            and k_cache.is_contiguous() and v_cache.is_contiguous()
             and slot_mapping.is_contiguous() and positions.is_contiguous()
-            and cos_sin.is_contiguous())
+            and cos_sin.is_contiguous()):
+        return NB, Hkv, bs, D
+    return None
 
 
 def _check_append(dims, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out, dtype):
@@ -533,25 +542,36 @@ def _check_append(dims, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_ca
     return qs, ks, vs
 
 
-def _append(fn: str, dims, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out,
-            interleaved, stream, dtype):
-    NB, Hkv, bs, D = dims
-    qs = ks = vs = 0
-    if q_out is not None or not _append_plain(dims, q, k, v, positions, cos_sin, slot_mapping,
-                                              k_cache, v_cache, dtype):
+def _append(fn: str, kv4: bool, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache,
+            q_out, interleaved, stream):
+    dims = None
+    if q_out is None:
+        dims = _append_plain(kv4, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache)
+    if dims is not None:
+        dtype, qs, ks, vs = k.dtype, 0, 0, 0
+    else:
+        if kv4:
+            dims, dtype = _kv4_dims(k_cache, v_cache), k.dtype
+        else:
+            dims, dtype = _cache_shape(k_cache), k_cache.dtype
+            _dense(k_cache, "k_cache")
+            _dense(v_cache, "v_cache", dtype)
+            if v_cache.shape != dims:
+                raise ValueError("caches must have one shape")
         qs, ks, vs = _check_append(dims, q, k, v, positions, cos_sin, slot_mapping, k_cache,
                                    v_cache, q_out, dtype)
+    NB, Hkv, bs, D = dims
     T, dev = k.shape[0], k_cache.device
     if torch.cuda.current_device() != dev.index:
         with torch.cuda.device(dev):
-            return _append(fn, dims, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache,
-                           q_out, interleaved, stream, dtype)
+            return _append(fn, kv4, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache,
+                           q_out, interleaved, stream)
     Hq = 0 if q is None else q.shape[1]
     rows, rot = (0, 0) if cos_sin is None else cos_sin.shape
     ptr = _launch_stream(stream, dev)
     if q is not None and q_out is None:
         if stream is None:
-            q_out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
+            q_out = torch.empty_like(q) if qs == 0 else torch.empty((T, Hq, D), dtype=dtype, device=dev)
         else:
             with torch.cuda.stream(stream):
                 q_out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
@@ -582,13 +602,8 @@ def rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
     be rotated in place (q_out=q).  interleaved: pairs are neighbours, not
     halves.
     """
-    dims = _cache_shape(k_cache)
-    _dense(k_cache, "k_cache")
-    _dense(v_cache, "v_cache", k_cache.dtype)
-    if v_cache.shape != dims:
-        raise ValueError("caches must have one shape")
-    return _append("pkv_rope_append", dims, q, k, v, positions, cos_sin, slot_mapping, k_cache,
-                   v_cache, q_out, interleaved, stream, k_cache.dtype)
+    return _append("pkv_rope_append", False, q, k, v, positions, cos_sin, slot_mapping, k_cache,
+                   v_cache, q_out, interleaved, stream)
 
 
 def kv4_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
@@ -597,9 +612,8 @@ def kv4_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
                q_out: torch.Tensor | None = None, *, interleaved: bool = False,
                stream=None) -> torch.Tensor | None:
     """rope_append into 4-bit caches (kv4_cache)."""
-    dims = _kv4_dims(k_cache, v_cache)
-    return _append("pkv_kv4_append", dims, q, k, v, positions, cos_sin, slot_mapping, k_cache,
-                   v_cache, q_out, interleaved, stream, k.dtype)
+    return _append("pkv_kv4_append", True, q, k, v, positions, cos_sin, slot_mapping, k_cache,
+                   v_cache, q_out, interleaved, stream)
 
 
 def kv4_gather(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor,
@@ -609,7 +623,7 @@ def kv4_gather(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch
     [T, Hkv, D] (allocated if not given).  Rows of negative slots are zero."""
     NB, Hkv, bs, D = _kv4_dims(k_cache, v_cache)
     code = _dtype_code(dtype)
-    _dense(slot_mapping, "slot_mapping", torch.int32)
+    _dense(slot_mapping, "slot_mapping", _I32)
     if slot_mapping.dim() != 1:
         raise ValueError("slot_mapping must be [T]")
     T = slot_mapping.shape[0]
