@@ -41,6 +41,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// Smallest and largest, NaN where one is; of three in one instruction.
 __device__ __forceinline__ float min_nan(float a, float b) {
   float r;
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -49,6 +50,16 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -85,12 +96,8 @@ __device__ __forceinline__ float quotient(float a, float b, float y) {
 // and is at least 1/1024 of its largest magnitude so that the zero point keeps
 // a fraction of a step in binary16.
 __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], __half* scale, __half* zero) {
-  float lo = x[0], hi = x[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    lo = min_nan(lo, x[i]);
-    hi = max_nan(hi, x[i]);
-  }
+  float lo = min_nan(min_nan(x[0], x[1], x[2]), min_nan(x[3], x[4], x[5]), min_nan(x[6], x[7]));
+  float hi = max_nan(max_nan(x[0], x[1], x[2]), max_nan(x[3], x[4], x[5]), max_nan(x[6], x[7]));
 #pragma unroll
   for (int m = 1; m <= 2; m <<= 1) {
     lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, m));
@@ -106,15 +113,25 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], __half* scale
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
   y = fmaf(fmaf(-s, y, 1.f), y, y);
-  const __half z = __float2half_rn(fminf(fmaxf(quotient(lo, s, y), -65504.f), 65504.f));
+  const float low = quotient(lo, s, y);
+  const __half z = __float2half_rn(fminf(fmaxf(low, -65504.f), 65504.f));
   const float zf = __half2float(z);
+  // 1.5 * 2^23 more rounds to a whole number, ties to even, in the low bits.
+  // The codes' order is the values', so where lo's and hi's are within 0 .. 15
+  // all are; the scale and zero point see to that but where z is large and
+  // rounded by up to half a step, or the scale is at its end.
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __fsub_rn(quotient(x[i], s, y), zf);
+  const bool within = __fsub_rn(low, zf) >= -0.5f && __fsub_rn(quotient(hi, s, y), zf) < 15.5f;
+  if (__any_sync(0xffffffffu, !within)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(v[i], 0.f), 15.f);
+  }
   uint32_t w = 0;
 #pragma unroll
-  for (int i = 7; i >= 0; --i) {
-    const float v = fminf(fmaxf(__fsub_rn(quotient(x[i], s, y), zf), 0.f), 15.f);
-    // 1.5 * 2^23 more rounds to a whole number, ties to even, in the low bits
-    w = w * 16u + (__float_as_uint(__fadd_rn(v, 12582912.f)) - 0x4b400000u);
-  }
+  for (int i = 7; i >= 0; --i) w = w * 16u + __float_as_uint(__fadd_rn(v[i], 12582912.f));
+  w -= 0x3f400000u;   // the sum of 0x4b400000 * 16^i, which the eight roundings brought with them
   *scale = finite ? h : __ushort_as_half(0x7e00);   // an infinity or NaN: the group reads as NaN
   *zero = finite ? z : __ushort_as_half(0x7e00);
   return finite ? w : 0u;
@@ -131,13 +148,19 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], __half* scale
 // half-split partner chunk from shared memory (so queries may be rotated in
 // place).  The four lanes of 32 channels agree on the scale by shuffles.
 // Measured on one GB300, 8192 tokens of 32 + 2 x 8 bfloat16 heads of 128 (206 MB
-// in and out): 34.4 us, 5.98 TB/s, 0.89 of a copy; lanes that fetched their own
+// in and out): 33.5 us, 6.1 TB/s, 0.91 of a copy; lanes that fetched their own
 // chunks (16-byte asynchronous copies, six ahead) took 50 us and 210
-// instructions a chunk, against 116.  Four stages 35.2 us, 128 threads 40 us.
-// Into the 4-bit cache, 2047 tokens of 32 + 2 x 32 binary16 heads (78 MB):
-// 24.7 us, 0.47 of a copy, bound by the instructions of the codes (a division
-// per channel in place of `quotient`: 29.6 us).
-constexpr int kStages = 3;
+// instructions a chunk, against 116.  Three CTAs per SM 34.6 us, half of the
+// threads 40, slices of 8 KB 49.  Into the 4-bit cache, 2047 tokens of 32 + 2 x
+// 32 binary16 heads (78 MB): 22.6 us, 0.51 of a copy, bound by the instructions
+// of the codes (two thirds of the issue slots) and by 2047 tokens on 608 CTAs;
+// 24.5 with slices of 16 KB, 29.6 with a division per channel in place of
+// `quotient`.  A warp of its own for the fetching, with barriers both ways:
+// 34.3 and 22.6 us, and 0.1-0.2 us more for a few tokens.
+constexpr int kStages = 2;
+
+constexpr int kSliceBytes = 24576;   // a slice's rows at most
+constexpr int kAppendCtas = 4;       // per SM
 
 struct TokenMeta {
   int slot;    // where k and v go, -1: nowhere
@@ -145,7 +168,7 @@ struct TokenMeta {
 };
 
 template <bool BF, int D, bool KV4>
-__global__ void __launch_bounds__(kThreads, 3) rope_append_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int LPR = D / 8;              // lanes per row
   constexpr int R = kThreads / LPR;       // rows per pass
   constexpr int ROW = D * 2;              // bytes
@@ -417,7 +440,7 @@ cudaError_t raise_smem(const void* kern, bool kv4, bool bf, int D) {
   if (e != cudaSuccess) return e;
   const unsigned bit = dev < 32 ? 1u << dev : 0u;
   if (bit != 0 && (mask.load(std::memory_order_acquire) & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kStages * (16384 + 1024));
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kStages * (kSliceBytes + 1024));
   if (e == cudaSuccess) mask.fetch_or(bit, std::memory_order_release);
   return e;
 }
@@ -482,11 +505,11 @@ int append(const pkv_shape* s, const pkv_rope* rope, const void* q, const void* 
   int sms = 0;
   rc = device_sms(&sms);
   if (rc != PKV_OK) return rc;
-  // Three CTAs per SM walk the tokens.  A slice has at most 16 KB of rows (three
-  // CTAs of four stages fit an SM's shared memory), and fewer where there are
+  // kAppendCtas CTAs per SM walk the tokens.  A slice has at most 24 KB of rows
+  // (the CTAs' stages fit an SM's shared memory), and fewer where there are
   // not tokens enough for every CTA: down to one pass of the CTA's threads.
-  const int pass = kThreads / (D / 8), all = a.Hq + 2 * a.Hkv, most = 16384 / (D * 2);
-  const int resident = 3 * sms;
+  const int pass = kThreads / (D / 8), all = a.Hq + 2 * a.Hkv, most = kSliceBytes / (D * 2);
+  const int resident = kAppendCtas * sms;
   long long slices = (all + most - 1) / most;
   if (num_tokens * slices < resident) {
     slices = resident / num_tokens;
