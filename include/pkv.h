@@ -381,7 +381,12 @@ int pkv_kv4_attn_decode(const pkv_shape* shape, const void* q, const void* k_cac
                         void* workspace, size_t workspace_bytes, pkv_stream_t stream);
 
 /* How pkv_kv4_attn_decode will run on the current device, or, with num_sms >
- * 0, on a device with that many SMs (host only then).  plan->variant is 3. */
+ * 0, on a device with that many SMs (host only then).  plan->variant is 3.
+ * With the automatic choice (shape->split_tokens = 0), where partitions are
+ * 1024 tokens or more and there are more than four sequences, the last eighth
+ * of the sequences is cut into partitions of 512 tokens instead (more past
+ * 524288 tokens): split_tokens and num_splits are those of the others, and
+ * grid_ctas and workspace_bytes count both. */
 int pkv_kv4_decode_plan(const pkv_shape* shape, int32_t num_sms, pkv_plan* plan);
 
 /* Workspace bytes pkv_kv4_attn_decode needs for `shape` (0 if none). */

@@ -51,9 +51,9 @@
 // copy rate): 128 sequences of 8192 tokens, 8 kv heads, 205 us of a 201 us
 // floor, so in the steady state memory does.  A tile's instructions alone (no
 // loads) take nearly as long as its bytes (64 x 512-4096 tokens, 32 kv heads:
-// 96 us and 108; both together 121, floor 111), so what start-up and the tail
-// of unequal lengths leave idle is not caught up: 256 x 1-2048 72 us of 54,
-// 128 log-normal 62 of 40, 4 x 32768 36 of 25.  Half of the instructions are
+// 96 us and 108; both together 117, floor 111), so what start-up and the tail
+// of unequal lengths leave idle is not caught up: 256 x 1-2048 69 us of 54,
+// 128 log-normal 56 of 40, 4 x 32768 36 of 25.  Half of the instructions are
 // the shift and ANDs of the codes, at two cycles each per SM quarter.
 #pragma once
 
@@ -73,6 +73,11 @@ struct Kv4Args {
   const uint8_t* k;     // [NB, Hkv, tile]
   const uint8_t* v;
   int chunks;           // query-head chunks per kv head
+  // The sequences from `late` on, dispatched last, are cut into partitions of
+  // P2 tokens, S2 of them (d.P and d.S for those before): see the host's rule.
+  int late, P2, S2;
+  int early_ctas;       // CTAs of the sequences before `late`
+  size_t late_part;     // partials of those sequences
 };
 
 constexpr int kKv4Warps = 4;
@@ -599,6 +604,12 @@ struct Kv4Compute {
   }
 };
 
+// First partial of output row `row` (sequence seq).
+__device__ __forceinline__ size_t kv4_partial(const Kv4Args& p, int seq, size_t row) {
+  return seq < p.late ? row * p.d.S
+                      : p.late_part + (row - static_cast<size_t>(p.late) * p.d.Hq) * p.S2;
+}
+
 template <bool BF, int D, int BS, int HC, int NT>
 __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas(D, HC, NT)) kv4_decode_kernel(const __grid_constant__ Kv4Args p) {
   using Compute = Kv4Compute<BF, D, BS, HC, NT>;
@@ -615,12 +626,15 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas(D, HC, NT)) kv4_decod
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int idx = blockIdx.x;
-  const int split = idx % a.S;
-  idx /= a.S;
+  const bool late = idx >= p.early_ctas;
+  if (late) idx -= p.early_ctas;
+  const int P = late ? p.P2 : a.P, S = late ? p.S2 : a.S;
+  const int split = idx % S;
+  idx /= S;
   const int chunk = idx % p.chunks;
   idx /= p.chunks;
   const int kvh = idx % a.Hkv;
-  const int seq = idx / a.Hkv;
+  const int seq = idx / a.Hkv + (late ? p.late : 0);
   const int heads = min(NH, a.G - chunk * NH);          // of this CTA
   const int h0 = kvh * a.G + chunk * NH;                // the first of them
   // resident before the stream's previous kernel is done; nothing is read before it is
@@ -629,11 +643,11 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas(D, HC, NT)) kv4_decod
 
   // block ids of the partition, range-checked; the first partition's are
   // loaded together with the length (it is empty only for padding rows)
-  const int t0 = split * a.P, j0 = t0 / BS;
+  const int t0 = split * P, j0 = t0 / BS;
   const int32_t* trow = a.block_tables + static_cast<size_t>(seq) * a.MB + j0;
   const int L = a.context_lens[seq];
   if (split == 0)
-    for (int k = threadIdx.x; k < min(a.P / BS, a.MB - j0); k += NW * 32) ids[k] = __ldg(trow + k);
+    for (int k = threadIdx.x; k < min(P / BS, a.MB - j0); k += NW * 32) ids[k] = __ldg(trow + k);
   if (L < 0 || L > a.max_ctx) {
     if (threadIdx.x == 0 && split == 0 && kvh == 0 && chunk == 0) record_error(a.err, kDevBadContext);
     return;
@@ -645,7 +659,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas(D, HC, NT)) kv4_decod
     return;
   }
   if (t0 >= L) return;
-  const int t1 = min(t0 + a.P, L);
+  const int t1 = min(t0 + P, L);
   const int nblk = (t1 - t0 + BS - 1) / BS;
   bool bad = false;
   for (int k = threadIdx.x; k < nblk; k += NW * 32) {
@@ -722,7 +736,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas(D, HC, NT)) kv4_decod
   float* cl = cm + NW * NH;
   cs.publish(cm + warp * NH, cl + warp * NH, co + warp * NH * kv4_row(D), lane);
   __syncthreads();
-  const bool single = (L + a.P - 1) / a.P == 1;
+  const bool single = (L + P - 1) / P == 1;
   for (int i = threadIdx.x; i < heads * (D / 4); i += NW * 32) {
     const int h = i / (D / 4), d = i % (D / 4) * 4;
     float M = -INFINITY;
@@ -745,15 +759,79 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas(D, HC, NT)) kv4_decod
       *reinterpret_cast<uint2*>(a.out + row * D + d) =
           make_uint2(pack2<BF>(x[0] * r, x[1] * r), pack2<BF>(x[2] * r, x[3] * r));
     } else {
-      const size_t pr = row * a.S + split;
+      const size_t pr = kv4_partial(p, seq, row) + split;
       *reinterpret_cast<float4*>(a.part_o + pr * D + d) = make_float4(x[0], x[1], x[2], x[3]);
       if (d == 0) a.part_ml[pr] = make_float2(M, lsum);
     }
   }
 }
 
+// Cross-split reduce: one warp per output row of more than one partition; rows
+// of sequences that all have one are not in the grid.  M = max m, w = 2^(m - M),
+// out = sum w o / sum w l in the order of the partitions.  A lane owns D / 32
+// elements and has the loads of eight partials in flight, the first of them
+// together with those of m.
+template <bool BF, int D>
+__global__ void __launch_bounds__(128) kv4_reduce_kernel(const __grid_constant__ Kv4Args p, int row0) {
+  constexpr int OPL = D / 32, J = 8;
+  pdl_launch_dependents();
+  const DecodeArgs& a = p.d;
+  const int lane = threadIdx.x & 31;
+  const long long row = row0 + blockIdx.x * 4ll + (threadIdx.x >> 5);
+  int n = 0, seq = 0;
+  if (row < static_cast<long long>(a.B) * a.Hq) {
+    seq = static_cast<int>(row / a.Hq);
+    const int L = a.context_lens[seq];   // written before the decode grid began
+    const int P = seq < p.late ? a.P : p.P2;
+    if (L >= 1 && L <= a.max_ctx) n = (L + P - 1) / P;
+  }
+  pdl_wait();
+  if (n <= 1) return;
+  const size_t first = kv4_partial(p, seq, row);
+  const float2* ml = a.part_ml + first;
+  const float* po = a.part_o + first * D + lane * OPL;
+  float x[J][OPL], acc[OPL], lsum = 0.f;
+  float2 y[J];
+  auto load = [&](int j0) {
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (j0 + j < n) {
+        y[j] = __ldcg(ml + j0 + j);
+#pragma unroll
+        for (int e = 0; e < OPL; e += 2) {
+          const float2 t = __ldcg(reinterpret_cast<const float2*>(po + static_cast<size_t>(j0 + j) * D + e));
+          x[j][e] = t.x;
+          x[j][e + 1] = t.y;
+        }
+      }
+  };
+  load(0);
+  float M = -INFINITY;
+  for (int j = lane; j < n; j += 32) M = fmaxf(M, __ldcg(ml + j).x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll
+  for (int e = 0; e < OPL; ++e) acc[e] = 0.f;
+  for (int j0 = 0; j0 < n; j0 += J) {
+    if (j0 > 0) load(j0);
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (j0 + j < n) {
+        const float w = fast_exp2(y[j].x - M);
+        lsum = fmaf(w, y[j].y, lsum);
+#pragma unroll
+        for (int e = 0; e < OPL; ++e) acc[e] = fmaf(w, x[j][e], acc[e]);
+      }
+  }
+  const float r = 1.f / lsum;
+  uint16_t* out = a.out + static_cast<size_t>(row) * D + lane * OPL;
+#pragma unroll
+  for (int e = 0; e < OPL; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack2<BF>(acc[e] * r, acc[e + 1] * r);
+}
+
 // Launch for one element type (pkv_kv4_inst.cu, compiled once per type).
-cudaError_t launch_kv4_f16(const Kv4Args&, int head_dim, int block_size, unsigned grid, cudaStream_t);
-cudaError_t launch_kv4_bf16(const Kv4Args&, int head_dim, int block_size, unsigned grid, cudaStream_t);
+// With `reduce`, the cross-split reduce behind it.
+cudaError_t launch_kv4_f16(const Kv4Args&, int head_dim, int block_size, unsigned grid, bool reduce, cudaStream_t);
+cudaError_t launch_kv4_bf16(const Kv4Args&, int head_dim, int block_size, unsigned grid, bool reduce, cudaStream_t);
 
 }  // namespace pkv

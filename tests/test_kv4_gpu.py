@@ -179,6 +179,31 @@ def test_decode_lengths_and_splits(pkv, lens, split):
               max_context_len=max(max(lens), 1))
 
 
+@pytest.mark.parametrize("B,max_len,Hq,D,bs,splits", [(75, 1024, 8, 128, 16, (1024, 1)), (75, 1600, 16, 64, 32, (1024, 2)),
+                                                      (40, 2048, 72, 128, 16, (1024, 2))])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_decode_whose_last_sequences_are_cut_finer(pkv, B, max_len, Hq, D, bs, splits, dtype):
+    """Both regions of the grid with lengths at their partitions' edges, empty
+    sequences, one partition and several; nothing outside the workspace."""
+    last = -(-B // 8)
+    edge = [0, 1, 511, 512, 513, 1023, 1024, max_len - 1, max_len]
+    lens = [edge[i % 9] if i % 5 == 0 else i for i in range(B - last)]
+    lens += [edge[(4 * i + 8) % 9] for i in range(last)]
+    b = batch(lens, Hq, 8, D, bs, dtype, seed=B)
+    d = device(b)
+    shape = pkv.kv4_decode_shape(d["q"], d["k_cache"], d["block_tables"], max_len)
+    p = pkv.kv4_decode_plan(shape)
+    assert (p.split_tokens, p.num_splits) == splits
+    assert p.grid_ctas % 8 == 0 and p.grid_ctas > B * 8 * p.num_splits
+    n = pkv.kv4_workspace_bytes(shape)
+    ws = torch.full((n + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+    got = check(pkv, b, d, max_context_len=max_len, workspace=ws[4096:4096 + n])
+    assert bool((ws[:4096] == 0xA5).all()) and bool((ws[4096 + n:] == 0xA5).all())
+    assert torch.equal(got, pkv.kv4_attn_decode(**d, max_context_len=max_len))
+    one = check(pkv, b, d, max_context_len=max_len, split_tokens=p.split_tokens)
+    assert torch.equal(got[:B - last], one[:B - last])
+
+
 @pytest.mark.parametrize("k_mul,v_mul,v_add", [(1, 1e-4, 0), (1, 6000, 0), (1, 1, 300), (1, 1e-7, 0), (30, 1, 0),
                                                (1e-3, 1, 0), (1, 3, -2e4)])
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])

@@ -230,7 +230,13 @@ def restated_plan(B_, Hq, Hkv, D, bs, maxL, split, sms):
         P = -(-maxL // bs) * bs
     P = max(P, bs)
     S = -(-maxL // P)
-    return P, S, units * S, (B_ * Hq * S * (4 * D + 8) if S > 1 else 0)
+    last, S2 = 0, S                      # the sequences dispatched last, finer
+    if split == 0 and P >= 1024 and B_ > 4:
+        last = -(-B_ // 8)
+        S2 = -(-maxL // max(512, -(-least // 128) * 128))
+    grid = units // B_ * ((B_ - last) * S + last * S2) if B_ else 0
+    rows = (B_ - last) * S * (S > 1) + last * S2 * (S2 > 1)
+    return P, S, grid, rows * Hq * (4 * D + 8)
 
 
 @pytest.mark.parametrize("sms", [1, 16, 152])
@@ -238,7 +244,7 @@ def restated_plan(B_, Hq, Hkv, D, bs, maxL, split, sms):
 def test_plan_follows_its_rule(lib, sms, D, bs):
     for B_ in (0, 1, 3, 4, 5, 64, 300):
         for Hkv, G in ((1, 1), (8, 4), (32, 1), (2, 8), (8, 16), (3, 5), (1, 32)):
-            for maxL in (1, 16, 200, 256, 257, 2048, 5000, 40000):
+            for maxL in (1, 16, 200, 256, 257, 1100, 2048, 5000, 40000, 700001):
                 for split in (0, 1, 100, 4096, 100000):
                     s = B.make_shape(num_seqs=B_, num_q_heads=Hkv * G, num_kv_heads=Hkv, head_dim=D, block_size=bs,
                                      num_blocks=4096, max_blocks_per_seq=-(-maxL // bs), max_context_len=maxL,
@@ -257,9 +263,9 @@ def test_plan_worked_examples(lib):
         p = B.kv4_decode_plan(s, num_sms=152)
         return p.split_tokens, p.num_splits, p.grid_ctas
 
-    assert plan(64, 32, 32, 128, 16, 4096) == (2048, 2, 4096)
+    assert plan(64, 32, 32, 128, 16, 4096) == (2048, 2, 56 * 64 + 8 * 256)
     assert plan(4, 64, 8, 128, 32, 32768) == (2432, 14, 448)        # one wave of three CTAs per SM
-    assert plan(256, 32, 8, 128, 16, 2048) == (2048, 1, 2048)
+    assert plan(256, 32, 8, 128, 16, 2048) == (2048, 1, 224 * 8 + 32 * 32)
     assert plan(4, 8, 8, 64, 16, 200) == (208, 1, 32)                # no split of up to 256 tokens
 
 
