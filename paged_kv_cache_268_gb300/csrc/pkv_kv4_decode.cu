@@ -77,10 +77,12 @@ int kv4_plan(const pkv_shape* s, int sms, pkv_plan* plan, Late* late) {
     // (71.5), 64 x 512-4096 with 32 heads 116.8 (120.8), 64 x 1-4096 37.8
     // (39.7).  A quarter of the sequences: 56.7, 69.6, 119.9; 256 tokens: 59.1,
     // 69.6, 123.8.
+    late->first = s->num_seqs - (s->num_seqs - 1) / 8 - 1;
     const long long pmin = (static_cast<long long>(maxL) + 1023) / 1024;
-    late->first = s->num_seqs - (s->num_seqs + 7) / 8;
-    late->P = pmin <= 512 ? 512 : static_cast<int>((pmin + gran - 1) / gran * gran);
-    late->S = (maxL + late->P - 1) / late->P;
+    long long P2 = pmin <= 512 ? 512 : (pmin + gran - 1) / gran * gran;
+    if (P2 > P) P2 = P;
+    late->P = static_cast<int>(P2);
+    late->S = static_cast<int>((maxL + P2 - 1) / P2);
   }
   const long long per_split = static_cast<long long>(s->num_kv_heads) * kv4_chunks(s);
   const long long first = late->first, rest = s->num_seqs - late->first;

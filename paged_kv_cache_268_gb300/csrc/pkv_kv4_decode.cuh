@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas(D, HC, NT)) kv4_decod
     return;
   }
   if (t0 >= L) return;
-  const int t1 = min(t0 + P, L);
+  const int t1 = L - t0 < P ? L : t0 + P;
   const int nblk = (t1 - t0 + BS - 1) / BS;
   bool bad = false;
   for (int k = threadIdx.x; k < nblk; k += NW * 32) {
@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, kv4_ctas(D, HC, NT)) kv4_decod
   float* cl = cm + NW * NH;
   cs.publish(cm + warp * NH, cl + warp * NH, co + warp * NH * kv4_row(D), lane);
   __syncthreads();
-  const bool single = (L + P - 1) / P == 1;
+  const bool single = L <= P;
   for (int i = threadIdx.x; i < heads * (D / 4); i += NW * 32) {
     const int h = i / (D / 4), d = i % (D / 4) * 4;
     float M = -INFINITY;
@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(128) kv4_reduce_kernel(const __grid_constant__
     seq = static_cast<int>(row / a.Hq);
     const int L = a.context_lens[seq];   // written before the decode grid began
     const int P = seq < p.late ? a.P : p.P2;
-    if (L >= 1 && L <= a.max_ctx) n = (L + P - 1) / P;
+    if (L >= 1 && L <= a.max_ctx) n = (L - 1) / P + 1;
   }
   pdl_wait();
   if (n <= 1) return;

@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(cons
             }
           }
         } else {
-          uint16_t* dst = static_cast<uint16_t*>(is_v ? a.v_cache : a.k_cache) + static_cast<size_t>((block + h) * a.bs + r) * D + c * 8;
+          uint16_t* dst = static_cast<uint16_t*>(is_v ? a.v_cache : a.k_cache) + (static_cast<size_t>(block + h) * a.bs + r) * D + c * 8;
           *reinterpret_cast<uint4*>(dst) = is_v ? raw : pack8<BF>(x);
         }
       }

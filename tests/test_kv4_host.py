@@ -233,7 +233,7 @@ def restated_plan(B_, Hq, Hkv, D, bs, maxL, split, sms):
     last, S2 = 0, S                      # the sequences dispatched last, finer
     if split == 0 and P >= 1024 and B_ > 4:
         last = -(-B_ // 8)
-        S2 = -(-maxL // max(512, -(-least // 128) * 128))
+        S2 = -(-maxL // min(P, max(512, -(-least // 128) * 128)))
     grid = units // B_ * ((B_ - last) * S + last * S2) if B_ else 0
     rows = (B_ - last) * S * (S > 1) + last * S2 * (S2 > 1)
     return P, S, grid, rows * Hq * (4 * D + 8)
@@ -254,6 +254,23 @@ def test_plan_follows_its_rule(lib, sms, D, bs):
                     assert (p.split_tokens, p.num_splits, p.grid_ctas, p.workspace_bytes) == (P, S, grid, ws)
                     assert p.split_tokens % bs == 0 and (p.num_splits - 1) * p.split_tokens < maxL
                     assert p.variant == 3 and p.schedule == 0 and p.warps_per_cta == 4
+
+
+@pytest.mark.parametrize("maxL", [600_000, 4_194_304, 5_000_000, 100_000_000, 2 ** 31 - 16])
+@pytest.mark.parametrize("bs", [16, 32])
+def test_plan_of_very_long_contexts(lib, maxL, bs):
+    """A partition's block ids always fit its CTA (256), whatever the length."""
+    for B_ in (1, 5, 8):
+        s = B.make_shape(num_seqs=B_, num_q_heads=4, num_kv_heads=1, head_dim=128, block_size=bs, num_blocks=4096,
+                         max_blocks_per_seq=-(-maxL // bs), max_context_len=maxL, dtype=1)
+        p = B.kv4_decode_plan(s, num_sms=152)
+        P, S, grid, ws = restated_plan(B_, 4, 1, 128, bs, maxL, 0, 152)
+        assert (p.split_tokens, p.num_splits, p.grid_ctas, p.workspace_bytes) == (P, S, grid, ws)
+        last = -(-B_ // 8) if B_ > 4 else 0
+        assert p.split_tokens <= 256 * bs
+        if last:
+            late = (p.grid_ctas - (B_ - last) * S) // last
+            assert late * 256 * bs >= maxL and late >= S
 
 
 def test_plan_worked_examples(lib):
