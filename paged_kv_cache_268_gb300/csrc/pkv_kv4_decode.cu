@@ -37,7 +37,8 @@ int kv4_plan(const pkv_shape* s, int sms, pkv_plan* plan, Late* late) {
   } else {
     // Tokens per resident CTA if every sequence were of the largest length.
     // Measured on one GB300 over batches of 1 to 128 sequences (uniform and
-    // log-normal lengths, 8 and 32 kv heads, head_dim 64 to 256):
+    // log-normal lengths, 8 and 32 kv heads, head_dim 64 to 256), one size for
+    // all sequences:
     //  - from 6000 on, 2048-token partitions (64 x 512-4096 tokens, 32 heads:
     //    123 us, 126 at 1024), from 1000 on, 1024 (64 x 1-4096, 8 heads: 40 us,
     //    43 at 2048 or 512), below, half of it;

@@ -349,16 +349,17 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(cons
 // Rows of the 4-bit cache back in 16 bits.  value = scale * (code + zero) in
 // FP32 (the sum is exact), one rounding at the store.  Rows of a negative or
 // bad slot become zeros.  The D/8 lanes of a row hold one chunk each; a CTA
-// takes two tokens (whose value parameters share bytes) and kLoops passes over
-// their head rows.  Bound by memory: three of its four bytes are written.
-// Measured on one GB300, 32768 rows of 8 bfloat16 heads of 128 (176 MB in and
-// out): 33.7 us, 5.24 TB/s, 0.78 of a copy; 256 threads 38.5 us, one pass a CTA
-// 37.1, CTAs that walk all pairs with the next one's bytes in flight 32.7-38.
+// takes TOK tokens and LOOPS passes over their head rows, all of whose bytes
+// it asks for before it works on the first.  Bound by memory: three of its four
+// bytes are written.  Measured on one GB300, 32768 rows of 8 bfloat16 heads of
+// 128 (176 MB in and out): 29.8 us, 5.9 TB/s, 0.88 of a copy, with four tokens
+// and one pass (31.2 with two and two, 33.7 when a pass waited for the one
+// before, 58 with 64-bit divisions and one load at a time; 256 threads 35.4,
+// 64 30.1, eight tokens 30.5).  Small calls want more CTAs: 1999 rows 3.3 us
+// with two tokens, 3.4 with four; 128 rows of 32 + 32 heads 1.9 and 2.3.
 constexpr int kGatherThreads = 128;
-constexpr int kTokens = 2;
-constexpr int kLoops = 2;
 
-template <bool BF, int D, int BS>
+template <bool BF, int D, int BS, int TOK, int LOOPS>
 __global__ void __launch_bounds__(kGatherThreads)
     kv4_gather_kernel(const uint8_t* __restrict__ k_cache, const uint8_t* __restrict__ v_cache,
                       const int32_t* __restrict__ slots, uint16_t* __restrict__ k,
@@ -368,12 +369,12 @@ __global__ void __launch_bounds__(kGatherThreads)
   constexpr uint32_t TILE = kv4_tile_bytes(D, BS);
   pdl_wait();
   pdl_launch_dependents();
-  const int t0 = blockIdx.x * kTokens;
+  const int t0 = blockIdx.x * TOK;
   const int c = threadIdx.x % LPR, g = c >> 2;
-  uint32_t block[kTokens];   // first tile of the slot's block
-  int row[kTokens];
+  uint32_t block[TOK];   // first tile of the slot's block
+  int row[TOK];
 #pragma unroll
-  for (int i = 0; i < kTokens; ++i) {
+  for (int i = 0; i < TOK; ++i) {
     row[i] = -1;
     if (t0 + i < T) {
       const int slot = __ldg(slots + t0 + i);
@@ -385,47 +386,64 @@ __global__ void __launch_bounds__(kGatherThreads)
       }
     }
   }
-  const int last = min(2 * Hkv, R * kLoops * static_cast<int>(blockIdx.y + 1));
-  for (int u = R * kLoops * blockIdx.y + threadIdx.x / LPR; u < last; u += R) {
+  const int last = min(2 * Hkv, R * LOOPS * static_cast<int>(blockIdx.y + 1));
+  const int u0 = R * LOOPS * blockIdx.y + threadIdx.x / LPR;
+  // all of the CTA's bytes first, so that their latencies overlap
+  uint32_t w[LOOPS][TOK], par[LOOPS][TOK];
+#pragma unroll
+  for (int j = 0; j < LOOPS; ++j) {
+    const int u = u0 + j * R;
     const bool is_v = u >= Hkv;
     const int h = is_v ? u - Hkv : u;
     const uint8_t* cache = is_v ? v_cache : k_cache;
-    uint32_t w[kTokens], par[kTokens];
 #pragma unroll
-    for (int i = 0; i < kTokens; ++i) {
-      w[i] = par[i] = 0;                         // a padding row: scale 0, all zeros
-      if (row[i] < 0) continue;
+    for (int i = 0; i < TOK; ++i) {
+      w[j][i] = par[j][i] = 0;                   // a padding row: scale 0, all zeros
+      if (row[i] < 0 || u >= last) continue;
       const uint8_t* base = cache + static_cast<size_t>(block[i] + h) * TILE;
-      w[i] = __ldg(reinterpret_cast<const uint32_t*>(base + kv4_code_off<D>(row[i], g) + (c & 3) * 4));
+      w[j][i] = __ldg(reinterpret_cast<const uint32_t*>(base + kv4_code_off<D>(row[i], g) + (c & 3) * 4));
       if (is_v) {
         const uint8_t* p = base + kv4_v_par_off<D>(BS, row[i], g);
-        par[i] = __ldg(reinterpret_cast<const uint16_t*>(p)) |
-                 static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p + 4))) << 16;
+        par[j][i] = __ldg(reinterpret_cast<const uint16_t*>(p)) |
+                    static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p + 4))) << 16;
       } else {
-        par[i] = __ldg(reinterpret_cast<const uint32_t*>(base + kv4_k_par_off<D>(BS, row[i], g)));
+        par[j][i] = __ldg(reinterpret_cast<const uint32_t*>(base + kv4_k_par_off<D>(BS, row[i], g)));
       }
     }
-    uint16_t* dst = (is_v ? v : k) + (static_cast<size_t>(t0) * Hkv + h) * D + c * 8;
+  }
 #pragma unroll
-    for (int i = 0; i < kTokens; ++i) {
+  for (int j = 0; j < LOOPS; ++j) {
+    const int u = u0 + j * R;
+    if (u >= last) break;
+    const bool is_v = u >= Hkv;
+    uint16_t* dst = (is_v ? v : k) + (static_cast<size_t>(t0) * Hkv + (is_v ? u - Hkv : u)) * D + c * 8;
+#pragma unroll
+    for (int i = 0; i < TOK; ++i) {
       if (t0 + i >= T) break;
-      const float2 p = unpack2<false>(par[i]);
+      const float2 p = unpack2<false>(par[j][i]);
       float x[8];
-      // nibbles j and j + 4 as binary16 subnormals, n * 2^-24; n + z and 2^24 (n 2^-24) are exact
+      // nibbles e and e + 4 as binary16 subnormals, n * 2^-24; n + z and 2^24 (n 2^-24) are exact
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 n = unpack2<false>((w[i] >> (4 * j)) & 0x000f000fu);
-        x[j] = p.x * fmaf(n.x, 0x1p24f, p.y);
-        x[j + 4] = p.x * fmaf(n.y, 0x1p24f, p.y);
+      for (int e = 0; e < 4; ++e) {
+        const float2 n = unpack2<false>((w[j][i] >> (4 * e)) & 0x000f000fu);
+        x[e] = p.x * fmaf(n.x, 0x1p24f, p.y);
+        x[e + 4] = p.x * fmaf(n.y, 0x1p24f, p.y);
       }
       *reinterpret_cast<uint4*>(dst + static_cast<size_t>(i) * Hkv * D) = pack8<BF>(x);
     }
   }
 }
 
-template <bool BF, int D>
+template <int TOK, int LOOPS, bool BF, int D>
 auto gather_kernel(int bs) {
-  return bs == 32 ? kv4_gather_kernel<BF, D, 32> : kv4_gather_kernel<BF, D, 16>;
+  return bs == 32 ? kv4_gather_kernel<BF, D, 32, TOK, LOOPS> : kv4_gather_kernel<BF, D, 16, TOK, LOOPS>;
+}
+template <int TOK, int LOOPS>
+auto gather_kernel(bool bf, int D, int bs) {
+  auto kern = bf ? gather_kernel<TOK, LOOPS, true, 64>(bs) : gather_kernel<TOK, LOOPS, false, 64>(bs);
+  if (D == 128) kern = bf ? gather_kernel<TOK, LOOPS, true, 128>(bs) : gather_kernel<TOK, LOOPS, false, 128>(bs);
+  if (D == 256) kern = bf ? gather_kernel<TOK, LOOPS, true, 256>(bs) : gather_kernel<TOK, LOOPS, false, 256>(bs);
+  return kern;
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -566,18 +584,23 @@ extern "C" int pkv_kv4_gather(const pkv_shape* s, const void* k_cache, const voi
       !aligned(slot_mapping, 4))
     return PKV_ERR_ALIGN;
   const int D = s->head_dim;
-  const int rows = kGatherThreads / (D / 8) * kLoops;    // of a CTA
-  const long long slices = (2ll * s->num_kv_heads - 1) / rows + 1;
-  if (num_tokens > (1 << 30) || slices > 65535) return PKV_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>((num_tokens - 1) / kTokens + 1),
-                  static_cast<unsigned>(slices));
+  const int rows = kGatherThreads / (D / 8);             // of a pass
+  const long long passes = (2ll * s->num_kv_heads - 1) / rows + 1;
+  if (num_tokens > (1 << 30) || passes > 65535) return PKV_ERR_UNSUPPORTED;
+  int sms = 0;
+  rc = device_sms(&sms);
+  if (rc != PKV_OK) return rc;
+  // Four tokens a CTA where that leaves 32 CTAs for every SM, two resident
+  // waves (measured equal at 27, 2047 rows of 32 heads: 10.7 us both; figures
+  // beyond and below at the kernel).
+  const bool many = (num_tokens / 4) * passes >= 32ll * sms;
+  const int tokens = many ? 4 : 2, loops = many ? 1 : 2;
+  const dim3 grid(static_cast<unsigned>((num_tokens - 1) / tokens + 1),
+                  static_cast<unsigned>((passes + loops - 1) / loops));
   int* err = device_error_word();
   if (!err) return PKV_ERR_CUDA;
   const bool bf = s->dtype == PKV_BF16;
-  const int bs = s->block_size;
-  auto kern = bf ? gather_kernel<true, 64>(bs) : gather_kernel<false, 64>(bs);
-  if (D == 128) kern = bf ? gather_kernel<true, 128>(bs) : gather_kernel<false, 128>(bs);
-  if (D == 256) kern = bf ? gather_kernel<true, 256>(bs) : gather_kernel<false, 256>(bs);
+  auto kern = many ? gather_kernel<4, 1>(bf, D, s->block_size) : gather_kernel<2, 2>(bf, D, s->block_size);
   cudaError_t e = launch_pdl(kern, grid, kGatherThreads, 0,
                              reinterpret_cast<cudaStream_t>(stream), static_cast<const uint8_t*>(k_cache),
                              static_cast<const uint8_t*>(v_cache), slot_mapping,

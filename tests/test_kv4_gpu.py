@@ -93,7 +93,9 @@ def test_append_refuses_on_the_device(pkv):
 # ---------------------------------------------------------------- gather
 @pytest.mark.parametrize("T,Hkv,D,bs,dtype", [
     (1, 1, 64, 16, torch.float16), (3, 5, 256, 32, torch.bfloat16), (129, 8, 128, 16, torch.bfloat16),
-    (1000, 3, 64, 32, torch.float16), (77, 16, 128, 32, torch.float16), (40, 2, 256, 16, torch.bfloat16)])
+    (1000, 3, 64, 32, torch.float16), (77, 16, 128, 32, torch.float16), (40, 2, 256, 16, torch.bfloat16),
+    # enough rows for the form of four tokens a CTA
+    (19467, 3, 64, 16, torch.bfloat16), (3895, 20, 128, 32, torch.float16), (6491, 5, 256, 16, torch.float16)])
 def test_gather(pkv, T, Hkv, D, bs, dtype):
     a, NB = make(T, 1, Hkv, D, bs, dtype, 0, seed=T, pad=T // 5)
     kc, vc = pkv.kv4_cache(NB, Hkv, bs, D), pkv.kv4_cache(NB, Hkv, bs, D)
