@@ -76,8 +76,9 @@ int kv4_plan(const pkv_shape* s, int sms, pkv_plan* plan, Late* late) {
     // finer, which evens the ends out.  Measured against one size for all:
     // 128 log-normal lengths, 8 kv heads, 55.9 us (61.6), 256 x 1-2048 69.4
     // (71.5), 64 x 512-4096 with 32 heads 116.8 (120.8), 64 x 1-4096 37.8
-    // (39.7).  A quarter of the sequences: 56.7, 69.6, 119.9; 256 tokens: 59.1,
-    // 69.6, 123.8.
+    // (39.7); equal lengths, which end together, lose: 128 x 8192 209 (206).
+    // A quarter of the sequences: 56.7, 69.6, 119.9; 256 tokens: 59.1, 69.6,
+    // 123.8.
     late->first = s->num_seqs - (s->num_seqs - 1) / 8 - 1;
     const long long pmin = (static_cast<long long>(maxL) + 1023) / 1024;
     long long P2 = pmin <= 512 ? 512 : (pmin + gran - 1) / gran * gran;

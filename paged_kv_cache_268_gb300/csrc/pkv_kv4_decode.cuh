@@ -48,8 +48,8 @@
 // sequences of 512-4096 tokens take 123 us in all three; 256 of 1-2048, four
 // query heads a key head, 72.9, 71.7 and 71 us.)
 // What bounds it (one GB300, graph-timed; floor: K and V bytes at the measured
-// copy rate): 128 sequences of 8192 tokens, 8 kv heads, 205 us of a 201 us
-// floor, so in the steady state memory does.  A tile's instructions alone (no
+// copy rate): 128 sequences of 8192 tokens, 8 kv heads, 206 us of a 201 us
+// floor in partitions of one size, so in the steady state memory does.  A tile's instructions alone (no
 // loads) take nearly as long as its bytes (64 x 512-4096 tokens, 32 kv heads:
 // 96 us and 108; both together 117, floor 111), so what start-up and the tail
 // of unequal lengths leave idle is not caught up: 256 x 1-2048 69 us of 54,
