@@ -373,6 +373,31 @@ def test_two_graphs_share_a_workspace_and_another_stream(pkv, split):
     assert all(torch.equal(o, w) for o, w in zip(got, want))
 
 
+def test_graph_replayed_with_other_lengths(pkv):
+    """A captured call reads its lengths when it runs: rows that were one
+    partition become several and the other way round, in both grid regions."""
+    B, max_len = 75, 1600
+    rng = np.random.default_rng(5)
+    full = rng.integers(1000, max_len + 1, B)
+    b = batch(full, 8, 8, 64, 16, torch.float16, seed=9)
+    d = device(b)
+    p = pkv.kv4_decode_plan(pkv.kv4_decode_shape(d["q"], d["k_cache"], d["block_tables"], max_len))
+    assert (p.split_tokens, p.num_splits) == (1024, 2)
+    out = torch.zeros_like(d["q"])
+    pkv.kv4_attn_decode(**d, out=out, max_context_len=max_len)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pkv.kv4_attn_decode(**d, out=out, max_context_len=max_len)
+    for lens in (full, np.minimum(full, rng.integers(0, 700, B)), full // 2, np.where(np.arange(B) % 3, full, 0)):
+        d["context_lens"].copy_(torch.from_numpy(lens.astype(np.int32)))
+        g.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        want = check(pkv, dict(b, lens=lens.astype(np.int32)), d, max_context_len=max_len)
+        assert torch.equal(got, want)
+
+
 def test_cache_past_32_bit_offsets(pkv):
     """A 4-bit pool of more than 2^32 bytes: append to, gather from and attend
     over its last blocks."""
