@@ -374,6 +374,11 @@ int pkv_kv4_gather(const pkv_shape* shape, const void* k_cache, const void* v_ca
  *    max_context_len are errors, as for pkv_paged_attn_decode.
  *  - workspace: pkv_kv4_workspace_bytes; NULL takes the workspace set with
  *    pkv_set_workspace.
+ *  - Precision: products and sums are FP32, but a softmax weight is rounded to
+ *    binary16, and again after its product with a value's scale.  With w the
+ *    weights, W the largest of them and S the largest scale among 32
+ *    neighbouring tokens of the channel's group, that adds up to 2^-10 sum w |v|
+ *    + W sum (2^-37 |v| + max(2^-24 S, 2^-51) (n + |z|)) to an element.
  */
 int pkv_kv4_attn_decode(const pkv_shape* shape, const void* q, const void* k_cache,
                         const void* v_cache, const int32_t* block_tables,

@@ -30,18 +30,28 @@
 // bulk copy for K and one for V.  Per 16 tokens:
 //   S[16 tok x 8 columns]: ldmatrix gives a lane one word (8 channels) of each
 //     of two tokens; two k16 steps per group.
-//   P' = P s in binary16, per column (a weight's rounding, 2^-12 of it at most,
-//     and its product's are the only ones below FP32; P is binary16 for
-//     bfloat16 inputs too, which have fewer bits).
+//   P' = P s in binary16, per column (a weight's rounding, 2^-11 of it at most
+//     where it is a normal number, and its product's are the only ones below
+//     FP32; P is binary16 for bfloat16 inputs too, which have fewer bits).
 //   O^T[32 ch x 8 columns] += codes^T P': ldmatrix.trans puts two neighbouring
 //     tokens' words side by side; two m16 tiles per group.
 //   z^T P' with the pairs (s, z) as they lie in the cache for the A operand:
 //     rows 8 on give the zero-point sums (one m16 tile per GS groups).
-// P is scaled by 2^(12-E), E >= 0 the exponent of the largest value scale so
-// far, so that neither small weights nor small scales fall out of binary16; the
-// running sum carries the same factor.  The reference follows the running
-// maximum only when that is more than a factor of 2 ahead, which spares the
-// rescalings for small gains: P stays at most 2^13 and P' below 2^14.
+// P is scaled by 2^12, as the running sum is, so that weights down to 2^-26 of
+// the largest are normal numbers.  The reference follows the running maximum
+// only when that is more than a factor of 2 ahead, which spares the rescalings
+// for small gains: P stays at most 2^13.  P' is below 2^14 and, for the largest
+// weight, a normal number where the scales are usual ones: below 2, and of
+// 2^-13 or more in some token of each channel group's 32.  A group whose scales
+// are not has them multiplied by a power of two in shared memory as its stages
+// come, and its sums by what brings them in line (`follow`).  So the weights'
+// share of a group of channels gets lost only below max(2^-24 S, 2^-51) (n + z)
+// of the largest weight, S the largest scale of the group in the 32 tokens:
+// small values keep their weights, beside large ones of other channels or
+// tokens too.  The look for unusual scales costs ordinary values 0.2-0.7% (64 x
+// 512-4096 tokens, 32 kv heads, 117.7 us, 117.2 without; 256 x 1-2048, 69.5 and
+// 69.1; up to 2% at head_dim 256), unusual ones more (256 x 1-2048 with values
+// of 1e-5, 78.2 us).
 // (Following at once makes the largest weight a power of two, which rounds to
 // itself: binary16 results are then off by 2.7e-4 of their size in all, 2.8e-4
 // as it is, 3.3e-4 at a factor of 32; their own rounding is 2.1e-4.  The 64
@@ -83,7 +93,7 @@ struct Kv4Args {
 constexpr int kKv4Warps = 4;
 constexpr int kKv4Tokens = 32;   // per stage
 
-// Stages per warp: about 40-60 KB of ring per CTA.
+// Stages per warp: 40 KB of ring per CTA, 80 KB at head_dim 256.
 constexpr int kv4_stages(int D) { return D == 64 ? 4 : 2; }
 // Resident CTAs per SM that the registers are budgeted for.
 constexpr int kv4_ctas(int D, int HC, int NT) {
@@ -206,8 +216,9 @@ struct Kv4Compute {
   float sc[NT][2];                         // to log2 units, not negative
   float o[2 * NG][NT][4];                  // codes^T P'
   float oz[NS][NT][4];                     // (s, z)^T P': elements 2 and 3 are z's
-  float ref[NT][2], l[NT][2];              // running maximum less shift; sum
-  float shift;                             // kShift - E
+  float ref[NT][2], l[NT][2];              // running maximum less kShift; sum
+  int down;                                // value scales of group lane % NG count 2^-down times,
+                                           // down in bits 0 .. 4; bit 14 where it is not 0
 
   static __device__ __forceinline__ int place(int column) { return column / HC; }   // j of a column
 
@@ -305,7 +316,7 @@ struct Kv4Compute {
   }
 
   __device__ __forceinline__ void reset() {
-    shift = kShift;
+    down = 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       ref[nt][0] = ref[nt][1] = -INFINITY;
@@ -342,38 +353,82 @@ struct Kv4Compute {
     __syncwarp();
   }
 
-  // The running maximum is more than the slack behind `top`, or (large) a value
-  // scale of 2 or more is in the stage: set the reference (and the shift, so
-  // that weights times the largest scale stay in binary16) and rescale the sums.
-  __device__ __forceinline__ void catch_up(const float (&top)[NT][2], bool large, uint32_t kt, int lane) {
-    float now = shift;
-    if (__any_sync(0xffffffffu, large)) {
-      float most = 0.f;
-      for (int i = lane; i < 16 * NG; i += 32) {
-        const int half = i / (8 * NG), rest = i % (8 * NG);
-        uint32_t x;
-        asm volatile("ld.shared.b32 %0, [%1];"
-                     : "=r"(x)
-                     : "r"(kt + VT + PAR + (half ? block_of(1) + row_of(1) / 2 * NG * 8 : 0) + rest * 8));
-        const float2 f = unpack2<false>(x);
-        most = fmaxf(most, fmaxf(f.x, f.y));
-      }
+  // Address of this lane's share i of the stage's value scales: pair i * 32 +
+  // lane of (two tokens, group), which is one of group lane % NG.
+  static __device__ __forceinline__ uint32_t scale_pair(uint32_t kt, int i, int lane) {
+    const int k = i * 32 + lane, half = k / (8 * NG), rest = k % (8 * NG);
+    return kt + VT + PAR + (half ? block_of(1) + row_of(1) / 2 * NG * 8 : 0) + rest * 8;
+  }
+
+  static __device__ __forceinline__ float power_of_two(int e) {
+    return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+  }
+
+  static __device__ __forceinline__ int down_of(int down) { return static_cast<int>(static_cast<uint32_t>(down) << 27) >> 27; }
+
+  // Some group's value scales are not usual ones, of 2^-13 to 2, or were not
+  // before.  Where a group's largest is not, its scales in the stage are
+  // multiplied by the power of two that brings it to [1, 2) (2^15 at most),
+  // and its sums, so far of other multiples, by the one between the two; both
+  // are exact, but where large scales make small ones subnormal.  The power
+  // stays while the largest is between 1/2 and 2.
+  __device__ __forceinline__ void follow(uint32_t kt, int lane) {
+    uint32_t x[NG / 2];
+    int most = 0;                          // the group's largest, its binary16 bits
 #pragma unroll
-      for (int m = 1; m < 32; m <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
-      const int e = static_cast<int>(__float_as_uint(most) >> 23) - 127;   // most < 2^(e + 1)
-      now = fminf(now, kShift - static_cast<float>(min(max(e, 0), 17)));
+    for (int i = 0; i < NG / 2; ++i) {
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x[i]) : "r"(scale_pair(kt, i, lane)));
+      const int a = x[i] & 0xffff, b = x[i] >> 16;
+      most = max(most, max(a > 0x7bff ? 0 : a, b > 0x7bff ? 0 : b));   // a NaN counts for none
     }
+#pragma unroll
+    for (int m = NG; m < 32; m <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, m));
+    const int old = down_of(down), e = most >> 10;   // 2^(e - 15) <= most < 2^(e - 14)
+    int now = max(min(e - 15, 14), -15);
+    if (e >= 2 && e < 16) now = 0;
+    if ((old != 0 && (e == old + 15 || e == old + 14)) || most == 0) now = old;
+    if (now != 0) {
+      const uint32_t f = static_cast<uint32_t>(15 - now) * 0x04000400u;   // 2^-now, twice
+#pragma unroll
+      for (int i = 0; i < NG / 2; ++i)
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(scale_pair(kt, i, lane)), "r"(hmul2_bits(x[i], f)) : "memory");
+    }
+    down = now == 0 ? 0 : 0x4000 | (now & 31);
+    __syncwarp();
+    if (!__any_sync(0xffffffffu, now != old)) return;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const float f = power_of_two(__shfl_sync(0xffffffffu, old - now, g));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e4 = 0; e4 < 4; ++e4) {
+          o[2 * g][nt][e4] *= f;
+          o[2 * g + 1][nt][e4] *= f;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {         // columns 2c and 2c + 1
+      const float f = power_of_two(__shfl_sync(0xffffffffu, old - now, place(2 * (lane & 3)) * NS + i));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e4 = 0; e4 < 4; ++e4) oz[i][nt][e4] *= f;
+    }
+  }
+
+  // The running maximum is more than the slack behind `top`: set the reference
+  // and rescale the sums.
+  __device__ __forceinline__ void catch_up(const float (&top)[NT][2]) {
     float by[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float old = ref[nt][j];
-        const float keep = old + (shift - now);          // the same maximum, the new shift
-        ref[nt][j] = top[nt][j] > keep + (now + kSlack) ? top[nt][j] - now : keep;
+        if (top[nt][j] > old + (kShift + kSlack)) ref[nt][j] = top[nt][j] - kShift;
         by[nt][j] = old == ref[nt][j] ? 1.f : fast_exp2(old - ref[nt][j]);
       }
-    shift = now;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -395,17 +450,14 @@ struct Kv4Compute {
   template <bool RAGGED>
   __device__ __forceinline__ void stage(uint32_t kt, int valid, const uint32_t (&lrow)[NG / 2], int lane) {
     if constexpr (RAGGED) clear_tail(kt, valid, lane);
-    // Is a value scale of 2 or more among the stage's?  Every lane looks at its
-    // share of the scales' pairs.
-    uint32_t large = 0;
+    // Is a value scale of 2 or more among the stage's, or none of 2^-13 or more
+    // among a lane's share of them, all of group lane % NG?
+    uint32_t scales = down;
 #pragma unroll
     for (int i = 0; i < NG / 2; ++i) {
-      const int k = i * 32 + lane, half = k / (8 * NG), rest = k % (8 * NG);
       uint32_t x;
-      asm volatile("ld.shared.b32 %0, [%1];"
-                   : "=r"(x)
-                   : "r"(kt + VT + PAR + (half ? block_of(1) + row_of(1) / 2 * NG * 8 : 0) + rest * 8));
-      large |= x;
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(scale_pair(kt, i, lane)));
+      scales |= x;
     }
     uint32_t at[NG / 2];
 #pragma unroll
@@ -485,8 +537,9 @@ struct Kv4Compute {
 
     // Running maximum and sum; s stays in its own units (sc is not negative).
     float top[NT][2];
-    const bool big = (large & 0x40004000u) != 0;
-    bool rare = big;
+    // (bits of the exponent; a share past a sequence's end is all zeros)
+    const bool unusual = (scales & 0x40004000u) != 0 || ((scales & 0x38003800u) == 0 && !(RAGGED && scales == 0));
+    bool rare = unusual;
     if constexpr (RAGGED) {   // out of the maximum past the end
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -505,10 +558,13 @@ struct Kv4Compute {
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
         top[nt][j] = v * sc[nt][j];
-        rare |= top[nt][j] > ref[nt][j] + (shift + kSlack);
+        rare |= top[nt][j] > ref[nt][j] + (kShift + kSlack);
       }
     }
-    if (__any_sync(0xffffffffu, rare)) catch_up(top, big, kt, lane);
+    if (__any_sync(0xffffffffu, rare)) {
+      if (__any_sync(0xffffffffu, unusual)) follow(kt, lane);
+      catch_up(top);
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -570,6 +626,9 @@ struct Kv4Compute {
   // columns 2c, 2c + 1 hold group g only where it has their place.
   __device__ __forceinline__ void publish(float* cm, float* cl, float* co, int lane) {
     const int c = lane & 3, j = place(2 * c), h0 = 2 * c % HC;
+    float back[NG];   // takes the groups' powers of two out
+#pragma unroll
+    for (int g = 0; g < NG; ++g) back[g] = power_of_two(down_of(__shfl_sync(0xffffffffu, down, g)));
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -591,11 +650,12 @@ struct Kv4Compute {
           for (int x = 0; x < GS; ++x) {
             if (x != j) continue;
             const int g = x * NS + i;
+            const float f = back[g];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               const int d = 32 * g + 4 * (lane >> 2) + 2 * t;
               *reinterpret_cast<float2*>(co + h * kv4_row(D) + d) =
-                  make_float2(fmaf(o[2 * g + t][nt][k], 0x1p24f, z), fmaf(o[2 * g + t][nt][2 + k], 0x1p20f, z));
+                  make_float2(f * fmaf(o[2 * g + t][nt][k], 0x1p24f, z), f * fmaf(o[2 * g + t][nt][2 + k], 0x1p20f, z));
             }
           }
         }
