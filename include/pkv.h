@@ -355,7 +355,8 @@ int pkv_kv4_append(const pkv_shape* shape, const pkv_rope* rope, const void* q,
 /*
  * Read rows of the 4-bit cache back in 16 bits (a prefix for the attention of
  * a prompt's next chunk, an export): for every token t and kv head h,
- *     k[t][h][:] and v[t][h][:] = the values at slot_mapping[t], one rounding.
+ *     k[t][h][:] and v[t][h][:] = the values at slot_mapping[t],
+ * rounded once in FP32, and from there to 16 bits.
  *   shape         uses num_kv_heads, head_dim, block_size, num_blocks, dtype
  *   slot_mapping  [T] int32; the row of a negative slot is set to zero
  *   k, v          [T, Hkv, D], 16-byte aligned

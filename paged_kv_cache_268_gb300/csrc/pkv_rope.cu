@@ -346,8 +346,9 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(cons
   }
 }
 
-// Rows of the 4-bit cache back in 16 bits.  value = scale * (code + zero) in
-// FP32 (the sum is exact), one rounding at the store.  Rows of a negative or
+// Rows of the 4-bit cache back in 16 bits.  value = scale * code + scale * zero:
+// both products are exact in FP32 (15 and 22 bits), so the value is rounded once
+// there, and once at the store.  Rows of a negative or
 // bad slot become zeros.  The D/8 lanes of a row hold one chunk each; a CTA
 // takes TOK tokens and LOOPS passes over their head rows, all of whose bytes
 // it asks for before it works on the first.  Bound by memory: three of its four
@@ -421,13 +422,14 @@ __global__ void __launch_bounds__(kGatherThreads)
     for (int i = 0; i < TOK; ++i) {
       if (t0 + i >= T) break;
       const float2 p = unpack2<false>(par[j][i]);
+      const float scale = p.x * 0x1p24f, low = p.x * p.y;
       float x[8];
-      // nibbles e and e + 4 as binary16 subnormals, n * 2^-24; n + z and 2^24 (n 2^-24) are exact
+      // nibbles e and e + 4 as binary16 subnormals, n * 2^-24
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 n = unpack2<false>((w[j][i] >> (4 * e)) & 0x000f000fu);
-        x[e] = p.x * fmaf(n.x, 0x1p24f, p.y);
-        x[e + 4] = p.x * fmaf(n.y, 0x1p24f, p.y);
+        x[e] = fmaf(n.x, scale, low);
+        x[e + 4] = fmaf(n.y, scale, low);
       }
       *reinterpret_cast<uint4*>(dst + static_cast<size_t>(i) * Hkv * D) = pack8<BF>(x);
     }
