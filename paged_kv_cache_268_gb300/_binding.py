@@ -767,8 +767,11 @@ def copy_blocks(src_k: torch.Tensor, src_v: torch.Tensor, dst_k: torch.Tensor,
     (dst_k, dst_v).  Pools are [NB, Hkv, bs, D] tensors on the GPU or in
     pinned host memory, or 4-bit ones (kv4_cache); pairs is an int32 [n, 2]
     tensor the GPU can read."""
-    if all(t.dtype == torch.uint8 and t.dim() == 4 and t.is_contiguous() and t.shape[3] % 2 == 0
-           for t in (src_k, src_v, dst_k, dst_v)):
+    if torch.uint8 in (src_k.dtype, src_v.dtype, dst_k.dtype, dst_v.dtype):
+        for t, n in ((src_k, "src_k"), (src_v, "src_v"), (dst_k, "dst_k"), (dst_v, "dst_v")):
+            if (t.dtype != torch.uint8 or t.dim() != 4 or not t.is_contiguous()
+                    or t.shape[3] not in (40, 80, 160) or t.shape[2] not in (16, 32)):
+                raise ValueError(f"{n} must be a contiguous 4-bit pool [NB, Hkv, bs, 5D/8] like the others")
         if src_k.shape[1:] != dst_k.shape[1:]:
             raise ValueError("pools must share the block shape")
         src_k, src_v, dst_k, dst_v = map(_kv4_as_rows, (src_k, src_v, dst_k, dst_v))
