@@ -40,7 +40,10 @@
 // P is scaled by 2^12, as the running sum is, so that weights down to 2^-26 of
 // the largest are normal numbers.  The reference follows the running maximum
 // only when that is more than a factor of 2 ahead, which spares the rescalings
-// for small gains: P stays at most 2^13.  P' is below 2^14 and, for the largest
+// for small gains: P stays at most 2^13.  It is subtracted where a logit's sum
+// begins, in the logit's own units: the exponents that are left are small, so
+// that logits past 2^24, whose products with the scale are rounded to more
+// than one, still give weights of at most 2^13.  P' is below 2^14 and, for the largest
 // weight, a normal number where the scales are usual ones: below 2, and of
 // 2^-13 or more in some token of each channel group's 32.  A group whose scales
 // are not has them multiplied by a power of two in shared memory as its stages
@@ -216,9 +219,11 @@ struct Kv4Compute {
   float sc[NT][2];                         // to log2 units, not negative
   float o[2 * NG][NT][4];                  // codes^T P'
   float oz[NS][NT][4];                     // (s, z)^T P': elements 2 and 3 are z's
-  float ref[NT][2], l[NT][2];              // running maximum less kShift; sum
+  float m[NT][2], l[NT][2];                // reference, in the logits' units before sc; sum
+                                           // (m only in the lanes of group place 0, else 0)
   int down;                                // value scales of group lane % NG count 2^-down times,
-                                           // down in bits 0 .. 4; bit 14 where it is not 0
+                                           // down in bits 0 .. 4; bit 14 where it is not 0;
+                                           // negative before the first stage
 
   static __device__ __forceinline__ int place(int column) { return column / HC; }   // j of a column
 
@@ -316,10 +321,10 @@ struct Kv4Compute {
   }
 
   __device__ __forceinline__ void reset() {
-    down = 0;
+    down = static_cast<int>(0x80000000u);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      ref[nt][0] = ref[nt][1] = -INFINITY;
+      m[nt][0] = m[nt][1] = 0.f;
       l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -417,28 +422,29 @@ struct Kv4Compute {
     }
   }
 
-  // The running maximum is more than the slack behind `top`: set the reference
-  // and rescale the sums.
-  __device__ __forceinline__ void catch_up(const float (&top)[NT][2]) {
-    float by[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float old = ref[nt][j];
-        if (top[nt][j] > old + (kShift + kSlack)) ref[nt][j] = top[nt][j] - kShift;
-        by[nt][j] = old == ref[nt][j] ? 1.f : fast_exp2(old - ref[nt][j]);
-      }
+  // The first stage, or its maximum (`top`, above the reference) is past the
+  // slack: it becomes the reference, and the sums and the stage's logits follow.
+  __device__ __forceinline__ void catch_up(const float (&top)[NT][2], float (&s)[2][NT][4], bool first, int lane) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      float by[2], more[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) l[nt][j] *= by[nt][j];
+      for (int j = 0; j < 2; ++j) {
+        const float gain = top[nt][j] * sc[nt][j];
+        const bool go = first || gain > kSlack;
+        by[j] = first ? 0.f : (go ? fast_exp2(-gain) : 1.f);
+        more[j] = go ? top[nt][j] : 0.f;
+        if (place(2 * (lane & 3)) == 0) m[nt][j] += more[j];
+        l[nt][j] *= by[j];
+      }
 #pragma unroll
       for (int e4 = 0; e4 < 4; ++e4) {
+        s[0][nt][e4] -= more[e4 & 1];
+        s[1][nt][e4] -= more[e4 & 1];
 #pragma unroll
-        for (int i = 0; i < 2 * NG; ++i) o[i][nt][e4] *= by[nt][e4 & 1];
+        for (int i = 0; i < 2 * NG; ++i) o[i][nt][e4] *= by[e4 & 1];
 #pragma unroll
-        for (int i = 0; i < NS; ++i) oz[i][nt][e4] *= by[nt][e4 & 1];
+        for (int i = 0; i < NS; ++i) oz[i][nt][e4] *= by[e4 & 1];
       }
     }
   }
@@ -452,7 +458,7 @@ struct Kv4Compute {
     if constexpr (RAGGED) clear_tail(kt, valid, lane);
     // Is a value scale of 2 or more among the stage's, or none of 2^-13 or more
     // among a lane's share of them, all of group lane % NG?
-    uint32_t scales = down;
+    uint32_t scales = 0;
 #pragma unroll
     for (int i = 0; i < NG / 2; ++i) {
       uint32_t x;
@@ -521,7 +527,7 @@ struct Kv4Compute {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float by = e < 2 ? sl : su;
-            s[mt][nt][e] = i == 0 ? by * acc[mt][nt][e] : fmaf(by, acc[mt][nt][e], s[mt][nt][e]);
+            s[mt][nt][e] = fmaf(by, acc[mt][nt][e], i == 0 ? -m[nt][e & 1] : s[mt][nt][e]);
           }
       }
     });
@@ -535,11 +541,13 @@ struct Kv4Compute {
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[mt][nt][e] += __shfl_xor_sync(0xffffffffu, s[mt][nt][e], m);
 
-    // Running maximum and sum; s stays in its own units (sc is not negative).
+    // The stage's maximum; s stays in its own units (sc is not negative), above
+    // the reference: subtracted first, so that the exponents of large logits
+    // have no rounding that the reference has not.
     float top[NT][2];
     // (bits of the exponent; a share past a sequence's end is all zeros)
     const bool unusual = (scales & 0x40004000u) != 0 || ((scales & 0x38003800u) == 0 && !(RAGGED && scales == 0));
-    bool rare = unusual;
+    bool rare = unusual || down != 0;
     if constexpr (RAGGED) {   // out of the maximum past the end
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -557,13 +565,15 @@ struct Kv4Compute {
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-        top[nt][j] = v * sc[nt][j];
-        rare |= top[nt][j] > ref[nt][j] + (kShift + kSlack);
+        top[nt][j] = v;
+        rare |= v * sc[nt][j] > kSlack;
       }
     }
     if (__any_sync(0xffffffffu, rare)) {
-      if (__any_sync(0xffffffffu, unusual)) follow(kt, lane);
-      catch_up(top);
+      const bool first = down < 0;
+      if (first) down = 0;
+      if (__any_sync(0xffffffffu, unusual || down != 0)) follow(kt, lane);
+      catch_up(top, s, first, lane);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -571,7 +581,7 @@ struct Kv4Compute {
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float p = fast_exp2(fmaf(s[mt][nt][e], sc[nt][e & 1], -ref[nt][e & 1]));
+          float p = fast_exp2(fmaf(s[mt][nt][e], sc[nt][e & 1], kShift));
           // (a scale of zero times minus infinity is no number)
           if (RAGGED && mt * 16 + (e >> 1) * 8 + (lane >> 2) >= valid) p = 0.f;
           s[mt][nt][e] = p;
@@ -639,7 +649,7 @@ struct Kv4Compute {
         lt += __shfl_xor_sync(0xffffffffu, lt, 16);
         const int h = nt * 8 + h0 + k;
         if (lane < HC / 2) {
-          cm[h] = ref[nt][k];
+          cm[h] = down < 0 ? -INFINITY : fmaf(m[nt][k], sc[nt][k], -kShift);   // in log2 units
           cl[h] = lt;
         }
 #pragma unroll
