@@ -271,10 +271,15 @@ struct Kv4Compute {
       int e = 14 + 127 - static_cast<int>(__float_as_uint(top) >> 23);
       e = top > 0.f ? min(e, 120) : 0;
       float f = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      if (warp == 0 && n < HC && c == 0)   // an infinite or NaN query gives NaN
-        scales[h] = top < INFINITY
-                        ? fabsf(scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * 0x1p24f
-                        : __uint_as_float(0x7fc00000u);
+      if (warp == 0 && n < HC && c == 0) {
+        // Queries near bfloat16's largest would take this past FP32's.  The sums
+        // that it multiplies are whole multiples of 2^-96, so from 2^127 on every
+        // difference between two decides alone, as it does for the true factor.
+        const int up = min(24 - e, 127);
+        const float by = fabsf(scale_log2) * power_of_two(up) * power_of_two(24 - e - up);
+        // an infinite or NaN query gives NaN
+        scales[h] = top < INFINITY ? (by > 0x1p127f ? 0x1p127f : by) : __uint_as_float(0x7fc00000u);
+      }
       if (scale_log2 < 0.f) f = -f;
 #pragma unroll
       for (int i = 0; i < PG; ++i) {
