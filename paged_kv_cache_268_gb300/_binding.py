@@ -423,10 +423,14 @@ def _sized(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks
            max_blocks_per_seq, max_context_len, dtype, split_tokens=0) -> Shape:
     """A Shape, made once for the same sizes.  Read only.  It carries a reference
     to itself for calls and, per device, the 4-bit decode's workspace size."""
-    shape = make_shape(num_seqs=num_seqs, num_q_heads=num_q_heads, num_kv_heads=num_kv_heads,
-                       head_dim=head_dim, block_size=block_size, num_blocks=num_blocks,
-                       max_blocks_per_seq=max_blocks_per_seq, max_context_len=max_context_len,
-                       dtype=dtype, split_tokens=split_tokens)
+    sizes = dict(num_seqs=num_seqs, num_q_heads=num_q_heads, num_kv_heads=num_kv_heads,
+                 head_dim=head_dim, block_size=block_size, num_blocks=num_blocks,
+                 max_blocks_per_seq=max_blocks_per_seq, max_context_len=max_context_len,
+                 split_tokens=split_tokens)
+    for n, x in sizes.items():
+        if not -2 ** 31 <= x < 2 ** 31:      # the struct would hold other numbers
+            raise ValueError(f"{n} must fit 32 bits, got {x}")
+    shape = make_shape(**sizes, dtype=dtype)
     shape.ref, shape.kv4_workspace = ctypes.byref(shape), {}
     return shape
 
