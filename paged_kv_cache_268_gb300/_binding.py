@@ -395,6 +395,8 @@ def rope_table(max_position: int, rot_dim: int, base: float = 10000.0,
     """The cos_sin table [max_position, rot_dim] float32 of rope_append and
     kv4_append: cosines, then sines, of position * base^(-2i / rot_dim).  The
     angles are worked out in 64 bits (far positions need them)."""
+    if rot_dim < 0 or rot_dim % 2:
+        raise ValueError("rot_dim must be an even number of channels")
     f = float(base) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
     a = torch.arange(max_position, dtype=torch.float64, device=device)[:, None] * f
     return torch.cat([a.cos(), a.sin()], 1).float()

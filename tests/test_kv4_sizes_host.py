@@ -15,3 +15,10 @@ def test_sizes_past_32_bits_are_refused(kw):
         B.kv4_decode_shape(**call, **kw)
     good = B.kv4_decode_shape(**call, max_context_len=20, split_tokens=16)
     assert (good.max_context_len, good.split_tokens) == (20, 16)
+
+
+def test_rope_table_refuses_an_odd_width():
+    for rot in (15, 1, -2):
+        with pytest.raises(ValueError):
+            B.rope_table(8, rot, device="cpu")
+    assert B.rope_table(8, 16, device="cpu").shape == (8, 16) and B.rope_table(8, 0, device="cpu").shape == (8, 0)
