@@ -270,11 +270,9 @@ int cache_map(CUtensorMap* out, const void* base, const pkv_shape& s, bool three
   return PKV_OK;
 }
 
-// ------------------------------------------------------------------ checks
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 }  // namespace
 
+// ------------------------------------------------------------------ checks
 int check_cache_shape(const pkv_shape* s) {
   if (!s) return PKV_ERR_NULL;
   if (s->num_kv_heads < 1 || s->head_dim < 1 || s->block_size < 1 || s->num_blocks < 1)
@@ -358,7 +356,7 @@ int make_plan(const pkv_shape* s, int sms, pkv_plan* plan) {
     // CTAs per SM): 2048-token partitions, 4096 where one CTA fills an SM.
     // The 16- and 32-head mma.sync tiles (two CTAs per SM) also run best on
     // 2048 (measured on one GB300: 5% faster than 1024 at 32 heads, 2% at 16;
-    // 3072 and 4096 slower again).
+    // larger ones slower again).
     const bool wide_mma = plan->variant == 1 && G > 8;
     if (plan->variant == 2)
       P = G > 16 ? 4096 : 2048;
@@ -436,10 +434,6 @@ int device_workspace(void** ptr, size_t* bytes) {
   const int rc = current_device(&d);
   if (rc == PKV_OK) set_workspace_of(d, ptr, bytes);
   return rc;
-}
-
-cudaError_t launch_split_reduce(const DecodeArgs& a, bool bf16, int D, cudaStream_t stream) {
-  return bf16 ? launch_reduce<true>(a, D, stream) : launch_reduce<false>(a, D, stream);
 }
 
 void count_launch() { g_launches.fetch_add(1); }

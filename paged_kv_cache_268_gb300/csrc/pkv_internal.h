@@ -76,14 +76,14 @@ int tc_warps(int group_size);        // warps per CTA (softmax, producer, MMA)
 
 int* device_error_word();  // device address of the error word (current device)
 
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
 // Services of the front end (pkv_api.cu) to the other entry points.
 int check_cache_shape(const pkv_shape*);     // PKV_OK or the PKV_ERR_* of a bad cache shape
 int check_decode_shape(const pkv_shape*);    // the same for a decode batch
 int device_sms(int* sms);                    // SM count of the current device
 // Workspace set for the current device with pkv_set_workspace, or {nullptr, 0}.
 int device_workspace(void** ptr, size_t* bytes);
-// Cross-split reduce of a.part_o / a.part_ml into a.out (head_dim D).
-cudaError_t launch_split_reduce(const DecodeArgs& a, bool bf16, int D, cudaStream_t stream);
 void count_launch();                         // one more kernel for pkv_launch_count
 
 // Launch with programmatic stream serialisation: the grid may become resident

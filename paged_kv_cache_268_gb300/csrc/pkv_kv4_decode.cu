@@ -5,8 +5,6 @@
 namespace pkv {
 namespace {
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 // CTAs that share the query heads of one kv head.
 int kv4_chunks(const pkv_shape* s) {
   const int G = s->num_q_heads / s->num_kv_heads;

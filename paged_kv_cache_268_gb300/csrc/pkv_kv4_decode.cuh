@@ -122,21 +122,6 @@ constexpr int kv4_smem(int D, int NT) {
   return kv4_tail(D, NT) + kv4_query_bytes(D, NT) + kKv4Warps * kv4_stages(D) * 8 + kMaxBlocksPerCta * 4 + 128;
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar,
-                                          uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], "
-      "%2, [%3], %4;" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
-      : "memory");
-}
-
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // for (i = 0; i < N; ++i) f(i) with i a constant, so that offsets can be
 // immediates of the shared-memory instructions.
 template <int N, int I = 0, class F>

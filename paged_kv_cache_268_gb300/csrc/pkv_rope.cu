@@ -33,36 +33,6 @@ struct RopeArgs {
   int rot, inter, max_pos;
 };
 
-// Untiled bulk copy to shared memory, completing on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
-}
-
-// Smallest and largest, NaN where one is; of three in one instruction.
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float min_nan(float a, float b, float c) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b, float c) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 template <bool BF>
 __device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
   const float2 a = unpack2<BF>(u.x), b = unpack2<BF>(u.y), c = unpack2<BF>(u.z),
@@ -447,8 +417,6 @@ auto gather_kernel(bool bf, int D, int bs) {
   if (D == 256) kern = bf ? gather_kernel<TOK, LOOPS, true, 256>(bs) : gather_kernel<TOK, LOOPS, false, 256>(bs);
   return kern;
 }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // The kernels' shared-memory limit, raised once per device and kernel (threads
 // that race here set the same attribute).
