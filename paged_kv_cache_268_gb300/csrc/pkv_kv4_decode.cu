@@ -33,15 +33,20 @@ int kv4_plan(const pkv_shape* s, int sms, pkv_plan* plan, Late* late) {
   if (s->split_tokens > 0) {
     P = (static_cast<long long>(s->split_tokens) + bs - 1) / bs * bs;
   } else {
-    // Tokens per resident CTA if every sequence were of the largest length.
+    // Tokens per resident CTA if every sequence were of the largest length
+    // (max_context_len, all that the host knows: a bound far above the lengths
+    // costs empty CTAs and partitions of another size; 128 log-normal lengths
+    // of up to 8192 56 us, 70 under a bound of 32768, 129 under 131072).
     // Measured on one GB300 over batches of 1 to 128 sequences (uniform and
     // log-normal lengths, 8 and 32 kv heads, head_dim 64 to 256), one size for
-    // all sequences:
+    // all sequences, before the last of them were cut finer (below):
     //  - from 6000 on, 2048-token partitions (64 x 512-4096 tokens, 32 heads:
     //    123 us, 126 at 1024), from 1000 on, 1024 (64 x 1-4096, 8 heads: 40 us,
     //    43 at 2048 or 512), below, half of it;
     //  - up to four sequences, whose lengths are mostly near the largest: one
-    //    wave of equal partitions (4 x 32768 tokens: 36 us, 42-45 at 768-2048);
+    //    wave of equal partitions (4 x 32768 tokens: 36 us, 42-45 at 768-2048).
+    //    Where that ends is not measured: 5 x 32768 tokens take 52 us, 8 take 75
+    //    (floors 31 and 50);
     //  - at least 256 tokens, 128 where a sequence has at most 2048, since
     //    start-up and merge cost a CTA as much as about that many (1 x 8192: 8.1
     //    us at 256, 10.4 at 128; 1 x 500: 5.2 us at 128, 6.2 at 256); no split of

@@ -43,31 +43,35 @@
 // for small gains: P stays at most 2^13.  It is subtracted where a logit's sum
 // begins, in the logit's own units: the exponents that are left are small, so
 // that logits past 2^24, whose products with the scale are rounded to more
-// than one, still give weights of at most 2^13.  P' is below 2^14 and, for the largest
-// weight, a normal number where the scales are usual ones: below 2, and of
-// 2^-13 or more in some token of each channel group's 32.  A group whose scales
-// are not has them multiplied by a power of two in shared memory as its stages
-// come, and its sums by what brings them in line (`follow`).  So the weights'
-// share of a group of channels gets lost only below max(2^-24 S, 2^-51) (n + z)
-// of the largest weight, S the largest scale of the group in the 32 tokens:
-// small values keep their weights, beside large ones of other channels or
-// tokens too.  The look for unusual scales costs ordinary values 0.2-0.7% (64 x
+// than one, still give weights of at most 2^13.
+// P' is below 2^14 and, for the largest weight, a normal number where the
+// scales are usual ones: below 2, and of 2^-13 or more in some token of each
+// channel group's 32.  A group whose scales are not has them multiplied by a
+// power of two in shared memory as its stages come, and its sums by what brings
+// them in line (`follow`).  So a token's share in a group of channels gets lost
+// only below max(2^-24 S, 2^-51) (n + z) of the largest weight, S the largest
+// scale of the group in the 32 tokens: small values keep their weights, beside
+// large ones of other channels or tokens too.  The look for unusual scales costs ordinary values 0.2-0.7% (64 x
 // 512-4096 tokens, 32 kv heads, 117.7 us, 117.2 without; 256 x 1-2048, 69.5 and
 // 69.1; up to 2% at head_dim 256), unusual ones more (256 x 1-2048 with values
 // of 1e-5, 78.2 us).
 // (Following at once makes the largest weight a power of two, which rounds to
 // itself: binary16 results are then off by 2.7e-4 of their size in all, 2.8e-4
-// as it is, 3.3e-4 at a factor of 32; their own rounding is 2.1e-4.  The 64
-// sequences of 512-4096 tokens take 123 us in all three; 256 of 1-2048, four
-// query heads a key head, 72.9, 71.7 and 71 us.)
+// as it is, 3.3e-4 at a factor of 32; their own rounding is 2.1e-4.  Measured
+// on a form of the kernel before the finer last partitions: 64 sequences of
+// 512-4096 tokens 123 us in all three; 256 of 1-2048, four query heads a key
+// head, 72.9, 71.7 and 71 us.)
 // What bounds it (one GB300, graph-timed; floor: K and V bytes at the measured
-// copy rate): 128 sequences of 8192 tokens, 8 kv heads, 206 us of a 201 us
-// floor in partitions of one size, so in the steady state memory does.  A tile's instructions alone (no
-// loads) take nearly as long as its bytes (64 x 512-4096 tokens, 32 kv heads:
-// 96 us and 108; both together 117, floor 111), so what start-up and the tail
-// of unequal lengths leave idle is not caught up: 256 x 1-2048 69 us of 54,
-// 128 log-normal 56 of 40, 4 x 32768 36 of 25.  Half of the instructions are
-// the shift and ANDs of the codes, at two cycles each per SM quarter.
+// copy rate): 128 sequences of 8192 tokens, 32/8 heads, 207 us of a 201 us
+// floor in partitions of one size, so in the steady state memory does.  A
+// tile's instructions alone (no loads) take nearly as long as its bytes (64 x
+// 512-4096 tokens, 32/32 heads: 96 us and 108; both together 118, floor 111),
+// so what start-up and the tail of unequal lengths leave idle is not caught up:
+// 256 x 1-2048 69.5 us of 54, 128 log-normal 56 of 40, 4 x 32768 36.5 of 25.
+// Half of the instructions are the shift and ANDs of the codes, at two cycles
+// each per SM quarter.  Groups of 8 query heads are bound by them (64 x 8192
+// tokens: 129 us of 100), wider ones take a multiple (16 heads 211, 32 heads
+// 413, whose tiles are fetched twice too).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -191,7 +195,8 @@ struct Kv4Compute {
   static constexpr int PER = kKv4Tokens / BS;   // blocks per stage
   // Query fragments in registers, or read from shared memory for every stage:
   // at head_dim 128 the registers serve the schedule better (64 x 512-4096
-  // tokens: 121 us, 123 with fragments in registers).
+  // tokens, before the finer last partitions: 121 us, 123 with fragments in
+  // registers).
   static constexpr bool QREG = D * NT < 128;
   static constexpr uint32_t M0 = 0x000f000fu, M1 = 0x00f000f0u;
   static constexpr float kShift = 12.f, kSlack = 1.f;
