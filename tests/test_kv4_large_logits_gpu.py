@@ -6,7 +6,9 @@ import pytest
 import torch
 
 import kv4_ref as R
-from test_kv4_gpu import batch, device
+from kv4_bound import attention_and_bound
+from test_kv4_decode_values_gpu import HALF_SUBNORMAL
+from test_kv4_gpu import EPS, batch, device
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +44,23 @@ def test_large_logits(pkv, dtype, Hq, D, mag):
                     lo = hi = v[near, g][0]
                 room = 2.0 ** -8 * np.abs(v[near, g]).max(0) + 2.0 ** -9 * np.abs(v[:, g]).max()
                 assert np.all(got[i, h] >= lo - room) and np.all(got[i, h] <= hi + room)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("Hq,D", [(1, 128), (4, 128), (8, 64), (16, 128), (3, 256)])
+@pytest.mark.parametrize("span", [20.0, 400.0, 4000.0])
+def test_logits_that_grow_along_a_sequence(pkv, dtype, Hq, D, span):
+    """The reference moves at nearly every stage, or at the first alone."""
+    L = 3000
+    for down in (False, True):
+        b = batch([L, 45], Hq, 1, D, 16, dtype, seed=Hq + D)
+        t = np.arange(L)
+        slots = b["tables"][0, t // 16].astype(np.int64) * 16 + t % 16
+        x = (t[::-1] if down else t) / L * span - 0.7 * span + np.random.default_rng(1).standard_normal(L)
+        k = np.broadcast_to((x / (b["scale"] * D))[:, None, None], (L, 1, D))
+        R.store(b["kc"], k.astype(np.float32), slots, False)
+        b["q"][0] = 1
+        for split in (0, 1024):
+            out = pkv.kv4_attn_decode(**device(b), split_tokens=split)
+            want, bound = attention_and_bound(b, EPS[dtype], HALF_SUBNORMAL[dtype])
+            assert np.all(np.abs(R.to_np(out).astype(np.float64) - want) <= bound)
