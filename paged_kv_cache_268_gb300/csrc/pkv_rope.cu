@@ -50,9 +50,10 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 // within 2^-23 of it.  q = a y, corrected by its exact remainder (Markstein's
 // correction): before its last rounding the result is within 2^-22 half-steps
 // of a / b.  That decides the rounding, as a / b is never that near a border
-// between two floats: the border c has 25 bits, a - b c is a multiple of 2^-36 of a, and not zero, so
-// a / b is at least 2^-12 steps away from c.  (Quotients below 2^-70 may be
-// off by more: their remainder is not exact.  They are never told from zero.)
+// between two floats: the border c has 25 bits, a - b c is a multiple of 2^-36
+// of a, and not zero, so a / b is at least 2^-12 steps away from c.  (Quotients
+// below 2^-70 may be off by more: their remainder is not exact.  They are never
+// told from zero.)
 __device__ __forceinline__ float quotient(float a, float b, float y) {
   const float q = __fmul_rn(a, y);
   return fmaf(fmaf(-q, b, a), y, q);
