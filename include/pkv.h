@@ -66,7 +66,8 @@ enum {
   PKV_DEV_BAD_CONTEXT = 2,   /* a context length outside [1, max_context_len] */
   PKV_DEV_BAD_SLOT = 3,      /* a slot >= num_blocks * block_size */
   PKV_DEV_TIMEOUT = 4,       /* a pipeline wait gave up (should never happen) */
-  PKV_DEV_BAD_POSITION = 5   /* a position outside [0, max_position) */
+  PKV_DEV_BAD_POSITION = 5,  /* a position outside [0, max_position) */
+  PKV_DEV_BAD_STARTS = 6     /* query or key starts that fall or pass the rows' end */
 };
 
 /* Shape of one paged cache and of the batch that reads it.
@@ -402,6 +403,94 @@ int pkv_kv4_decode_plan(const pkv_shape* shape, int32_t num_sms, pkv_plan* plan)
 
 /* Workspace bytes pkv_kv4_attn_decode needs for `shape` (0 if none). */
 int pkv_kv4_workspace_bytes(const pkv_shape* shape, size_t* bytes);
+
+/*
+ * Attention of a chunk of new tokens over the paged cache: a prompt's next
+ * chunk, a scheduler's mixed step, the verification of drafted tokens.  The
+ * tokens' keys and values are in the cache already (pkv_rope_append).
+ * Sequence i has the query rows [query_starts[i], query_starts[i + 1]), n of
+ * them, and L = context_lens[i] cached tokens that count them.  With k_t and
+ * v_t as for pkv_paged_attn_decode, its j-th row stands at position p = L - n
+ * + j and sees the tokens up to it:
+ *     out[row][h][:] = sum_{t <= p} softmax_t(scale * q[row][h] . k_t) * v_t
+ * A row that sees no token (p < 0) is set to zero.
+ *
+ *   shape         as for pkv_paged_attn_decode; num_seqs is B, kernel must be
+ *                 0; split_tokens > 0 sets the keys per partition (rounded up
+ *                 to a key tile, 128 tokens, 64 at head_dim 256)
+ *   q             [T, Hq, D], 16-byte aligned, q_stride elements from one
+ *                 token's row to the next: a multiple of 8, at least Hq * D; 0
+ *                 means dense
+ *   query_starts  [B + 1] int32, 0 <= s_0 <= s_1 <= ... <= s_B <= T.  Rows that
+ *                 no sequence has are left as they were in out.
+ *   context_lens  [B] int32, each in [0, max_context_len]
+ *   out           [T, Hq, D] dense, 16-byte aligned, not overlapping q
+ *   workspace     as for pkv_paged_attn_decode, pkv_chunk_workspace_bytes long
+ * A sequence whose length (PKV_DEV_BAD_CONTEXT) or rows (PKV_DEV_BAD_STARTS)
+ * are out of range is skipped and its out rows are left as they were.  An
+ * out-of-range block id among a sequence's ceil(L / bs) is not read
+ * (PKV_DEV_BAD_BLOCK_ID), and that sequence's out rows are undefined.
+ * num_seqs == 0 or num_tokens == 0 is a no-op.
+ */
+int pkv_paged_attn_chunk(const pkv_shape* shape, const void* q, int64_t q_stride,
+                         int32_t num_tokens, const int32_t* query_starts,
+                         const void* k_cache, const void* v_cache,
+                         const int32_t* block_tables, const int32_t* context_lens,
+                         float scale, void* out, void* workspace,
+                         size_t workspace_bytes, pkv_stream_t stream);
+
+/* Workspace bytes pkv_paged_attn_chunk needs for `shape` and num_tokens query
+ * rows on the current device (0 if none). */
+int pkv_chunk_workspace_bytes(const pkv_shape* shape, int32_t num_tokens, size_t* bytes);
+
+/*
+ * Attention over prompts packed one after the other.
+ *   num_seqs      B
+ *   num_tokens    T, query rows of all sequences; num_keys: S, key rows
+ *   causal        not 0: a query sees the keys up to its own position, the
+ *                 last query standing at the last key; 0: all keys
+ *   split_tokens  as for pkv_paged_attn_chunk
+ *   q_stride, k_stride, v_stride  elements from one token's row to the next
+ *                 (a fused projection's output has all three in one row): a
+ *                 multiple of 8, at least heads * head_dim; 0 means dense
+ */
+typedef struct {
+  int32_t num_seqs;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t num_tokens;
+  int32_t num_keys;
+  int32_t dtype;
+  int32_t causal;
+  int32_t split_tokens;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+} pkv_prompt;
+
+/*
+ * For the n query rows [query_starts[i], query_starts[i + 1]) of sequence i
+ * and its L keys and values, rows [key_starts[i], key_starts[i + 1]) of k and
+ * v, as pkv_paged_attn_chunk: row j sees key t where t <= L - n + j, or every
+ * key without `causal`; a row that sees no key is set to zero.
+ *
+ *   q, k, v       [T, Hq, D], [S, Hkv, D], [S, Hkv, D], 16-byte aligned, with
+ *                 the token strides of `prompt`
+ *   query_starts, key_starts  [B + 1] int32, from 0 up, not falling, at most T
+ *                 and S; the same array where keys and queries are the same
+ *                 tokens
+ *   out           [T, Hq, D] dense, 16-byte aligned, not overlapping q, k, v
+ *   workspace     pkv_prompt_workspace_bytes long; NULL takes the workspace
+ *                 set with pkv_set_workspace
+ * A sequence whose starts fall or pass T or S (PKV_DEV_BAD_STARTS) is skipped.
+ */
+int pkv_prompt_attn(const pkv_prompt* prompt, const void* q, const void* k, const void* v,
+                    const int32_t* query_starts, const int32_t* key_starts, float scale,
+                    void* out, void* workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+/* Workspace bytes pkv_prompt_attn needs for `prompt` on the current device. */
+int pkv_prompt_workspace_bytes(const pkv_prompt* prompt, size_t* bytes);
 
 /*
  * Block manager (host only, no GPU calls): the bookkeeping side of the paged

@@ -10,6 +10,8 @@ from ._binding import (  # noqa: F401
     PkvError,
     copy_blocks,
     alloc_workspace,
+    chunk_shape,
+    chunk_workspace_bytes,
     decode_plan,
     decode_shape,
     decode_step,
@@ -24,7 +26,11 @@ from ._binding import (  # noqa: F401
     kv_cache_append,
     launch_count,
     load_library,
+    paged_attn_chunk,
     paged_attn_decode,
+    prompt_attn,
+    prompt_shape,
+    prompt_workspace_bytes,
     rope_append,
     rope_table,
     selftest_wait_timeout,

@@ -42,6 +42,12 @@ class Rope(ctypes.Structure):
                 + [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")])
 
 
+class Prompt(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in (
+        "num_seqs", "num_q_heads", "num_kv_heads", "head_dim", "num_tokens", "num_keys", "dtype",
+        "causal", "split_tokens")] + [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")])
+
+
 class Plan(ctypes.Structure):
     _fields_ = [("schedule", ctypes.c_int32), ("split_tokens", ctypes.c_int32),
                 ("num_splits", ctypes.c_int32),
@@ -113,6 +119,15 @@ def load_library(path: str | None = None):
     lib.pkv_kv4_decode_plan.restype = ctypes.c_int
     lib.pkv_kv4_workspace_bytes.argtypes = [sp, ctypes.POINTER(sz)]
     lib.pkv_kv4_workspace_bytes.restype = ctypes.c_int
+    lib.pkv_paged_attn_chunk.argtypes = [sp, vp, i64, i32, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, sz, vp]
+    lib.pkv_paged_attn_chunk.restype = ctypes.c_int
+    lib.pkv_chunk_workspace_bytes.argtypes = [sp, i32, ctypes.POINTER(sz)]
+    lib.pkv_chunk_workspace_bytes.restype = ctypes.c_int
+    pp = ctypes.POINTER(Prompt)
+    lib.pkv_prompt_attn.argtypes = [pp, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, sz, vp]
+    lib.pkv_prompt_attn.restype = ctypes.c_int
+    lib.pkv_prompt_workspace_bytes.argtypes = [pp, ctypes.POINTER(sz)]
+    lib.pkv_prompt_workspace_bytes.restype = ctypes.c_int
     lib.pkv_get_device_error.argtypes = [i32p, vp]
     lib.pkv_get_device_error.restype = ctypes.c_int
     lib.pkv_selftest_wait_timeout.argtypes = [i32, vp]
@@ -759,6 +774,187 @@ def kv4_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         None if workspace is None else workspace.data_ptr(), _nbytes(workspace), ptr)
     if rc:
         raise PkvError("pkv_kv4_attn_decode", rc)
+    return out
+
+
+def chunk_shape(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tensor,
+                max_context_len: int | None = None, split_tokens: int = 0) -> Shape:
+    """decode_shape for paged_attn_chunk: q [T, Hq, D], a sequence per row of
+    block_tables."""
+    return Shape.from_buffer_copy(_chunk_sized(q, k_cache, block_tables, max_context_len, split_tokens))
+
+
+def _chunk_sized(q, k_cache, block_tables, max_context_len, split_tokens) -> Shape:
+    (_, Hq, D), (NB, Hkv, bs, _), (B, MB) = q.shape, k_cache.shape, block_tables.shape
+    return _sized(B, Hq, Hkv, D, bs, NB, MB, MB * bs if max_context_len is None else int(max_context_len),
+                  _dtype_code(q.dtype), int(split_tokens))
+
+
+def chunk_workspace_bytes(shape: Shape, num_tokens: int) -> int:
+    """Workspace bytes paged_attn_chunk needs for `shape` (chunk_shape) and that
+    many query rows."""
+    n = ctypes.c_size_t(0)
+    _check("pkv_chunk_workspace_bytes",
+           load_library().pkv_chunk_workspace_bytes(ctypes.byref(shape), int(num_tokens), ctypes.byref(n)))
+    return int(n.value)
+
+
+def prompt_shape(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, query_starts: torch.Tensor, *,
+                 causal: bool = True, split_tokens: int = 0) -> Prompt:
+    """The sizes of a prompt_attn call, for prompt_workspace_bytes."""
+    qs = _token_stride(q, "q", q.shape[1], q.shape[2], q.shape[0], q.dtype)
+    ks, vs = (_token_stride(t, n, k.shape[1], q.shape[2], k.shape[0], q.dtype) for t, n in ((k, "k"), (v, "v")))
+    return Prompt.from_buffer_copy(_prompt(query_starts.shape[0] - 1, q.shape[1], k.shape[1], q.shape[2], q.shape[0],
+                                           k.shape[0], _dtype_code(q.dtype), bool(causal), int(split_tokens),
+                                           qs, ks, vs))
+
+
+@functools.lru_cache(maxsize=256)
+def _prompt(*fields) -> Prompt:
+    """The Prompt of these fields, made once.  Read only."""
+    for (n, t), x in zip(Prompt._fields_, fields):
+        if t is ctypes.c_int32 and not -2 ** 31 <= x < 2 ** 31:      # the struct would hold other numbers
+            raise ValueError(f"{n} must fit 32 bits, got {x}")
+    prompt = Prompt(*fields)
+    prompt.ref, prompt.workspace = ctypes.byref(prompt), {}
+    return prompt
+
+
+def prompt_workspace_bytes(prompt: Prompt) -> int:
+    """Workspace bytes prompt_attn needs for `prompt` (prompt_shape)."""
+    n = ctypes.c_size_t(0)
+    _check("pkv_prompt_workspace_bytes",
+           load_library().pkv_prompt_workspace_bytes(ctypes.byref(prompt), ctypes.byref(n)))
+    return int(n.value)
+
+
+def _starts(t: torch.Tensor, name: str):
+    """Refuse what is no [B + 1] array of starts."""
+    _dense(t, name, _I32)
+    if t.dim() != 1 or t.shape[0] < 1:
+        raise ValueError(f"{name} must be [B + 1]")
+
+
+def _check_out(out, q, workspace):
+    if out is not None:
+        _dense(out, "out", q.dtype)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape [T, Hq, D]")
+    if workspace is not None:
+        _dense(workspace, "workspace")
+
+
+def paged_attn_chunk(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     block_tables: torch.Tensor, context_lens: torch.Tensor,
+                     query_starts: torch.Tensor, scale: float, out: torch.Tensor | None = None, *,
+                     max_context_len: int | None = None, split_tokens: int = 0,
+                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Causal attention of new tokens over the paged cache, which holds them
+    already: a prompt's next chunk, a mixed step, drafted tokens.
+
+    q [T, Hq, D]: the sequences' rows one after the other, heads dense, token
+    rows at any stride that is a multiple of 8 elements; sequence i has rows
+    query_starts[i] .. query_starts[i + 1] (int32 [B + 1]).  caches [NB, Hkv,
+    bs, D]; block_tables [B, MB] int32; context_lens [B] int32 count the new
+    tokens.  Row j of a sequence's n sees the tokens up to position
+    context_len - n + j.  Returns out [T, Hq, D] (allocated if not given; rows
+    of no sequence are not written).  workspace as for paged_attn_decode
+    (chunk_workspace_bytes).
+    """
+    _dense(k_cache, "k_cache")
+    _dense(v_cache, "v_cache", k_cache.dtype)
+    _dense(block_tables, "block_tables", _I32)
+    _dense(context_lens, "context_lens", _I32)
+    _starts(query_starts, "query_starts")
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("caches must be [NB, Hkv, bs, D] tensors of one shape")
+    if q.dim() != 3 or q.shape[2] != k_cache.shape[3]:
+        raise ValueError("q must be [T, Hq, D] with the caches' head_dim")
+    B = query_starts.shape[0] - 1
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
+        raise ValueError("block_tables must be [B, MB], context_lens [B], query_starts [B + 1]")
+    T, Hq, D = q.shape
+    q_stride = _token_stride(q, "q", Hq, D, T, k_cache.dtype)
+    _check_out(out, q, workspace)
+    dev = _one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                      context_lens=context_lens, query_starts=query_starts, out=out, workspace=workspace)
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return paged_attn_chunk(q, k_cache, v_cache, block_tables, context_lens, query_starts, scale,
+                                    out, max_context_len=max_context_len, split_tokens=split_tokens,
+                                    workspace=workspace, stream=stream)
+    ptr = _launch_stream(stream, dev)
+    shape = _chunk_sized(q, k_cache, block_tables, max_context_len, split_tokens)
+    n = 0
+    if workspace is None and dev.index not in _SET_WS:
+        n = chunk_workspace_bytes(shape, T)
+    if n or out is None:
+        with _allocating_on(stream):
+            workspace = torch.empty(n, dtype=_U8, device=dev) if n else workspace
+            out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev) if out is None else out
+    rc = (_LIB or load_library()).pkv_paged_attn_chunk(
+        shape.ref, q.data_ptr(), q_stride, T, query_starts.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), float(scale),
+        out.data_ptr(), None if workspace is None else workspace.data_ptr(), _nbytes(workspace), ptr)
+    if rc:
+        raise PkvError("pkv_paged_attn_chunk", rc)
+    return out
+
+
+def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, query_starts: torch.Tensor,
+                scale: float, out: torch.Tensor | None = None, *,
+                key_starts: torch.Tensor | None = None, causal: bool = True, split_tokens: int = 0,
+                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention over prompts packed one after the other.
+
+    q [T, Hq, D]; k, v [S, Hkv, D]: heads dense, token rows at any stride that
+    is a multiple of 8 elements (slices of a fused projection).  Sequence i has
+    the query rows query_starts[i] .. query_starts[i + 1] and the key rows
+    key_starts[i] .. key_starts[i + 1] (int32 [B + 1]; None: query_starts).
+    causal: a query sees the keys up to its position, the last query standing
+    at the last key (more keys than queries: a prefix).  A row that sees no key
+    is zero.  Returns out [T, Hq, D] (allocated if not given; rows of no
+    sequence are not written).  workspace as for paged_attn_decode
+    (prompt_workspace_bytes).
+    """
+    if key_starts is None:
+        key_starts = query_starts
+    _starts(query_starts, "query_starts")
+    _starts(key_starts, "key_starts")
+    if key_starts.shape != query_starts.shape:
+        raise ValueError("key_starts must be [B + 1] like query_starts")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [T, Hq, D]; k, v [S, Hkv, D]")
+    (T, Hq, D), (S, Hkv, _) = q.shape, k.shape
+    code = _dtype_code(q.dtype)
+    qs = _token_stride(q, "q", Hq, D, T, q.dtype)
+    ks = _token_stride(k, "k", Hkv, D, S, q.dtype)
+    vs = _token_stride(v, "v", Hkv, D, S, q.dtype)
+    _check_out(out, q, workspace)
+    dev = _one_device(q=q, k=k, v=v, query_starts=query_starts, key_starts=key_starts, out=out,
+                      workspace=workspace)
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return prompt_attn(q, k, v, query_starts, scale, out, key_starts=key_starts, causal=causal,
+                               split_tokens=split_tokens, workspace=workspace, stream=stream)
+    ptr = _launch_stream(stream, dev)
+    prompt = _prompt(query_starts.shape[0] - 1, Hq, Hkv, D, T, S, code, bool(causal), int(split_tokens),
+                     qs, ks, vs)
+    n = 0
+    if workspace is None and dev.index not in _SET_WS:
+        n = prompt.workspace.get(dev.index)
+        if n is None:
+            n = prompt.workspace[dev.index] = prompt_workspace_bytes(prompt)
+    if n or out is None:
+        with _allocating_on(stream):
+            workspace = torch.empty(n, dtype=_U8, device=dev) if n else workspace
+            out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev) if out is None else out
+    rc = (_LIB or load_library()).pkv_prompt_attn(
+        prompt.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), query_starts.data_ptr(),
+        key_starts.data_ptr(), float(scale), out.data_ptr(),
+        None if workspace is None else workspace.data_ptr(), _nbytes(workspace), ptr)
+    if rc:
+        raise PkvError("pkv_prompt_attn", rc)
     return out
 
 

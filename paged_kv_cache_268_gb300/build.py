@@ -34,7 +34,8 @@ def nvcc() -> str:
 def _units():
     units = [("pkv_api", "pkv_api.cu", []), ("pkv_noalloc", "pkv_noalloc.cu", []),
              ("pkv_blocks", "pkv_blocks.cpp", []), ("pkv_decode_tc", "pkv_decode_tc.cu", []),
-             ("pkv_rope", "pkv_rope.cu", []), ("pkv_kv4_decode", "pkv_kv4_decode.cu", [])]
+             ("pkv_rope", "pkv_rope.cu", []), ("pkv_prefill", "pkv_prefill.cu", []),
+             ("pkv_kv4_decode", "pkv_kv4_decode.cu", [])]
     for bf in (0, 1):
         units.append((f"pkv_kv4_{'bf16' if bf else 'f16'}", "pkv_kv4_inst.cu", [f"-DPKV_INST_BF16={bf}"]))
         for mma in (0, 1):

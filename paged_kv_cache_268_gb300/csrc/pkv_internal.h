@@ -17,7 +17,8 @@ enum : int {
   kDevBadContext = 2,
   kDevBadSlot = 3,
   kDevTimeout = 4,
-  kDevBadPosition = 5
+  kDevBadPosition = 5,
+  kDevBadStarts = 6
 };
 
 // Largest number of KV blocks one CTA's partition may span.
