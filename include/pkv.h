@@ -355,6 +355,35 @@ int pkv_kv4_append(const pkv_shape* shape, const pkv_rope* rope, const void* q,
                    pkv_stream_t stream);
 
 /*
+ * Positions of several axes (time, height and width of an image's or a video's
+ * patches; text counts on in all of them).  The channel pairs are cut into
+ * consecutive sections, one an axis; pairs of axis x turn by the position in
+ * row x of `positions`.
+ *   num_axes      1 .. 4
+ *   sections      channel pairs of each axis, not negative, R / 2 in all (rows
+ *                 of multiples of eight pairs, of four when interleaved, are
+ *                 read faster)
+ */
+typedef struct {
+  int32_t num_axes;
+  int32_t sections[4];
+} pkv_rope_axes;
+
+/* pkv_rope_append and pkv_kv4_append with positions [num_axes][num_tokens]:
+ * pair i's c_i and s_i come from the row of its axis' position.  rot_dim must
+ * not be 0.  A token is skipped when any of its positions is out of range. */
+int pkv_rope_append_axes(const pkv_shape* shape, const pkv_rope* rope,
+                         const pkv_rope_axes* axes, const void* q, const void* k,
+                         const void* v, const int32_t* positions, const float* cos_sin,
+                         const int32_t* slot_mapping, int32_t num_tokens, void* q_out,
+                         void* k_cache, void* v_cache, pkv_stream_t stream);
+int pkv_kv4_append_axes(const pkv_shape* shape, const pkv_rope* rope,
+                        const pkv_rope_axes* axes, const void* q, const void* k,
+                        const void* v, const int32_t* positions, const float* cos_sin,
+                        const int32_t* slot_mapping, int32_t num_tokens, void* q_out,
+                        void* k_cache, void* v_cache, pkv_stream_t stream);
+
+/*
  * Read rows of the 4-bit cache back in 16 bits (a prefix for the attention of
  * a prompt's next chunk, an export): for every token t and kv head h,
  *     k[t][h][:] and v[t][h][:] = the values at slot_mapping[t],

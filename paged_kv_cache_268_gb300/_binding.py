@@ -42,6 +42,10 @@ class Rope(ctypes.Structure):
                 + [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")])
 
 
+class RopeAxes(ctypes.Structure):
+    _fields_ = [("num_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4)]
+
+
 class Prompt(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int32) for n in (
         "num_seqs", "num_q_heads", "num_kv_heads", "head_dim", "num_tokens", "num_keys", "dtype",
@@ -110,6 +114,10 @@ def load_library(path: str | None = None):
     rp = ctypes.POINTER(Rope)
     for n in ("pkv_rope_append", "pkv_kv4_append"):
         getattr(lib, n).argtypes = [sp, rp, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp]
+        getattr(lib, n).restype = ctypes.c_int
+    ap = ctypes.POINTER(RopeAxes)
+    for n in ("pkv_rope_append_axes", "pkv_kv4_append_axes"):
+        getattr(lib, n).argtypes = [sp, rp, ap, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp]
         getattr(lib, n).restype = ctypes.c_int
     lib.pkv_kv4_gather.argtypes = [sp, vp, vp, vp, i32, vp, vp, vp]
     lib.pkv_kv4_gather.restype = ctypes.c_int
@@ -458,6 +466,16 @@ def _rope(*fields):
     return ctypes.byref(Rope(*fields))
 
 
+@functools.lru_cache(maxsize=256)
+def _axes(sections: tuple, rot: int):
+    """A reference to the RopeAxes of these sections, made once."""
+    if not 1 <= len(sections) <= 4 or any(n < 0 for n in sections):
+        raise ValueError("sections must be one to four numbers of channel pairs")
+    if 2 * sum(sections) != rot or rot == 0:
+        raise ValueError(f"sections must be {rot // 2} pairs in all (half of cos_sin's width), got {sections}")
+    return ctypes.byref(RopeAxes(len(sections), (ctypes.c_int32 * 4)(*sections)))
+
+
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -497,7 +515,7 @@ def _token_stride(t: torch.Tensor, name: str, heads: int, D: int, T: int, dtype)
 _I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
 
 
-def _append_plain(kv4: bool, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache):
+def _append_plain(kv4: bool, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, sections):
     """(NB, Hkv, bs, D) of the usual call (everything dense, on one GPU, of
     fitting sizes), of which _check_append would find nothing to refuse; else
     None.  A decode step makes this call for every layer, so it looks at each
@@ -513,7 +531,8 @@ def _append_plain(kv4: bool, q, k, v, positions, cos_sin, slot_mapping, k_cache,
     one = (T,)
     if (ks[1] == Hkv and W * 8 == D * 5 if kv4 else ks[1] == Hkv and W == D) and (
             v_cache.shape == cache and v.shape == ks and qs[0] == T and qs[2] == D and qs[1] > 0
-            and slot_mapping.shape == one and positions.shape == one
+            and slot_mapping.shape == one
+            and positions.shape == (one if sections is None else (len(sections), T))
             and k_cache.dtype is (_U8 if kv4 else dtype) and v_cache.dtype is k_cache.dtype
             and q.dtype is dtype and v.dtype is dtype and slot_mapping.dtype is _I32
             and positions.dtype is _I32 and cos_sin.dtype is _F32
@@ -528,7 +547,8 @@ def _append_plain(kv4: bool, q, k, v, positions, cos_sin, slot_mapping, k_cache,
     return None
 
 
-def _check_append(dims, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out, dtype):
+def _check_append(dims, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out, dtype,
+                  sections):
     """Refuse what does not fit together; the token strides of q, k and v."""
     NB, Hkv, bs, D = dims
     _dtype_code(dtype)
@@ -556,18 +576,24 @@ def _check_append(dims, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_ca
     if cos_sin is not None:
         _dense(positions, "positions", torch.int32)
         _dense(cos_sin, "cos_sin", torch.float32)
-        if positions.shape != (T,) or cos_sin.dim() != 2:
-            raise ValueError("positions must be [T], cos_sin [max_position, rot_dim]")
+        if positions.shape != ((T,) if sections is None else (len(sections), T)) or cos_sin.dim() != 2:
+            raise ValueError("positions must be [T] ([axes, T] with sections), cos_sin [max_position, rot_dim]")
+    elif sections is not None:
+        raise ValueError("sections without positions")
     _one_device(q=q, k=k, v=v, positions=positions, cos_sin=cos_sin, slot_mapping=slot_mapping,
                 k_cache=k_cache, v_cache=v_cache, q_out=q_out)
     return qs, ks, vs
 
 
 def _append(fn: str, kv4: bool, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache,
-            q_out, interleaved, stream):
+            q_out, interleaved, sections, stream):
     dims = None
+    if sections is not None:
+        sections = tuple(sections)
+        if any(type(n) is not int for n in sections):       # (8.0 would find the cached 8)
+            raise ValueError("sections must be whole numbers")
     if q_out is None:
-        dims = _append_plain(kv4, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache)
+        dims = _append_plain(kv4, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, sections)
     if dims is not None:
         dtype, qs, ks, vs = k.dtype, 0, 0, 0
     else:
@@ -580,15 +606,16 @@ def _append(fn: str, kv4: bool, q, k, v, positions, cos_sin, slot_mapping, k_cac
             if v_cache.shape != dims:
                 raise ValueError("caches must have one shape")
         qs, ks, vs = _check_append(dims, q, k, v, positions, cos_sin, slot_mapping, k_cache,
-                                   v_cache, q_out, dtype)
+                                   v_cache, q_out, dtype, sections)
     NB, Hkv, bs, D = dims
     T, dev = k.shape[0], k_cache.device
     if torch.cuda.current_device() != dev.index:
         with torch.cuda.device(dev):
             return _append(fn, kv4, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache,
-                           q_out, interleaved, stream)
+                           q_out, interleaved, sections, stream)
     Hq = 0 if q is None else q.shape[1]
     rows, rot = (0, 0) if cos_sin is None else cos_sin.shape
+    axes = None if sections is None else _axes(sections, rot)
     ptr = _launch_stream(stream, dev)
     if q is not None and q_out is None:
         if stream is None:
@@ -596,12 +623,16 @@ def _append(fn: str, kv4: bool, q, k, v, positions, cos_sin, slot_mapping, k_cac
         else:
             with torch.cuda.stream(stream):
                 q_out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
-    rc = getattr(_LIB or load_library(), fn)(
-        _sized(0, Hq or 1, Hkv, D, bs, NB, 1, 1, _DT[dtype]).ref,
-        _rope(rot, 1 if interleaved else 0, rows, qs, ks, vs), q.data_ptr() if Hq else None,
-        k.data_ptr(), v.data_ptr(), positions.data_ptr() if rot else None,
-        cos_sin.data_ptr() if rot else None, slot_mapping.data_ptr(), T,
-        q_out.data_ptr() if Hq else None, k_cache.data_ptr(), v_cache.data_ptr(), ptr)
+    args = (q.data_ptr() if Hq else None, k.data_ptr(), v.data_ptr(), positions.data_ptr() if rot else None,
+            cos_sin.data_ptr() if rot else None, slot_mapping.data_ptr(), T,
+            q_out.data_ptr() if Hq else None, k_cache.data_ptr(), v_cache.data_ptr(), ptr)
+    shape = _sized(0, Hq or 1, Hkv, D, bs, NB, 1, 1, _DT[dtype]).ref
+    rope = _rope(rot, 1 if interleaved else 0, rows, qs, ks, vs)
+    if sections is None:
+        rc = getattr(_LIB or load_library(), fn)(shape, rope, *args)
+    else:
+        fn += "_axes"
+        rc = getattr(_LIB or load_library(), fn)(shape, rope, axes, *args)
     if rc:
         raise PkvError(fn, rc)
     return q_out
@@ -611,7 +642,7 @@ def rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
                 positions: torch.Tensor | None, cos_sin: torch.Tensor | None,
                 slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                 q_out: torch.Tensor | None = None, *, interleaved: bool = False,
-                stream=None) -> torch.Tensor | None:
+                sections=None, stream=None) -> torch.Tensor | None:
     """Rotate q and k by their positions and append k and v to the 16-bit paged
     caches, in one launch.  Returns the rotated q.
 
@@ -621,20 +652,21 @@ def rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
     the rotated channels; both None: nothing is rotated.  slot_mapping [T]
     int32, negative: not stored.  q_out: allocated if not given; a dense q may
     be rotated in place (q_out=q).  interleaved: pairs are neighbours, not
-    halves.
+    halves.  sections: the channel pairs of each of up to four axes, R / 2 in
+    all; positions is then [axes, T], and a pair turns by its axis' position.
     """
     return _append("pkv_rope_append", False, q, k, v, positions, cos_sin, slot_mapping, k_cache,
-                   v_cache, q_out, interleaved, stream)
+                   v_cache, q_out, interleaved, sections, stream)
 
 
 def kv4_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
                positions: torch.Tensor | None, cos_sin: torch.Tensor | None,
                slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                q_out: torch.Tensor | None = None, *, interleaved: bool = False,
-               stream=None) -> torch.Tensor | None:
+               sections=None, stream=None) -> torch.Tensor | None:
     """rope_append into 4-bit caches (kv4_cache)."""
     return _append("pkv_kv4_append", True, q, k, v, positions, cos_sin, slot_mapping, k_cache,
-                   v_cache, q_out, interleaved, stream)
+                   v_cache, q_out, interleaved, sections, stream)
 
 
 def kv4_gather(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor,

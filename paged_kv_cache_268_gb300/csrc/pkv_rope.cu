@@ -15,6 +15,7 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMaxAxes = 4;
 
 struct RopeArgs {
   const uint16_t* q;            // [T, Hq, D] with a token stride, or null
@@ -31,6 +32,8 @@ struct RopeArgs {
   int T, Hq, Hkv, bs, bs_log2, NB;
   int rows;                                 // head rows of one slice
   int rot, inter, max_pos;
+  int axes;                                 // rows of positions, [axes, T]
+  int bound[kMaxAxes - 1];                  // first channel pair of axes 1, 2, ... (rot / 2: none)
 };
 
 template <bool BF>
@@ -138,7 +141,8 @@ struct TokenMeta {
   int known;   // the position has a table row
 };
 
-template <bool BF, int D, bool KV4>
+// AXES: positions of up to four axes; thread 0 stages the table row of each.
+template <bool BF, int D, bool KV4, bool AXES>
 __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int LPR = D / 8;              // lanes per row
   constexpr int R = kThreads / LPR;       // rows per pass
@@ -146,9 +150,10 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(cons
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[kStages];
   __shared__ TokenMeta meta[kStages];
+  __shared__ int axis_pos[kMaxAxes - 1];
   const int all = a.Hq + 2 * a.Hkv;
   const int ua = a.rows * blockIdx.y, n = min(a.rows, all - ua);   // rows of the slice
-  const int stage_bytes = a.rows * ROW + a.rot * 4;
+  const int stage_bytes = a.rows * ROW + (AXES ? a.axes : 1) * a.rot * 4;
   const uint32_t base = smem_u32(smem);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&bars[i]), 1);
@@ -158,10 +163,14 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(cons
   pdl_wait();
   pdl_launch_dependents();
 
-  // Thread 0: stage token `t`, whose position and slot are given.
-  auto issue = [&](int t, int pos, int slot, int st) {
+  // Thread 0: stage token `t`, whose position, further axes' positions and slot
+  // are given.
+  auto issue = [&](int t, int pos, const int (&more)[kMaxAxes - 1], int slot, int st) {
     const uint32_t bar = smem_u32(&bars[st]);
-    const bool known = a.rot == 0 || (pos >= 0 && pos < a.max_pos);
+    bool known = a.rot == 0 || (pos >= 0 && pos < a.max_pos);
+    if constexpr (AXES)
+#pragma unroll
+      for (int x = 1; x < kMaxAxes; ++x) known &= x >= a.axes || (more[x - 1] >= 0 && more[x - 1] < a.max_pos);
     const bool beyond = slot >= 0 && static_cast<long long>(slot) >= static_cast<long long>(a.NB) * a.bs;
     if (blockIdx.y == 0) {
       if (!known) record_error(a.err, kDevBadPosition);
@@ -174,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(cons
       return;
     }
     const int end = meta[st].slot >= 0 ? ua + n : min(ua + n, a.Hq);   // rows to fetch: [ua, end)
-    mbar_arrive_expect_tx(bar, max(end - ua, 0) * ROW + a.rot * 4);
+    mbar_arrive_expect_tx(bar, max(end - ua, 0) * ROW + (AXES ? a.axes : 1) * a.rot * 4);
     const uint32_t dst = base + st * stage_bytes;
     // rows [from, to) of one tensor whose first row is row `zero` of the token
     auto rows = [&](const uint16_t* x, long long stride, int zero, int heads) {
@@ -187,6 +196,11 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(cons
     rows(a.v, a.v_stride, a.Hq + a.Hkv, a.Hkv);
     if (a.rot > 0)
       bulk_load(dst + a.rows * ROW, a.cos_sin + static_cast<size_t>(pos) * a.rot, a.rot * 4, bar);
+    if constexpr (AXES)
+#pragma unroll
+      for (int x = 1; x < kMaxAxes; ++x)
+        if (x < a.axes)
+          bulk_load(dst + a.rows * ROW + x * a.rot * 4, a.cos_sin + static_cast<size_t>(more[x - 1]) * a.rot, a.rot * 4, bar);
   };
   const int gx = gridDim.x;
   int npos = 0, nslot = 0;                // of the next token to stage (thread 0)
@@ -194,6 +208,16 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(cons
     if (t < a.T) {
       npos = a.rot > 0 ? a.positions[t] : 0;
       nslot = a.slots[t];
+      if constexpr (AXES)                 // the further axes' positions, by way of shared memory
+        for (int x = 1; x < a.axes; ++x)
+          copy_async4(smem_u32(&axis_pos[x - 1]), a.positions + static_cast<size_t>(x) * a.T + t);
+    }
+  };
+  auto looked = [&](int (&more)[kMaxAxes - 1]) {
+    if constexpr (AXES) {
+      copy_async_wait();
+#pragma unroll
+      for (int x = 0; x < kMaxAxes - 1; ++x) more[x] = axis_pos[x];
     }
   };
   if (threadIdx.x == 0) {
@@ -202,8 +226,10 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(cons
       const int t = blockIdx.x + i * gx;
       if (t >= a.T) break;
       const int pos = npos, slot = nslot;
+      int more[kMaxAxes - 1];
+      looked(more);
       look(t + gx);
-      issue(t, pos, slot, i);
+      issue(t, pos, more, slot, i);
     }
   }
 
@@ -212,6 +238,11 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(cons
   const int partner = (first ? c * 8 + a.rot / 2 : c * 8 - a.rot / 2) * 2;   // byte of the other half's chunk
   const int i0 = a.inter ? c * 4 : (first ? c * 8 : c * 8 - a.rot / 2);
   const int g = c >> 2;
+  // The axis whose position turns pair i.  Sections of multiples of eight pairs
+  // (of four, interleaved) leave each lane's pairs in one axis.
+  auto axis_of = [&](int i) { return (i >= a.bound[0]) + (i >= a.bound[1]) + (i >= a.bound[2]); };
+  const int axis0 = AXES ? axis_of(i0) : 0;
+  const bool one_axis = !AXES || axis0 == axis_of(i0 + (a.inter ? 3 : 7));
   int st = 0;
   uint32_t phase = 0;
   bool failed = false;
@@ -226,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(cons
       float cs[8], sn[8];
       if (turned) {
         const float* row = reinterpret_cast<const float*>(stage + a.rows * ROW) + i0;
+        if constexpr (AXES) row += axis0 * a.rot;
         const float4 c0 = *reinterpret_cast<const float4*>(row);
         const float4 s0 = *reinterpret_cast<const float4*>(row + a.rot / 2);
         cs[0] = c0.x; cs[1] = c0.y; cs[2] = c0.z; cs[3] = c0.w;
@@ -235,6 +267,18 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(cons
           const float4 s1 = *reinterpret_cast<const float4*>(row + a.rot / 2 + 4);
           cs[4] = c1.x; cs[5] = c1.y; cs[6] = c1.z; cs[7] = c1.w;
           sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
+        }
+        if constexpr (AXES) {
+          if (!one_axis) {                    // some of the lane's pairs are of a later axis
+#pragma unroll
+            for (int j = 1; j < 8; ++j) {
+              const int x = axis_of(i0 + j);
+              if (x != axis0 && (j < 4 || !a.inter)) {
+                cs[j] = row[(x - axis0) * a.rot + j];
+                sn[j] = row[(x - axis0) * a.rot + a.rot / 2 + j];
+              }
+            }
+          }
         }
       }
       uint16_t* q_out = a.q_out + static_cast<size_t>(t) * a.Hq * D + c * 8;
@@ -300,9 +344,11 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(cons
       const int next = t + kStages * gx;
       if (next < a.T) {
         const int pos = npos, slot = nslot;
+        int more[kMaxAxes - 1];
+        looked(more);
         look(next + gx);
         fence_proxy_async_smem();
-        issue(next, pos, slot, st);
+        issue(next, pos, more, slot, st);
       }
     }
     if (++st == kStages) {
@@ -421,9 +467,9 @@ auto gather_kernel(bool bf, int D, int bs) {
 
 // The kernels' shared-memory limit, raised once per device and kernel (threads
 // that race here set the same attribute).
-cudaError_t raise_smem(const void* kern, bool kv4, bool bf, int D) {
-  static std::atomic<unsigned> masks[12];
-  std::atomic<unsigned>& mask = masks[(D == 64 ? 0 : (D == 128 ? 1 : 2)) * 4 + kv4 * 2 + bf];
+cudaError_t raise_smem(const void* kern, bool kv4, bool axes, bool bf, int D) {
+  static std::atomic<unsigned> masks[24];
+  std::atomic<unsigned>& mask = masks[(D == 64 ? 0 : (D == 128 ? 1 : 2)) * 8 + kv4 * 4 + axes * 2 + bf];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -434,8 +480,14 @@ cudaError_t raise_smem(const void* kern, bool kv4, bool bf, int D) {
   return e;
 }
 
+template <int D, bool KV4>
+auto append_kernel(bool bf, bool axes) {
+  if (axes) return bf ? rope_append_kernel<true, D, KV4, true> : rope_append_kernel<false, D, KV4, true>;
+  return bf ? rope_append_kernel<true, D, KV4, false> : rope_append_kernel<false, D, KV4, false>;
+}
+
 template <bool KV4>
-int append(const pkv_shape* s, const pkv_rope* rope, const void* q, const void* k, const void* v,
+int append(const pkv_shape* s, const pkv_rope* rope, const pkv_rope_axes* axes, const void* q, const void* k, const void* v,
            const int32_t* positions, const float* cos_sin, const int32_t* slots, int32_t num_tokens,
            void* q_out, void* k_cache, void* v_cache, pkv_stream_t stream) {
   if (!s || !rope) return PKV_ERR_NULL;
@@ -445,10 +497,23 @@ int append(const pkv_shape* s, const pkv_rope* rope, const void* q, const void* 
       (rope->rot_dim > 0 && rope->max_position < 1) || (q && s->num_q_heads < 1))
     return PKV_ERR_INVALID;
   if (rope->rot_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
-  const int D = s->head_dim;
+  const int D = s->head_dim, half = rope->rot_dim / 2;
+  RopeArgs a{};
+  a.axes = rope->rot_dim > 0 ? 1 : 0;
+  for (int x = 0; x < kMaxAxes - 1; ++x) a.bound[x] = half;
+  if (axes) {
+    if (axes->num_axes < 1 || axes->num_axes > kMaxAxes || rope->rot_dim == 0) return PKV_ERR_INVALID;
+    long long sum = 0;
+    for (int x = 0; x < axes->num_axes; ++x) {
+      if (axes->sections[x] < 0) return PKV_ERR_INVALID;
+      sum += axes->sections[x];
+      if (x + 1 < axes->num_axes) a.bound[x] = sum < half ? static_cast<int>(sum) : half;
+    }
+    if (sum != half) return PKV_ERR_INVALID;
+    a.axes = axes->num_axes;
+  }
   const long long qd = static_cast<long long>(s->num_q_heads) * D;
   const long long kd = static_cast<long long>(s->num_kv_heads) * D;
-  RopeArgs a{};
   a.q_stride = rope->q_stride ? rope->q_stride : qd;
   a.k_stride = rope->k_stride ? rope->k_stride : kd;
   a.v_stride = rope->v_stride ? rope->v_stride : kd;
@@ -488,16 +553,18 @@ int append(const pkv_shape* s, const pkv_rope* rope, const void* q, const void* 
   a.max_pos = rope->max_position;
   const bool bf = s->dtype == PKV_BF16;
   void (*kern)(RopeArgs) = nullptr;
-  if (D == 64) kern = bf ? rope_append_kernel<true, 64, KV4> : rope_append_kernel<false, 64, KV4>;
-  if (D == 128) kern = bf ? rope_append_kernel<true, 128, KV4> : rope_append_kernel<false, 128, KV4>;
-  if (D == 256) kern = bf ? rope_append_kernel<true, 256, KV4> : rope_append_kernel<false, 256, KV4>;
+  if (D == 64) kern = append_kernel<64, KV4>(bf, a.axes > 1);
+  if (D == 128) kern = append_kernel<128, KV4>(bf, a.axes > 1);
+  if (D == 256) kern = append_kernel<256, KV4>(bf, a.axes > 1);
   int sms = 0;
   rc = device_sms(&sms);
   if (rc != PKV_OK) return rc;
   // kAppendCtas CTAs per SM walk the tokens.  A slice has at most 24 KB of rows
   // (the CTAs' stages fit an SM's shared memory), and fewer where there are
   // not tokens enough for every CTA: down to one pass of the CTA's threads.
-  const int pass = kThreads / (D / 8), all = a.Hq + 2 * a.Hkv, most = kSliceBytes / (D * 2);
+  const int pass = kThreads / (D / 8), all = a.Hq + 2 * a.Hkv;
+  // (further axes' table rows take their place from the head rows)
+  const int most = (kSliceBytes - (a.axes > 1 ? (a.axes - 1) * a.rot * 4 : 0)) / (D * 2) / pass * pass;
   const int resident = kAppendCtas * sms;
   long long slices = (all + most - 1) / most;
   if (num_tokens * slices < resident) {
@@ -513,8 +580,8 @@ int append(const pkv_shape* s, const pkv_rope* rope, const void* q, const void* 
   if (walkers < 1) walkers = 1;
   const dim3 grid(static_cast<unsigned>(num_tokens < walkers ? num_tokens : walkers),
                   static_cast<unsigned>(slices));
-  const size_t smem = static_cast<size_t>(kStages) * (static_cast<size_t>(a.rows) * D * 2 + a.rot * 4);
-  cudaError_t e = raise_smem(reinterpret_cast<const void*>(kern), KV4, bf, D);
+  const size_t smem = static_cast<size_t>(kStages) * (static_cast<size_t>(a.rows) * D * 2 + a.axes * a.rot * 4);   // axes is 0 where rot is
+  cudaError_t e = raise_smem(reinterpret_cast<const void*>(kern), KV4, a.axes > 1, bf, D);
   if (e != cudaSuccess) return PKV_ERR_CUDA;
   e = launch_pdl(kern, grid, kThreads, smem, reinterpret_cast<cudaStream_t>(stream), a);
   if (e != cudaSuccess) return PKV_ERR_CUDA;
@@ -531,7 +598,7 @@ extern "C" int pkv_rope_append(const pkv_shape* s, const pkv_rope* rope, const v
                                const void* v, const int32_t* positions, const float* cos_sin,
                                const int32_t* slot_mapping, int32_t num_tokens, void* q_out,
                                void* k_cache, void* v_cache, pkv_stream_t stream) {
-  return append<false>(s, rope, q, k, v, positions, cos_sin, slot_mapping, num_tokens, q_out,
+  return append<false>(s, rope, nullptr, q, k, v, positions, cos_sin, slot_mapping, num_tokens, q_out,
                        k_cache, v_cache, stream);
 }
 
@@ -539,7 +606,25 @@ extern "C" int pkv_kv4_append(const pkv_shape* s, const pkv_rope* rope, const vo
                               const void* v, const int32_t* positions, const float* cos_sin,
                               const int32_t* slot_mapping, int32_t num_tokens, void* q_out,
                               void* k_cache, void* v_cache, pkv_stream_t stream) {
-  return append<true>(s, rope, q, k, v, positions, cos_sin, slot_mapping, num_tokens, q_out,
+  return append<true>(s, rope, nullptr, q, k, v, positions, cos_sin, slot_mapping, num_tokens, q_out,
+                      k_cache, v_cache, stream);
+}
+
+extern "C" int pkv_rope_append_axes(const pkv_shape* s, const pkv_rope* rope, const pkv_rope_axes* axes,
+                                    const void* q, const void* k, const void* v, const int32_t* positions,
+                                    const float* cos_sin, const int32_t* slot_mapping, int32_t num_tokens,
+                                    void* q_out, void* k_cache, void* v_cache, pkv_stream_t stream) {
+  if (!axes) return PKV_ERR_NULL;
+  return append<false>(s, rope, axes, q, k, v, positions, cos_sin, slot_mapping, num_tokens, q_out,
+                       k_cache, v_cache, stream);
+}
+
+extern "C" int pkv_kv4_append_axes(const pkv_shape* s, const pkv_rope* rope, const pkv_rope_axes* axes,
+                                   const void* q, const void* k, const void* v, const int32_t* positions,
+                                   const float* cos_sin, const int32_t* slot_mapping, int32_t num_tokens,
+                                   void* q_out, void* k_cache, void* v_cache, pkv_stream_t stream) {
+  if (!axes) return PKV_ERR_NULL;
+  return append<true>(s, rope, axes, q, k, v, positions, cos_sin, slot_mapping, num_tokens, q_out,
                       k_cache, v_cache, stream);
 }
 
