@@ -272,6 +272,28 @@ int cache_map(CUtensorMap* out, const void* base, const pkv_shape& s, bool three
 
 }  // namespace
 
+int block_map(CUtensorMap* out, const void* base, const pkv_shape& s) {
+  const int rc = get_encoder();
+  return rc != PKV_OK ? rc : cache_map(out, base, s, false);
+}
+
+int rows_map(CUtensorMap* out, const void* base, bool bf16, int head_dim, int heads, int64_t tokens,
+             int64_t stride, int box_heads, int box_tokens) {
+  const int rc = get_encoder();
+  if (rc != PKV_OK) return rc;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(heads),
+                        static_cast<cuuint64_t>(tokens)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2, static_cast<cuuint64_t>(stride) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r =
+      g_encode(out, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+               const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_CUDA;
+}
+
 // ------------------------------------------------------------------ checks
 int check_cache_shape(const pkv_shape* s) {
   if (!s) return PKV_ERR_NULL;

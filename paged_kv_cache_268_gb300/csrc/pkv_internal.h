@@ -85,6 +85,14 @@ int check_decode_shape(const pkv_shape*);    // the same for a decode batch
 int device_sms(int* sms);                    // SM count of the current device
 // Workspace set for the current device with pkv_set_workspace, or {nullptr, 0}.
 int device_workspace(void** ptr, size_t* bytes);
+// Tensor map of a cache in boxes of one block's rows and 64 channels (x channel,
+// y row of [NB, Hkv, bs]), 128-byte swizzled.
+int block_map(CUtensorMap* out, const void* base, const pkv_shape& s);
+// Tensor map of packed rows [tokens, heads, head_dim], `stride` elements between
+// tokens, in boxes of 64 channels x box_heads x box_tokens, 128-byte swizzled.
+// What lies past the last token reads as zero.
+int rows_map(CUtensorMap* out, const void* base, bool bf16, int head_dim, int heads, int64_t tokens,
+             int64_t stride, int box_heads, int box_tokens);
 void count_launch();                         // one more kernel for pkv_launch_count
 
 // Launch with programmatic stream serialisation: the grid may become resident
