@@ -20,6 +20,7 @@ __global__ void __launch_bounds__(kReduceThreads) prefill_reduce_kernel(const __
   constexpr int C = D / 32, BN = prefill_key_tile(D);
   pdl_wait();
   pdl_launch_dependents();
+  if (a.plan[a.B].parts == 0) return;
   const int lane = threadIdx.x & 31, warps = gridDim.x * (kReduceThreads / 32);
   const long long rows = static_cast<long long>(a.T) * a.Hq;
   for (long long row = blockIdx.x * (kReduceThreads / 32) + (threadIdx.x >> 5); row < rows; row += warps) {
@@ -93,7 +94,8 @@ CallSizes call_sizes(int B, int T, int Hq, int Hkv, int D, int max_keys, int spl
       const long long many = 2ll * kPrefillUnits * sms * 128 * prefill_row_tiles(D);
       if (c.rows > few + many) c.rows = few + many;
     }
-    c.plan_bytes = (static_cast<size_t>(B) * sizeof(PrefillPlan) + 15) / 16 * 16;
+    static_assert(sizeof(PrefillPlan) == 16, "what follows the plan is aligned");
+    c.plan_bytes = (static_cast<size_t>(B) + 1) * sizeof(PrefillPlan);
     c.bytes = c.plan_bytes + static_cast<size_t>(c.rows) * (D * 4 + 8);
   }
   // every sequence's last item may be a small one

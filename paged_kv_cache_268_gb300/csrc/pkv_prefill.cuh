@@ -9,13 +9,13 @@
 // (sequence, key head), over the keys that its rows see, or a partition of
 // them.  The CTAs, one an SM, take the items in turn.
 //
-//   warps 0-3, 4-7  softmax of row tile 0 and 1; a thread owns a row
-//   warp 8          producer: Q by TMA, K and V tiles into a ring of slots
-//   warp 9          issues the matrix products
-//   warp 10         finds the CTA's next item, one ahead
+//   softmax     eight warps a row tile: a thread has a row and half of the keys
+//   producer    a warp: Q by TMA, K and V tiles into a ring of slots
+//   issuer      a warp that issues the matrix products
+//   scheduler   a warp that finds the CTA's next item, one ahead
 //
 // S = Q K^T (both K-major in shared memory) goes to TMEM; a softmax thread
-// reads its row, p = 2^(s c - m c), and writes P over S in 16 bits, from where
+// reads its half row, p = 2^(s c - m c), and writes P over S in 16 bits, from where
 // it is the first operand of O += P V (V read MN-major from its tile).  While
 // one row tile is in softmax, the tensor cores work on the other: P0 V, S0 of
 // the next keys, P1 V, S1 of the next keys.  With a single row tile the two S
@@ -47,6 +47,8 @@ struct PrefillLayout {
   static constexpr int NQ = prefill_row_tiles(D);
   static constexpr int BN = prefill_key_tile(D);
   static constexpr int PANELS = D / 64;             // 128-byte columns of a row
+  static constexpr int SOFT = 8 * NQ;               // softmax warps
+  static constexpr int THREADS = (SOFT + 4) * 32;
   static constexpr int Q_TILE = 128 * D * 2;
   static constexpr int KV_TILE = BN * D * 2;
   static constexpr int STAGES = D == 64 ? 8 : 5;
@@ -54,20 +56,20 @@ struct PrefillLayout {
   static constexpr int OFF_BAR = OFF_KV + STAGES * KV_TILE;
   static constexpr int KV_FULL = 0, KV_EMPTY = STAGES, Q_FULL = 2 * STAGES, Q_EMPTY = Q_FULL + 1,
                        S_FULL = Q_FULL + 2, P_FULL = S_FULL + 3, O_DONE = P_FULL + 3,
-                       O_FREE = O_DONE + 2, I_FULL = O_FREE + 2, I_EMPTY = I_FULL + 2,
-                       NBAR = I_EMPTY + 2;
+                       O_LAST = O_DONE + 2, O_FREE = O_LAST + 2, I_FULL = O_FREE + 2,
+                       I_EMPTY = I_FULL + 2, NBAR = I_EMPTY + 2;
   static constexpr int OFF_ITEM = OFF_BAR + NBAR * 8;
   static constexpr int OFF_TMEM = OFF_ITEM + 2 * 80;
-  static constexpr int BYTES = OFF_TMEM + 16 + 1024;
+  static constexpr int OFF_XCH = OFF_TMEM + 16;     // [NQ][2][128] floats
+  static constexpr int BYTES = OFF_XCH + NQ * 1024;
   // S buffer 0, 1: of row tile 0, 1; 2: buffer 1 with a single row tile (a
   // barrier of its own, so that each has one group of softmax warps only)
   static constexpr int S_COL(int s) { return s > 0 ? BN : 0; }
   static constexpr int O_COL(int x) { return 256 + x * D; }
+  // P of keys 16 kk .. 16 kk + 15: each half of the keys over its own half of S
+  static constexpr int P_COL(int kk) { return kk < BN / 32 ? kk * 8 : BN / 2 + (kk - BN / 32) * 8; }
   static_assert(BYTES <= 227 * 1024, "shared memory");
 };
-
-constexpr int kPrefillThreads = 384;
-constexpr int kPrefillRegs = 168;     // a thread's at launch, which setmaxnreg shares out anew
 
 struct PrefillItem {
   int work;                      // 0: no more items
@@ -122,14 +124,48 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v) {
       : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem], one elected thread.
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t accumulate) {
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// Matrix products that the whole warp reaches and the lane with `leader` issues:
+// without a branch, the descriptors stay in uniform registers.  A descriptor is
+// its low word (address, leading offset) and a constant high word.
+//   D[tmem] (+)= A[smem] * B[smem]
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                        uint32_t accumulate, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+//   D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                        uint32_t accumulate, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_if(uint32_t bar, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(leader)
       : "memory");
 }
 
@@ -213,29 +249,32 @@ __device__ __forceinline__ int2 prefill_parts(const PrefillArgs& a, long long to
 }
 
 template <bool BF, int D>
-__global__ void __launch_bounds__(kPrefillThreads, 1)
+__global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
     prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ CUtensorMap tmQ,
                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV) {
   using LY = PrefillLayout<D>;
   constexpr int BN = LY::BN, ST = LY::STAGES, PANELS = LY::PANELS;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  constexpr int SOFT = LY::SOFT;
+  extern __shared__ __align__(1024) uint8_t smem[];   // swizzle atoms are 1024 bytes
   const uint32_t sb = smem_u32(smem);
   auto bar = [&](int i) { return sb + LY::OFF_BAR + 8 * i; };
   auto item_at = [&](int i) { return reinterpret_cast<PrefillItem*>(smem + LY::OFF_ITEM + (i & 1) * 80); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + LY::OFF_TMEM);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(kFullMask, tid >> 5, 0), lane = tid & 31;
   const int TPT = 128 / a.G;                       // tokens of a row tile
 
   if (tid < LY::NBAR) {
     int count = 1;
-    if (tid >= LY::P_FULL && tid < LY::P_FULL + 3) count = 4;
-    if (tid >= LY::O_FREE && tid < LY::O_FREE + 2) count = 4;
-    if (tid >= LY::I_EMPTY && tid < LY::I_EMPTY + 2) count = 10;
+    if (tid >= LY::P_FULL && tid < LY::P_FULL + 3) count = 8;
+    if (tid >= LY::O_FREE && tid < LY::O_FREE + 2) count = 8;
+    if (tid >= LY::I_EMPTY && tid < LY::I_EMPTY + 2) count = SOFT + 2;
     mbar_init(bar(tid), count);
   }
-  if (warp == 8 && lane == 0) {
+  if (sb & 1023) {                                 // (never: the array is aligned)
+    if (tid == 0) record_error(a.err, kDevTimeout);
+    return;
+  }
+  if (warp == SOFT && lane == 0) {
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
@@ -252,9 +291,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   pdl_launch_dependents();
   bool fail = false;
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (warp == 10) {
+  if (warp >= SOFT) {
+    if (warp == SOFT + 2) {
       // -------------------------------------------------------- next item
       // Sequences are looked at 32 at a time, a lane each.  Within a sequence
       // the last rows, which see most, come first.
@@ -299,6 +337,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           if (b0 + lane < a.B) a.plan[b0 + lane] = PrefillPlan{cut.x, cut.y, row};
           rows_before = __shfl_sync(kFullMask, row + (cut.x > 1 ? static_cast<long long>(s.n) * a.Hq * cut.x : 0), 31);
         }
+        if (lane == 0) a.plan[a.B] = PrefillPlan{rows_before > 0, 0, rows_before};
         rows_before = 0;
       }
       look(0);
@@ -356,19 +395,21 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         ++slot;
         if (!it.work) break;
       }
-    } else if (warp == 8) {
+    } else if (warp == SOFT) {
       // -------------------------------------------------------- producer
       const uint64_t stream_policy = l2_policy_evict_first();
       uint64_t keep_policy;
       asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep_policy));
       const bool paged = a.key_starts == nullptr;
       const int past = paged ? static_cast<int>((static_cast<long long>(a.NB) * a.Hkv) << a.bs_log2) : 0;
-      int ring = 0, qs = 0;                         // tiles and queries loaded so far
-      for (int slot = 0;; ++slot) {
-        if (!__all_sync(kFullMask, mbar_wait(bar(LY::I_FULL + (slot & 1)), (slot >> 1) & 1))) {
-          fail = true;
-          break;
-        }
+      int at = 0, loaded = 0;                       // slot, tiles so far
+      uint32_t phase = 0, qs = 0;                   // of the slot; queries loaded so far
+      auto wait = [&](int b, uint32_t parity) {
+        if (!__all_sync(kFullMask, mbar_wait(bar(b), parity))) fail = true;
+      };
+      for (int slot = 0; !fail; ++slot) {
+        wait(LY::I_FULL + (slot & 1), (slot >> 1) & 1);
+        if (fail) break;
         const PrefillItem it = *item_at(slot);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(LY::I_EMPTY + (slot & 1)));
@@ -391,17 +432,14 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           return (id * a.Hkv + it.kvh) << a.bs_log2;
         };
         int y = paged ? row_of(it.t0) : 0;
-        for (int i = 0; i < n && !fail; ++i) {
+        for (int i = 0; i < n; ++i) {
           const int y_next = paged && i + 1 < n ? row_of(it.t0 + i + 1) : 0;
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            const int sl = ring % ST;
-            if (ring >= ST && !__all_sync(kFullMask, mbar_wait(bar(LY::KV_EMPTY + sl), ((ring / ST) - 1) & 1))) {
-              fail = true;
-              break;
-            }
+            wait(LY::KV_EMPTY + at, phase ^ 1);     // (a slot's first use does not wait)
+            if (fail) break;
             const CUtensorMap* map = kv ? &tmV : &tmK;
-            const uint32_t full = bar(LY::KV_FULL + sl), dst = sb + LY::OFF_KV + sl * LY::KV_TILE;
+            const uint32_t full = bar(LY::KV_FULL + at), dst = sb + LY::OFF_KV + at * LY::KV_TILE;
             if (lane == 0) mbar_arrive_expect_tx(full, LY::KV_TILE);
             __syncwarp();
             if (paged) {
@@ -410,13 +448,15 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             } else if (lane < PANELS) {
               tma_load_3d(dst + lane * (BN * 128), map, lane * 64, it.kvh, it.key_base + (it.t0 + i) * BN, full, policy);
             }
-            ++ring;
-            if (i == 0 && kv == 0) {
+            ++loaded;
+            if (++at == ST) {
+              at = 0;
+              phase ^= 1;
+            }
+            if (kv == 0 && i == 0) {
               const int tiles = it.two ? 2 : 1;
-              if (qs > 0 && !__all_sync(kFullMask, mbar_wait(bar(LY::Q_EMPTY), (qs - 1) & 1))) {
-                fail = true;
-                break;
-              }
+              wait(LY::Q_EMPTY, (qs & 1) ^ 1);
+              if (fail) break;
               if (lane == 0) mbar_arrive_expect_tx(bar(LY::Q_FULL), tiles * PANELS * TPT * a.G * 128);
               __syncwarp();
               if (lane < tiles * PANELS) {
@@ -427,13 +467,13 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
               ++qs;
             }
           }
+          if (fail) break;
           y = y_next;
         }
-        if (fail) break;
       }
       // Nothing may land or arrive in this CTA's shared memory after it has
       // left: every slot's last load was read and its release has come.
-      for (int r = max(0, ring - ST); r < ring; ++r) {
+      for (int r = max(0, loaded - ST); r < loaded; ++r) {
         const bool landed = mbar_wait(bar(LY::KV_FULL + r % ST), (r / ST) & 1, 100000000ull);
         if (!fail && landed) mbar_wait(bar(LY::KV_EMPTY + r % ST), (r / ST) & 1, 100000000ull);
       }
@@ -441,119 +481,146 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         mbar_wait(bar(LY::Q_FULL), (qs - 1) & 1, 100000000ull);
         if (!fail) mbar_wait(bar(LY::Q_EMPTY), (qs - 1) & 1, 100000000ull);
       }
-    } else if (warp == 9) {
+    } else if (warp == SOFT + 1) {
       // -------------------------------------------------------- matrix products
-      if (lane == 0) {
-        const uint32_t idesc_qk = umma_idesc_f16(BF, 0, 0, BN, 128);
-        const uint32_t idesc_pv = umma_idesc_f16(BF, 0, 1, D, 128);
-        auto slot_of = [&](int r) { return sb + LY::OFF_KV + (r % ST) * LY::KV_TILE; };
-        auto landed = [&](int r) {
-          if (!mbar_wait(bar(LY::KV_FULL + r % ST), (r / ST) & 1)) fail = true;
-          return !fail;
-        };
-        auto qk = [&](int s, int x, int r) {        // S buffer s = Q tile x . K of ring tile r
-          tc_fence_after();
+      const uint32_t leader = elect_lane();
+      const uint32_t idesc_qk = umma_idesc_f16(BF, 0, 0, BN, 128);
+      const uint32_t idesc_pv = umma_idesc_f16(BF, 0, 1, D, 128);
+      // descriptors: eight rows of 128 bytes an atom (stride 1024), version 1,
+      // 128-byte swizzle; V's leading offset is from one 64-channel panel to the next
+      constexpr uint32_t kHi = (1024 >> 4) | 1u << 14 | 2u << 29;
+      const uint32_t q_lo = (sb >> 4) | 1u << 16, k_lo = ((sb + LY::OFF_KV) >> 4) | 1u << 16;
+      const uint32_t v_lo = ((sb + LY::OFF_KV) >> 4) | (BN * 128u >> 4) << 16;
+      auto qk = [&](int s, int x, int at) {         // S buffer s = Q tile x . K of slot `at`
+        tc_fence_after();
+        const uint32_t a_lo = q_lo + x * (LY::Q_TILE >> 4), b_lo = k_lo + at * (LY::KV_TILE >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t ad = umma_desc_sw128(sb + x * LY::Q_TILE + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024);
-            const uint64_t bd = umma_desc_sw128(slot_of(r) + (kk >> 2) * (BN * 128) + (kk & 3) * 32, 16, 1024);
-            umma_f16(tmem + LY::S_COL(s), ad, bd, idesc_qk, kk > 0 ? 1u : 0u);
-          }
-          umma_commit(bar(LY::S_FULL + s));
-        };
-        auto pv = [&](int s, int x, int r, bool first) {   // O tile x += P of buffer s . V of ring tile r
-          tc_fence_after();
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_ss(tmem + LY::S_COL(s), a_lo + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2,
+                  b_lo + (kk >> 2) * (BN * 128 >> 4) + (kk & 3) * 2, kHi, idesc_qk, kk > 0, leader);
+        umma_commit_if(bar(LY::S_FULL + s), leader);
+      };
+      auto pv = [&](int s, int x, int at, bool first, bool last) {   // O tile x += P of buffer s . V of slot `at`
+        tc_fence_after();
+        const uint32_t b_lo = v_lo + at * (LY::KV_TILE >> 4);
 #pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk) {
-            const uint64_t bd = umma_desc_sw128(slot_of(r) + kk * 2048, BN * 128, 1024);
-            umma_f16_ts(tmem + LY::O_COL(x), tmem + LY::S_COL(s) + kk * 8, bd, idesc_pv, !first || kk > 0 ? 1u : 0u);
-          }
-          umma_commit(bar(LY::O_DONE + x));
-        };
-        int ring = 0, qs = 0, su[3] = {0, 0, 0}, ou[2] = {0, 0};   // S buffers' and O tiles' uses so far
-        auto have_p = [&](int s, int x, bool first) {
-          // P of S buffer s has been written; before the first product of an item O must be free
-          if (!mbar_wait(bar(LY::P_FULL + s), su[s] & 1)) fail = true;
-          ++su[s];
-          if (!fail && first) {
-            if (ou[x] > 0 && !mbar_wait(bar(LY::O_FREE + x), (ou[x] - 1) & 1)) fail = true;
-            ++ou[x];
-          }
-          return !fail;
-        };
-        for (int slot = 0; !fail; ++slot) {
-          if (!mbar_wait(bar(LY::I_FULL + (slot & 1)), (slot >> 1) & 1)) {
-            fail = true;
-            break;
-          }
-          const PrefillItem it = *item_at(slot);
-          mbar_arrive(bar(LY::I_EMPTY + (slot & 1)));
-          if (!it.work) break;
-          const int n0 = it.n0, n1 = it.n1, n = max(n0, n1);
-          if (n == 0) continue;
-          if (!mbar_wait(bar(LY::Q_FULL), qs & 1)) {
-            fail = true;
-            break;
-          }
-          ++qs;
-          // ring tile of K(i) is ring + 2 i, of V(i) the one after
-          if (!landed(ring)) break;
-          if (it.two) {
-            if (n0 > 0) qk(0, 0, ring);
-            if (n1 > 0) qk(1, 1, ring);
-          } else {
-            qk(0, 0, ring);
-          }
-          umma_commit(bar(LY::KV_EMPTY + ring % ST));
-          if (n == 1) umma_commit(bar(LY::Q_EMPTY));
+        for (int kk = 0; kk < BN / 16; ++kk)
+          umma_ts(tmem + LY::O_COL(x), tmem + LY::S_COL(s) + LY::P_COL(kk), b_lo + kk * (2048 >> 4), kHi, idesc_pv,
+                  !first || kk > 0, leader);
+        umma_commit_if(bar(LY::O_DONE + x), leader);
+        if (last) umma_commit_if(bar(LY::O_LAST + x), leader);
+      };
+      // The ring's tiles come K(0) V(0) K(1) V(1) ...; slots and phases of the
+      // next tile that is waited for and of the next to be released.
+      int at = 0;
+      uint32_t phase = 0;
+      auto landed = [&] {
+        if (!__all_sync(kFullMask, mbar_wait(bar(LY::KV_FULL + at), phase))) fail = true;
+        const int slot = at;
+        if (++at == ST) {
+          at = 0;
+          phase ^= 1;
+        }
+        return slot;
+      };
+      uint32_t qs = 0, su0 = 0, su1 = 0, su2 = 0, ou0 = 0, ou1 = 0;   // uses so far: Q, S buffers, O tiles
+      auto have_p = [&](int s, uint32_t& uses) {    // P of S buffer s has been written
+        if (!__all_sync(kFullMask, mbar_wait(bar(LY::P_FULL + s), uses & 1))) fail = true;
+        ++uses;
+      };
+      auto have_o = [&](int x, uint32_t& uses) {    // O tile x has been read by the item before
+        if (uses > 0 && !__all_sync(kFullMask, mbar_wait(bar(LY::O_FREE + x), (uses - 1) & 1))) fail = true;
+        ++uses;
+      };
+      for (int slot = 0; !fail; ++slot) {
+        if (!__all_sync(kFullMask, mbar_wait(bar(LY::I_FULL + (slot & 1)), (slot >> 1) & 1))) {
+          fail = true;
+          break;
+        }
+        const PrefillItem* item = item_at(slot);
+        const int work = item->work, two = item->two, n0 = item->n0, n1 = item->n1, n = max(n0, n1);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(LY::I_EMPTY + (slot & 1)));
+        if (!work) break;
+        if (n == 0) continue;
+        if (!__all_sync(kFullMask, mbar_wait(bar(LY::Q_FULL), qs & 1))) {
+          fail = true;
+          break;
+        }
+        ++qs;
+        int k = landed();
+        if (fail) break;
+        if (!two || n0 > 0) qk(0, 0, k);
+        if (LY::NQ == 2 && n1 > 0) qk(1, 1, k);
+        umma_commit_if(bar(LY::KV_EMPTY + k), leader);
+        if (n == 1) umma_commit_if(bar(LY::Q_EMPTY), leader);
+        if (LY::NQ == 2 && two) {
           for (int i = 0; i < n; ++i) {
-            const int rv = ring + 2 * i + 1, rk = rv + 1;
-            const bool more = i + 1 < n;
-            if (it.two) {
-              if (!landed(rv)) break;
-              if (i < n0) {
-                if (!have_p(0, 0, i == 0)) break;
-                pv(0, 0, rv, i == 0);
-              }
-              if (more && !landed(rk)) break;
-              if (i + 1 < n0) qk(0, 0, rk);
-              if (i < n1) {
-                if (!have_p(1, 1, i == 0)) break;
-                pv(1, 1, rv, i == 0);
-              }
-              umma_commit(bar(LY::KV_EMPTY + rv % ST));
-              if (i + 1 < n1) qk(1, 1, rk);
-              if (more) umma_commit(bar(LY::KV_EMPTY + rk % ST));
-            } else {
-              if (more) {
-                if (!landed(rk)) break;
-                qk(i & 1 ? 0 : 2, 0, rk);
-                umma_commit(bar(LY::KV_EMPTY + rk % ST));
-              }
-              const int sp = i & 1 ? 2 : 0;
-              if (!landed(rv) || !have_p(sp, 0, i == 0)) break;
-              pv(sp, 0, rv, i == 0);
-              umma_commit(bar(LY::KV_EMPTY + rv % ST));
+            const int v = landed();
+            if (i + 1 < n) k = landed();
+            if (i < n0) {
+              have_p(0, su0);
+              if (i == 0) have_o(0, ou0);
+              if (fail) break;
+              pv(0, 0, v, i == 0, i + 1 == n0);
             }
-            if (i + 2 == n) umma_commit(bar(LY::Q_EMPTY));
+            if (fail) break;
+            if (i + 1 < n0) qk(0, 0, k);
+            if (i < n1) {
+              have_p(1, su1);
+              if (i == 0) have_o(1, ou1);
+              if (fail) break;
+              pv(1, 1, v, i == 0, i + 1 == n1);
+            }
+            umma_commit_if(bar(LY::KV_EMPTY + v), leader);
+            if (i + 1 < n1) qk(1, 1, k);
+            if (i + 1 < n) umma_commit_if(bar(LY::KV_EMPTY + k), leader);
+            if (i + 2 == n) umma_commit_if(bar(LY::Q_EMPTY), leader);
           }
-          ring += 2 * n;
+        } else {
+          for (int i = 0; i < n; ++i) {
+            const int v = landed();
+            if (i + 1 < n) {
+              k = landed();
+              if (fail) break;
+              qk(i & 1 ? 0 : 2, 0, k);
+              umma_commit_if(bar(LY::KV_EMPTY + k), leader);
+            }
+            if (i & 1) have_p(2, su2); else have_p(0, su0);
+            if (i == 0) have_o(0, ou0);
+            if (fail) break;
+            pv(i & 1 ? 2 : 0, 0, v, i == 0, i + 1 == n);
+            umma_commit_if(bar(LY::KV_EMPTY + v), leader);
+            if (i + 2 == n) umma_commit_if(bar(LY::Q_EMPTY), leader);
+          }
         }
       }
-      __syncwarp();
     }
   } else {
     // ---------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // Warps w and w + 4 of a row tile have the same rows and a half of the keys
+    // each (and of the output's channels); they meet at a barrier of their own.
+    // So none of them leaves an item early: after a failed wait a warp skips its
+    // later waits and runs on with whatever is there, and at the item's end the
+    // two leave together.
     constexpr float kShift = BF ? 0.f : 7.f;        // P is 2^kShift times the weight
-    const int w = warp >> 2, r = tid & 127;         // row tile, row
+    constexpr int HN = BN / 2, HD = D / 2;
+    const int w = warp >> 3, h = (warp >> 2) & 1, pair = 1 + w * 4 + (warp & 3);
+    const int r = (warp & 3) * 32 + lane;           // row of the tile
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    float* xch = reinterpret_cast<float*>(smem + LY::OFF_XCH) + w * 256;
+    float *own = xch + h * 128 + r, *others = xch + (h ^ 1) * 128 + r;
     const int tl = r / a.G;                         // token of the row within its tile
     const bool has_token = tl < TPT;
     const float c = a.scale_log2;
-    int ring = 0, su = 0, su2 = 0, od = 0;          // ring tiles, S buffers' uses, own O tile's products so far
-    for (int slot = 0; !fail; ++slot) {
-      if (!__all_sync(kFullMask, mbar_wait(bar(LY::I_FULL + (slot & 1)), (slot >> 1) & 1))) {
+    // ring tiles, S buffers' uses, own O tile's products and its items so far
+    int ring = 0, su = 0, su2 = 0, od = 0, outs = 0;
+    auto wait = [&](int b, uint32_t parity) {
+      if (!fail && !__all_sync(kFullMask, mbar_wait(bar(b), parity))) fail = true;
+    };
+    for (int slot = 0;; ++slot) {
+      wait(LY::I_FULL + (slot & 1), (slot >> 1) & 1);
+      if (named_bar_or(pair, 64, fail)) {
         fail = true;
         break;
       }
@@ -568,37 +635,32 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       float2 l2 = make_float2(0.f, 0.f);
       for (int i = 0; i < n; ++i) {
         const int s = two ? w : (i & 1 ? 2 : 0);
-        if (!__all_sync(kFullMask, mbar_wait(bar(LY::S_FULL + s), (s == 2 ? su2 : su) & 1))) {
-          fail = true;
-          break;
-        }
+        wait(LY::S_FULL + s, (s == 2 ? su2 : su) & 1);
         s == 2 ? ++su2 : ++su;
         tc_fence_after();
-        float x[BN];
+        const uint32_t mine = lanes + LY::S_COL(s) + h * HN;
+        float x[HN];
 #pragma unroll
-        for (int q = 0; q < BN / 32; ++q) tmem_ld32(lanes + LY::S_COL(s) + q * 32, x + q * 32);
+        for (int q = 0; q < HN / 32; ++q) tmem_ld32(mine + q * 32, x + q * 32);
         tmem_wait_ld();
 #pragma unroll
-        for (int q = 0; q < BN / 32; ++q) tmem_ready32(x + q * 32);
-        const int key0 = (t0 + i) * BN;
+        for (int q = 0; q < HN / 32; ++q) tmem_ready32(x + q * 32);
+        const int key0 = (t0 + i) * BN, col0 = key0 + h * HN;
         if (a.negative) {
 #pragma unroll
-          for (int e = 0; e < BN; ++e) x[e] = -x[e];
+          for (int e = 0; e < HN; ++e) x[e] = -x[e];
         }
-        if (__any_sync(kFullMask, valid && key0 + BN - 1 > lim)) {
+        if (__any_sync(kFullMask, valid && col0 + HN - 1 > lim)) {
 #pragma unroll
-          for (int e = 0; e < BN; ++e) x[e] = key0 + e <= lim ? x[e] : -INFINITY;
+          for (int e = 0; e < HN; ++e) x[e] = col0 + e <= lim ? x[e] : -INFINITY;
         }
-        // values that some row must not see (the first softmax warps to work on the tile)
+        // values that some row must not see (the first row tile's warps that work on the keys)
         if ((w == 0 || i >= n0) && key0 + BN > (a.causal ? min(L, off + 1) : L)) {
           const int rv = ring + 2 * i + 1;
-          if (!__all_sync(kFullMask, mbar_wait(bar(LY::KV_FULL + rv % ST), (rv / ST) & 1))) {
-            fail = true;
-            break;
-          }
+          wait(LY::KV_FULL + rv % ST, (rv / ST) & 1);
           const uint32_t tile = sb + LY::OFF_KV + (rv % ST) * LY::KV_TILE;
           const int first = max(0, (a.causal ? min(L, off + 1) : L) - key0), end = L - key0;
-          for (int u = first * (D / 8) + r; u < BN * (D / 8); u += 128) {
+          for (int u = first * (D / 8) + h * 128 + r; u < BN * (D / 8); u += 256) {
             const int vr = u / (D / 8), ch = u % (D / 8);
             const uint32_t at = tile + (ch >> 3) * (BN * 128) + vr * 128 + (ch & 7) * 16;
             uint32_t d[4] = {0, 0, 0, 0};
@@ -627,35 +689,32 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         }
         float top[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) top[q] = x[q];
+        for (int q = 0; q < 4; ++q) top[q] = fmaxf(x[q], x[4 + q]);
 #pragma unroll
-        for (int e = 4; e < BN; e += 8) {
+        for (int e = 8; e < HN; e += 8) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (e + 4 + q < BN)
-              top[q] = fmaxf(top[q], fmaxf(x[e + q], x[e + 4 + q]));
-            else
-              top[q] = fmaxf(top[q], x[e + q]);
-          }
+          for (int q = 0; q < 4; ++q) top[q] = fmaxf(top[q], fmaxf(x[e + q], x[e + 4 + q]));
         }
         const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        if (i == 0) {
-          m = mt;
-        } else if (__any_sync(kFullMask, (mt - m) * c > 8.f)) {
-          // raise the reference: O holds the products up to the last tile's
-          const float up = fmaxf(m, mt), keep = m == -INFINITY ? 0.f : fast_exp2((m - up) * c);
-          if (!__all_sync(kFullMask, mbar_wait(bar(LY::O_DONE + w), (od + i - 1) & 1))) {
-            fail = true;
-            break;
-          }
-          tc_fence_after();
+        if (named_bar_or(pair, 64, i == 0 || (mt - m) * c > 8.f)) {
+          // raise the reference to the whole row's maximum
+          *own = mt;
+          named_bar_sync(pair, 64);
+          const float up = fmaxf(m, fmaxf(mt, *others)), keep = m == -INFINITY ? 0.f : fast_exp2((m - up) * c);
+          if (i > 0) {
+            // O holds the products up to the last tile's.  (That barrier is at
+            // this phase or the next: the one before had ended when S was
+            // there, the one after waits for this tile's P.)
+            wait(LY::O_DONE + w, (od + i - 1) & 1);
+            tc_fence_after();
 #pragma unroll
-          for (int q = 0; q < D / 16; ++q) {
-            float o[16];
-            tmem_ld16(lanes + LY::O_COL(w) + q * 16, o);
+            for (int q = 0; q < HD / 16; ++q) {
+              float o[16];
+              tmem_ld16(lanes + LY::O_COL(w) + h * HD + q * 16, o);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] *= keep;
-            tmem_st16(lanes + LY::O_COL(w) + q * 16, o);
+              for (int e = 0; e < 16; ++e) o[e] *= keep;
+              tmem_st16(lanes + LY::O_COL(w) + h * HD + q * 16, o);
+            }
           }
           l2.x *= keep;
           l2.y *= keep;
@@ -665,7 +724,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
         float2 sum[2] = {l2, make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int q = 0; q < BN / 32; ++q) {
+        for (int q = 0; q < HN / 32; ++q) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -675,7 +734,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             sum[e & 1] = add2(sum[e & 1], p);
             pk[e] = pack2<BF>(p.x, p.y);
           }
-          tmem_st16u(lanes + LY::S_COL(s) + q * 16, pk);
+          tmem_st16u(mine + q * 16, pk);
         }
         l2 = add2(sum[0], sum[1]);
         tmem_wait_st();
@@ -683,19 +742,17 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(LY::P_FULL + s));
       }
-      if (fail) break;
       // -------------------------------------------------------- the item's rows out
-      const float l = l2.x + l2.y;
       if (n > 0) {
-        // (the last but one product may be under way as well where S runs ahead
-        // of it; a barrier must not be asked for a phase that is not its next)
-        if ((n > 1 && !__all_sync(kFullMask, mbar_wait(bar(LY::O_DONE + w), (od + n - 2) & 1))) ||
-            !__all_sync(kFullMask, mbar_wait(bar(LY::O_DONE + w), (od + n - 1) & 1))) {
-          fail = true;
-          break;
-        }
+        wait(LY::O_LAST + w, outs & 1);
+        ++outs;
         tc_fence_after();
       }
+      const bool left = named_bar_or(pair, 64, fail);   // (and the last maximum has been read)
+      float l = l2.x + l2.y;
+      *own = l;
+      named_bar_sync(pair, 64);
+      l += *others;
       const int kvh = item->kvh, parts = item->parts;
       const size_t row = (static_cast<size_t>(item->q_row + j) * a.Hq + kvh * a.G + (r - tl * a.G));
       size_t prow = 0;
@@ -705,10 +762,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       const float inv = parts > 1 ? 1.f : (l > 0.f ? 1.f / l : 0.f);
       const bool bad_values = n > 0 && item->bad_values;
 #pragma unroll 1
-      for (int q = 0; q < D / 32; ++q) {
+      for (int q = 0; q < HD / 32; ++q) {
+        const int ch0 = h * HD + q * 32;            // first channel
         float o[32];
         if (n > 0) {
-          tmem_ld32(lanes + LY::O_COL(w) + q * 32, o);
+          tmem_ld32(lanes + LY::O_COL(w) + ch0, o);
           tmem_wait_ld();
           tmem_ready32(o);
 #pragma unroll
@@ -727,7 +785,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
               }
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
-                const float2 y = unpack2<BF>(*reinterpret_cast<const uint32_t*>(v + q * 32 + e));
+                const float2 y = unpack2<BF>(*reinterpret_cast<const uint32_t*>(v + ch0 + e));
                 if (!(fabsf(y.x) <= 3.402823466e38f)) o[e] += y.x;
                 if (!(fabsf(y.y) <= 3.402823466e38f)) o[e + 1] += y.y;
               }
@@ -739,12 +797,12 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         }
         if (valid) {
           if (parts > 1) {
-            float* dst = a.part_o + prow * D + q * 32;
+            float* dst = a.part_o + prow * D + ch0;
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
               *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           } else {
-            uint16_t* dst = a.out + row * D + q * 32;
+            uint16_t* dst = a.out + row * D + ch0;
 #pragma unroll
             for (int e = 0; e < 32; e += 8)
               *reinterpret_cast<uint4*>(dst + e) =
@@ -753,13 +811,17 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           }
         }
       }
-      if (parts > 1 && valid)
+      if (parts > 1 && valid && h == 0)
         a.part_ml[prow] = make_float2(l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m * c) - kShift, l);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         if (n > 0) mbar_arrive(bar(LY::O_FREE + w));
         mbar_arrive(bar(LY::I_EMPTY + (slot & 1)));
+      }
+      if (left) {
+        fail = true;
+        break;
       }
       od += n;
       ring += 2 * max(n0, n1);

@@ -16,7 +16,7 @@ constexpr int kPrefillFewRows = 64;       // rows of a key head: cut finer up to
 constexpr int kPrefillFewUnits = 4;       // partitions a CTA's share of the work makes, few rows
 constexpr int kPrefillUnits = 2;          // and many
 
-// What the reduce has to know of a sequence.
+// What the reduce has to know of a sequence; a last one says whether any was cut.
 struct PrefillPlan {
   int parts;                     // partitions; below two: none were written
   int per;                       // key tiles of one
@@ -30,7 +30,7 @@ struct PrefillArgs {
   const int32_t* block_tables;   // paged: [B, MB]
   const uint16_t* v;             // packed: [S, Hkv, D]; paged: [NB, Hkv, bs, D]
   uint16_t* out;                 // [T, Hq, D]
-  PrefillPlan* plan;             // [B], or null: no sequence is cut
+  PrefillPlan* plan;             // [B + 1], or null: no sequence is cut
   float2* part_ml;               // (exponent, sum) of a partial row
   float* part_o;                 // its un-normalised output [D]
   int* err;

@@ -12,23 +12,18 @@ cudaError_t launch(const PrefillArgs& a, const CUtensorMap& q, const CUtensorMap
                    unsigned grid, cudaStream_t stream) {
   constexpr int SMEM = PrefillLayout<D>::BYTES;
   auto kern = prefill_kernel<BF, D>;
-  // once per device (every time past 32): the shared-memory limit, and that the
-  // registers which setmaxnreg shares out anew are there
+  // the shared-memory limit is raised once per device (every time past 32)
   static std::atomic<unsigned> mask{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned bit = dev < 32 ? 1u << dev : 0u;
   if (bit == 0 || !(mask.load(std::memory_order_acquire) & bit)) {
-    cudaFuncAttributes attr{};
-    e = cudaFuncGetAttributes(&attr, kern);
-    if (e != cudaSuccess) return e;
-    if (attr.numRegs != kPrefillRegs) return cudaErrorInvalidDeviceFunction;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
     mask.fetch_or(bit, std::memory_order_release);
   }
-  return launch_pdl(kern, dim3(grid), kPrefillThreads, SMEM, stream, a, q, k, v);
+  return launch_pdl(kern, dim3(grid), PrefillLayout<D>::THREADS, SMEM, stream, a, q, k, v);
 }
 
 template <bool BF>
