@@ -11,70 +11,71 @@ namespace pkv {
 namespace {
 
 constexpr int kReduceThreads = 256;
+constexpr int kReduceRows = 32;          // of a CTA
 
-// Joins the partitions of the sequences that were cut: a warp a (token, query
-// head) row, out = sum_p 2^(e_p - E) o_p / sum_p 2^(e_p - E) l_p with E the
-// largest exponent, in the partitions' order.
+// Joins the pieces of the items that were cut: out = sum_p 2^(e_p - E) o_p /
+// sum_p 2^(e_p - E) l_p with E the largest exponent, in the keys' order.  CTA
+// (c, y) looks after the item whose second piece attention's CTA c had, if it
+// had one, rows 32 y and up; a warp a row.
 template <bool BF, int D>
 __global__ void __launch_bounds__(kReduceThreads) prefill_reduce_kernel(const __grid_constant__ PrefillArgs a) {
-  constexpr int C = D / 32, BN = prefill_key_tile(D);
+  constexpr int C = D / 32;
   pdl_wait();
   pdl_launch_dependents();
-  if (a.plan[a.B].parts == 0) return;
-  const int lane = threadIdx.x & 31, warps = gridDim.x * (kReduceThreads / 32);
-  const long long rows = static_cast<long long>(a.T) * a.Hq;
-  for (long long row = blockIdx.x * (kReduceThreads / 32) + (threadIdx.x >> 5); row < rows; row += warps) {
-    const int t = static_cast<int>(row / a.Hq);
-    int lo = 0, hi = a.B;                    // the last sequence that starts at or before t
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (a.query_starts[mid] <= t) lo = mid; else hi = mid;
-    }
-    const PrefillPlan plan = a.plan[lo];
-    const int q0 = a.query_starts[lo], q1 = a.query_starts[lo + 1];
-    if (plan.parts < 2 || t < q0 || t >= q1) continue;
-    const int L = a.key_starts != nullptr ? a.key_starts[lo + 1] - a.key_starts[lo] : a.context_lens[lo];
-    const int lim = a.causal ? L - (q1 - t) : L - 1;           // last key that the row sees
-    const int parts = lim < 0 ? 0 : min(plan.parts, lim / (plan.per * BN) + 1);
-    const size_t from = static_cast<size_t>(plan.row) + (row - static_cast<long long>(q0) * a.Hq) * plan.parts;
-    float top = -INFINITY;
-    for (int p = lane; p < parts; p += 32) top = fmaxf(top, a.part_ml[from + p].x);
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+  const PrefillCut cut = a.cuts[c0];
+  const int rows = cut.ntok * a.G;
+  if (cut.kind != 2 || static_cast<int>(blockIdx.y) * kReduceRows >= rows) return;
+  for (int k = threadIdx.x >> 5; k < kReduceRows; k += kReduceThreads / 32) {
+    const int row = blockIdx.y * kReduceRows + k;
+    if (row >= rows) return;
+    float o[C] = {}, l = 0.f, top = -INFINITY;
+    // pieces: the first one, then c0's and those of the CTAs behind it
+    for (int c = c0, piece = 2 * cut.first + 1;;) {
+      const size_t at = static_cast<size_t>(piece) * a.rows + row;
+      const float2 ml = a.part_ml[at];
+      if (ml.y != 0.f) {
+        const float up = fmaxf(top, ml.x), keep = top == -INFINITY ? 0.f : fast_exp2(top - up);
+        const float w = fast_exp2(ml.x - up);
+        top = up;
+        l = fmaf(l, keep, w * ml.y);
+        const float2* src = reinterpret_cast<const float2*>(a.part_o + at * D + lane * C);
 #pragma unroll
-    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-    float o[C] = {}, l = 0.f;
-    for (int p = 0; p < parts; ++p) {
-      const float2 ml = a.part_ml[from + p];
-      if (ml.y == 0.f) continue;
-      const float w = fast_exp2(ml.x - top);
-      l = fmaf(w, ml.y, l);
-      const float2* src = reinterpret_cast<const float2*>(a.part_o + (from + p) * D + lane * C);
-#pragma unroll
-      for (int c = 0; c < C / 2; ++c) {
-        const float2 x = src[c];
-        o[2 * c] = fmaf(w, x.x, o[2 * c]);
-        o[2 * c + 1] = fmaf(w, x.y, o[2 * c + 1]);
+        for (int e = 0; e < C / 2; ++e) {
+          const float2 x = src[e];
+          o[2 * e] = fmaf(o[2 * e], keep, w * x.x);
+          o[2 * e + 1] = fmaf(o[2 * e + 1], keep, w * x.y);
+        }
       }
+      if (piece == 2 * cut.first + 1) {
+        piece = 2 * c;
+        continue;
+      }
+      if (a.cuts[c].ends) break;
+      do ++c; while (a.cuts[c].kind == 0);
+      piece = 2 * c;
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row * D + lane * C);
+    const size_t out = static_cast<size_t>(cut.q_row + row / a.G) * a.Hq + cut.kvh * a.G + row % a.G;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + out * D + lane * C);
 #pragma unroll
-    for (int c = 0; c < C / 2; ++c) dst[c] = pack2<BF>(o[2 * c] * inv, o[2 * c + 1] * inv);
+    for (int e = 0; e < C / 2; ++e) dst[e] = pack2<BF>(o[2 * e] * inv, o[2 * e + 1] * inv);
   }
 }
 
 template <bool BF>
-cudaError_t launch_reduce(const PrefillArgs& a, int D, unsigned grid, cudaStream_t stream) {
+cudaError_t launch_reduce(const PrefillArgs& a, int D, unsigned ctas, cudaStream_t stream) {
   auto kern = prefill_reduce_kernel<BF, 64>;
   if (D == 128) kern = prefill_reduce_kernel<BF, 128>;
   if (D == 256) kern = prefill_reduce_kernel<BF, 256>;
-  return launch_pdl(kern, dim3(grid), kReduceThreads, 0, stream, a);
+  return launch_pdl(kern, dim3(ctas, (a.rows + kReduceRows - 1) / kReduceRows), kReduceThreads, 0, stream, a);
 }
 
-// Sizes of a call: whether sequences may be cut, the workspace for that, the grid.
+// Sizes of a call: the grid, and the workspace where items may be cut.
 struct CallSizes {
-  int part_tiles;                // of a forced partition, else 0
-  long long rows;                // partial rows at most
-  size_t plan_bytes, bytes;
+  int min_part;                  // key tiles of a piece at least
+  int rows;                      // of an item at most
+  size_t cut_bytes, bytes;
   unsigned grid;
 };
 
@@ -82,25 +83,18 @@ CallSizes call_sizes(int B, int T, int Hq, int Hkv, int D, int max_keys, int spl
   CallSizes c{};
   const int BN = prefill_key_tile(D), G = Hq / Hkv;
   const int per_item = 128 / G * prefill_row_tiles(D);
-  c.part_tiles = (split_tokens + BN - 1) / BN;
-  const long long smallest = c.part_tiles ? static_cast<long long>(c.part_tiles) * BN : kPrefillMinPart;
-  const long long parts = (max_keys + smallest - 1) / smallest;    // of one sequence at most
-  if (parts > 1) {
-    c.rows = static_cast<long long>(T) * Hq * parts;
-    if (!c.part_tiles) {
-      // A sequence that is cut has at most twice the partitions that its key
-      // tiles are units (prefill_parts), and the units of all are a few a CTA.
-      const long long few = 2ll * kPrefillFewUnits * sms * kPrefillFewRows;
-      const long long many = 2ll * kPrefillUnits * sms * 128 * prefill_row_tiles(D);
-      if (c.rows > few + many) c.rows = few + many;
-    }
-    static_assert(sizeof(PrefillPlan) == 16, "what follows the plan is aligned");
-    c.plan_bytes = (static_cast<size_t>(B) + 1) * sizeof(PrefillPlan);
-    c.bytes = c.plan_bytes + static_cast<size_t>(c.rows) * (D * 4 + 8);
-  }
+  c.min_part = ((split_tokens > 0 ? split_tokens : kPrefillMinPart) - 1) / BN + 1;
+  c.rows = (T < per_item ? T : per_item) * G;
+  const int tiles = max_keys > 0 ? (max_keys - 1) / BN + 1 : 1;
+  const bool cuts = tiles >= 2ll * c.min_part;
   // every sequence's last item may be a small one
-  const long long items = (static_cast<long long>(T) / per_item + B) * Hkv * (parts > 1 ? parts : 1);
-  c.grid = static_cast<unsigned>(items < sms ? (items < 1 ? 1 : items) : sms);
+  const long long items = (static_cast<long long>(T) / per_item + B) * Hkv;
+  const long long pieces = items * (cuts ? tiles / c.min_part : 1);
+  c.grid = static_cast<unsigned>(pieces < sms ? pieces : sms);
+  if (cuts && c.grid > 1) {
+    c.cut_bytes = (c.grid * sizeof(PrefillCut) + 15) / 16 * 16;
+    c.bytes = c.cut_bytes + 2ull * c.grid * c.rows * (D * 4 + 8);
+  }
   return c;
 }
 
@@ -117,14 +111,14 @@ int launch(PrefillArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUt
     }
     if (!workspace || workspace_bytes < c.bytes || !aligned(workspace, 16)) return PKV_ERR_WORKSPACE;
     uint8_t* w = static_cast<uint8_t*>(workspace);
-    a.plan = reinterpret_cast<PrefillPlan*>(w);
-    a.part_o = reinterpret_cast<float*>(w + c.plan_bytes);
-    a.part_ml = reinterpret_cast<float2*>(w + c.plan_bytes + static_cast<size_t>(c.rows) * D * 4);
+    a.cuts = reinterpret_cast<PrefillCut*>(w);
+    a.part_o = reinterpret_cast<float*>(w + c.cut_bytes);
+    a.part_ml = reinterpret_cast<float2*>(w + c.cut_bytes + 2ull * c.grid * c.rows * D * 4);
   }
   a.err = device_error_word();
   if (!a.err) return PKV_ERR_CUDA;
-  a.part_tiles = c.part_tiles;
-  a.ctas = sms;
+  a.rows = c.rows;
+  a.min_part = c.min_part;
   a.negative = scale < 0.f;
   // (a factor of zero would turn a hidden key's minus infinity into no number)
   a.scale_log2 = fmaxf(fabsf(scale) * 1.4426950408889634f, 0x1p-126f);
@@ -133,9 +127,7 @@ int launch(PrefillArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUt
   if (e != cudaSuccess) return PKV_ERR_CUDA;
   count_launch();
   if (c.bytes > 0) {
-    const long long rows = static_cast<long long>(a.T) * a.Hq, ctas = (rows + kReduceThreads / 32 - 1) / (kReduceThreads / 32);
-    const unsigned grid = static_cast<unsigned>(ctas < 4ll * sms ? ctas : 4ll * sms);
-    e = bf ? launch_reduce<true>(a, D, grid, stream) : launch_reduce<false>(a, D, grid, stream);
+    e = bf ? launch_reduce<true>(a, D, c.grid, stream) : launch_reduce<false>(a, D, c.grid, stream);
     if (e != cudaSuccess) return PKV_ERR_CUDA;
     count_launch();
   }

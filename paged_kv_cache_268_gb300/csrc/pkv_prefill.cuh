@@ -6,13 +6,14 @@
 // token r / G, head r % G of its group, so grouped heads share every key tile
 // that is read, and a few new tokens of many heads still fill a tile (tiles
 // hold whole tokens: 128 / G of them).  An item is up to two row tiles of one
-// (sequence, key head), over the keys that its rows see, or a partition of
-// them.  The CTAs, one an SM, take the items in turn.
+// (sequence, key head), over the keys that its rows see, or a piece of them.
+// The CTAs, one an SM, share the items' keys out evenly among them.
 //
 //   softmax     eight warps a row tile: a thread has a row and half of the keys
 //   producer    a warp: Q by TMA, K and V tiles into a ring of slots
 //   issuer      a warp that issues the matrix products
 //   scheduler   a warp that finds the CTA's next item, one ahead
+//   values      a warp that looks V tiles over which hide something (below)
 //
 // S = Q K^T (both K-major in shared memory) goes to TMEM; a softmax thread
 // reads its half row, p = 2^(s c - m c), and writes P over S in 16 bits, from where
@@ -30,6 +31,7 @@
 // tiles that hide something from some row, values past the sequence's end are
 // cleared, and those that are no numbers as well (and kept in mind: at the
 // end they are added for the rows that see them, whose weights are positive).
+// A warp does so as the tiles land, before their products.
 //
 // Every wait is bounded; a role that gives up leaves, the others follow, and
 // the device error word is set.
@@ -57,7 +59,8 @@ struct PrefillLayout {
   static constexpr int KV_FULL = 0, KV_EMPTY = STAGES, Q_FULL = 2 * STAGES, Q_EMPTY = Q_FULL + 1,
                        S_FULL = Q_FULL + 2, P_FULL = S_FULL + 3, O_DONE = P_FULL + 3,
                        O_LAST = O_DONE + 2, O_FREE = O_LAST + 2, I_FULL = O_FREE + 2,
-                       I_EMPTY = I_FULL + 2, NBAR = I_EMPTY + 2;
+                       I_EMPTY = I_FULL + 2, V_HERE = I_EMPTY + 2, V_CLEAN = V_HERE + 2,
+                       NBAR = V_CLEAN + 2;
   static constexpr int OFF_ITEM = OFF_BAR + NBAR * 8;
   static constexpr int OFF_TMEM = OFF_ITEM + 2 * 80;
   static constexpr int OFF_XCH = OFF_TMEM + 16;     // [NQ][2][128] floats
@@ -80,11 +83,11 @@ struct PrefillItem {
   int off;                       // position of the first token
   int t0;                        // first key tile
   int n0, n1;                    // key tiles that row tile 0, 1 sees from there
+  int hidden;                    // of these, from here on some hide something from some row
   int key_base;                  // packed: row of the first key
   int once;                      // no other item reads these keys
-  int parts, part;
+  int piece;                     // of partial rows that the item's rows go to, or -1: whole
   int bad_values;                // values that are no numbers were cleared
-  long long row;                 // partial row of the sequence's first row
 };
 static_assert(sizeof(PrefillItem) <= 80, "item slot");
 
@@ -122,6 +125,27 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v) {
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
       "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+
+// mbar_wait in few instructions: a try sleeps for up to a microsecond, and after
+// half a million of them the wait gives up.
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 0;\n\t"
+      "TRY:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "@p bra DONE;\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.lt.u32 q, n, 500000;\n\t"
+      "@q bra TRY;\n\t"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(1000)
+      : "memory");
+  return ok != 0;
 }
 
 // One lane of a converged warp.
@@ -167,6 +191,19 @@ __device__ __forceinline__ void umma_commit_if(uint32_t bar, uint32_t leader) {
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
       "r"(leader)
       : "memory");
+}
+
+// 32 bytes to global memory: in one piece where the address is `wide`, aligned
+// to them, else in two.
+__device__ __forceinline__ void store32(uint16_t* p, const uint32_t (&v)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
 }
 
 // Pairs of floats in one instruction.
@@ -229,23 +266,42 @@ __device__ __forceinline__ PrefillSeq prefill_seq(const PrefillArgs& a, int b) {
   return s;
 }
 
-// Partitions of a sequence of `rows` rows a key head and `tiles` key tiles:
-// (count, tiles of each).  `total` is the key tiles of all items, `unit` keys
-// in tiles that make the smallest partition.  Items that are longer than a
-// half of a CTA's share of the work (a quarter where they have few rows, whose
-// partial results cost little) are cut to that length.
-__device__ __forceinline__ int2 prefill_parts(const PrefillArgs& a, long long total, int rows, int tiles,
-                                              int unit) {
-  if (a.plan == nullptr || rows == 0 || tiles == 0) return make_int2(1, max(tiles, 1));
-  long long most = a.part_tiles;
-  if (most == 0) {
-    const int units = a.ctas * (rows <= kPrefillFewRows ? kPrefillFewUnits : kPrefillUnits);
-    most = max(static_cast<long long>(unit), (total + units - 1) / units);
+// The work of one key head of a sequence, as a line: its row tiles (of `per`
+// tokens) one after the other, each as long as its keys and a constant.
+struct PrefillLine {
+  int n, L, per, tiles, causal;
+  __device__ __forceinline__ PrefillLine(int n_, int L_, int per_, int causal_)
+      : n(n_), L(L_), per(per_), tiles((n_ + per_ - 1) / per_), causal(causal_) {}
+  // keys that row tile t sees
+  __device__ __forceinline__ int keys(int t) const {
+    if (!causal) return L;
+    const long long last = static_cast<long long>(t + 1) * per;
+    return max(0, L - n + static_cast<int>(min(last, static_cast<long long>(n))));
   }
-  if (tiles <= most) return make_int2(1, tiles);
-  const int parts = static_cast<int>((tiles + most - 1) / most);
-  const int per = (tiles + parts - 1) / parts;
-  return make_int2((tiles + per - 1) / per, per);
+  __device__ __forceinline__ long long cost(int t) const { return static_cast<long long>(keys(t)) + kPrefillItemCost; }
+  // where row tile t begins
+  __device__ __forceinline__ long long begin(int t) const {
+    const long long own = static_cast<long long>(t) * kPrefillItemCost;
+    if (!causal) return own + static_cast<long long>(t) * L;
+    const long long d = static_cast<long long>(L) - n, blind = d < 0 ? -d / per : 0;   // tiles that see none
+    if (t <= blind) return own;
+    long long sum = (t - blind) * d + per * (t * (t + 1ll) - blind * (blind + 1)) / 2;
+    if (t == tiles) sum -= d + static_cast<long long>(t) * per - L;      // the last one is not whole
+    return own + sum;
+  }
+  __device__ __forceinline__ long long length() const { return begin(tiles); }
+};
+
+// Key tile of an item of `tiles` of them at which the line is cut `x` into the
+// item's `cost`: no piece is shorter than `least` tiles.
+__device__ __forceinline__ int prefill_cut(long long x, long long cost, int tiles, int least) {
+  if (x <= 0) return 0;
+  if (x >= cost) return tiles;
+  const int p = static_cast<int>((x * tiles + cost / 2) / cost);
+  if (tiles < 2 * least) return 2 * p <= tiles ? 0 : tiles;
+  if (p < least) return 2 * p <= least ? 0 : least;
+  if (tiles - p < least) return 2 * (tiles - p) <= least ? tiles : tiles - least;
+  return p;
 }
 
 template <bool BF, int D>
@@ -267,7 +323,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
     int count = 1;
     if (tid >= LY::P_FULL && tid < LY::P_FULL + 3) count = 8;
     if (tid >= LY::O_FREE && tid < LY::O_FREE + 2) count = 8;
-    if (tid >= LY::I_EMPTY && tid < LY::I_EMPTY + 2) count = SOFT + 2;
+    if (tid >= LY::I_EMPTY && tid < LY::I_EMPTY + 2) count = SOFT + 3;
     mbar_init(bar(tid), count);
   }
   if (sb & 1023) {                                 // (never: the array is aligned)
@@ -294,106 +350,124 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
   if (warp >= SOFT) {
     if (warp == SOFT + 2) {
       // -------------------------------------------------------- next item
-      // Sequences are looked at 32 at a time, a lane each.  Within a sequence
-      // the last rows, which see most, come first.
-      const int unit = max(1, kPrefillMinPart / BN);
+      // The lines of all sequences and key heads, one after the other, are cut
+      // into equal lengths, one a CTA; every CTA finds its own from the lengths
+      // on the device.  An item that a cut goes through is done in pieces, which
+      // the reduce joins (where a->cuts is null cuts move to the items' ends).
+      // Sequences are looked at 32 at a time, a lane each.
       const int per_item = TPT * LY::NQ;            // tokens
+      const int least = a.cuts != nullptr ? a.min_part : 0x3fffffff;
       long long total = 0;
-      auto tiles_of = [&](const PrefillSeq& s) { return (s.L + BN - 1) / BN; };
-      if (a.plan != nullptr && a.part_tiles == 0) {
-        for (int b = lane; b < a.B; b += 32) {
-          const PrefillSeq s = prefill_seq(a, b);
-          total += static_cast<long long>((s.n + per_item - 1) / per_item) * a.Hkv * tiles_of(s);
-        }
-#pragma unroll
-        for (int i = 16; i > 0; i >>= 1) total += __shfl_xor_sync(kFullMask, total, i);
-      }
-      int chunk = 0;
-      long long before = 0, rows_before = 0;        // items and partial rows of the chunks before
-      PrefillSeq s;
-      int2 cut;
-      long long mine, upto, row;                    // items of the lane's sequence, up to its end; its partial row
-      auto look = [&](int b0) {
-        s = prefill_seq(a, b0 + lane);
+#pragma unroll 4
+      for (int b = lane; b < a.B; b += 32) {
+        const PrefillSeq s = prefill_seq(a, b);
         if (s.code != 0 && blockIdx.x == 0) record_error(a.err, s.code);
-        cut = prefill_parts(a, total, s.n * a.G, tiles_of(s), unit);
-        mine = static_cast<long long>((s.n + per_item - 1) / per_item) * a.Hkv * cut.x;
-        const long long rows = cut.x > 1 ? static_cast<long long>(s.n) * a.Hq * cut.x : 0;
-        upto = mine;
-        row = rows;
+        total += PrefillLine(s.n, s.L, per_item, a.causal).length();
+      }
 #pragma unroll
-        for (int i = 1; i < 32; i <<= 1) {
-          const long long u = __shfl_up_sync(kFullMask, upto, i), r = __shfl_up_sync(kFullMask, row, i);
-          if (lane >= i) {
-            upto += u;
-            row += r;
+      for (int i = 16; i > 0; i >>= 1) total += __shfl_xor_sync(kFullMask, total, i);
+      total *= a.Hkv;
+      auto cut_at = [&](int c) { return total * c / static_cast<int>(gridDim.x); };
+      const long long x0 = cut_at(blockIdx.x), x1 = cut_at(blockIdx.x + 1);
+
+      int chunk = -32, seq = 31;                    // sequences [chunk, chunk + 32) are looked at; of them
+      long long start = 0;                          // where the line of sequence `seq` begins
+      PrefillSeq s;
+      long long length = 0;                         // of the lane's sequence, all key heads
+      // The next sequence with any row; false at the end.
+      auto next_seq = [&] {
+        start += __shfl_sync(kFullMask, length, seq);
+        for (;;) {
+          const uint32_t some = seq < 31 ? __ballot_sync(kFullMask, length > 0) >> (seq + 1) : 0;
+          if (some != 0) {
+            seq += __ffs(some);
+            return true;
+          }
+          chunk += 32;
+          if (chunk >= a.B) return false;
+          s = prefill_seq(a, chunk + lane);
+          length = PrefillLine(s.n, s.L, per_item, a.causal).length() * a.Hkv;
+          seq = -1;
+        }
+      };
+      int published = 0;
+      bool more = x1 > x0 && next_seq();
+      while (more && start + __shfl_sync(kFullMask, length, seq) <= x0) more = next_seq();
+      PrefillCut cut{};
+      if (more) {
+        // the item that x0 is in: key head, then row tile
+        PrefillLine line(__shfl_sync(kFullMask, s.n, seq), __shfl_sync(kFullMask, s.L, seq), per_item, a.causal);
+        const long long head_length = line.length();
+        int kvh = static_cast<int>((x0 - start) / head_length);
+        long long at = start + kvh * head_length;   // where the item begins
+        int tile = 0, step = line.tiles;
+        while (step > 1) {                          // the last tile that begins at or before x0
+          step = (step + 31) / 32;
+          const int t = tile + lane * step;
+          tile += (__popc(__ballot_sync(kFullMask, t < line.tiles && at + line.begin(t) <= x0)) - 1) * step;
+        }
+        at += line.begin(tile);
+        while (at < x1) {
+          const long long cost = line.cost(tile);
+          const int keys = line.keys(tile), tiles = (keys + BN - 1) / BN;
+          const int from = prefill_cut(x0 - at, cost, tiles, least), to = prefill_cut(x1 - at, cost, tiles, least);
+          if (from < to || (tiles == 0 && at >= x0)) {
+            PrefillItem it;
+            it.work = 1;
+            it.seq = chunk + seq;
+            it.kvh = kvh;
+            it.L = line.L;
+            it.key_base = __shfl_sync(kFullMask, s.k0, seq);
+            it.once = line.tiles == 1;
+            it.q_row = __shfl_sync(kFullMask, s.q0, seq) + tile * per_item;
+            it.ntok = min(per_item, line.n - tile * per_item);
+            it.two = it.ntok > TPT;
+            it.off = line.L - line.n + tile * per_item;
+            it.t0 = from;
+            const int last0 = a.causal ? it.off + min(TPT, it.ntok) - 1 : line.L - 1;
+            it.n0 = max(0, min(to, last0 < 0 ? 0 : last0 / BN + 1) - from);
+            it.n1 = it.two ? to - from : 0;
+            it.hidden = max(0, (a.causal ? it.off + 1 : it.L) / BN - from);
+            const int cta = blockIdx.x;
+            it.piece = from > 0 ? 2 * cta : (to < tiles ? 2 * cta + 1 : -1);
+            it.bad_values = 0;
+            if (from > 0) {                         // another CTA has the keys before
+              int c = blockIdx.x - 1;
+              while (prefill_cut(cut_at(c) - at, cost, tiles, least) == from) --c;
+              const bool first = prefill_cut(cut_at(c) - at, cost, tiles, least) == 0;
+              cut = PrefillCut{first ? 2 : 1, c, to == tiles, kvh, it.q_row, it.ntok};
+            }
+            if (published >= 2 &&
+                !__all_sync(kFullMask, mbar_wait_short(bar(LY::I_EMPTY + (published & 1)), ((published >> 1) - 1) & 1))) {
+              fail = true;
+              break;
+            }
+            if (lane == 0) {
+              *item_at(published) = it;
+              mbar_arrive(bar(LY::I_FULL + (published & 1)));
+            }
+            ++published;
+          }
+          at += cost;
+          if (++tile == line.tiles) {
+            tile = 0;
+            if (++kvh == a.Hkv) {
+              kvh = 0;
+              if (!next_seq()) break;
+              line = PrefillLine(__shfl_sync(kFullMask, s.n, seq), __shfl_sync(kFullMask, s.L, seq), per_item, a.causal);
+            }
           }
         }
-        row += rows_before - rows;
-      };
-      if (a.plan != nullptr && blockIdx.x == 0) {   // for the reduce
-        for (int b0 = 0; b0 < a.B; b0 += 32) {
-          look(b0);
-          if (b0 + lane < a.B) a.plan[b0 + lane] = PrefillPlan{cut.x, cut.y, row};
-          rows_before = __shfl_sync(kFullMask, row + (cut.x > 1 ? static_cast<long long>(s.n) * a.Hq * cut.x : 0), 31);
-        }
-        if (lane == 0) a.plan[a.B] = PrefillPlan{rows_before > 0, 0, rows_before};
-        rows_before = 0;
       }
-      look(0);
-      int slot = 0;
-      for (long long id = blockIdx.x;; id += gridDim.x) {
-        long long all = __shfl_sync(kFullMask, upto, 31);
-        while (chunk < a.B && id >= before + all) {
-          before += all;
-          rows_before = __shfl_sync(kFullMask, row + (cut.x > 1 ? static_cast<long long>(s.n) * a.Hq * cut.x : 0), 31);
-          chunk += 32;
-          if (chunk >= a.B) break;
-          look(chunk);
-          all = __shfl_sync(kFullMask, upto, 31);
-        }
-        PrefillItem it;
-        it.work = chunk < a.B;
-        if (it.work) {
-          const int from = __ffs(__ballot_sync(kFullMask, upto > id - before)) - 1;
-          long long r = id - before - (upto - mine);
-          r = __shfl_sync(kFullMask, r, from);
-          it.seq = chunk + from;
-          const int n = __shfl_sync(kFullMask, s.n, from), q0 = __shfl_sync(kFullMask, s.q0, from);
-          it.L = __shfl_sync(kFullMask, s.L, from);
-          it.key_base = __shfl_sync(kFullMask, s.k0, from);
-          it.parts = __shfl_sync(kFullMask, cut.x, from);
-          const int per = __shfl_sync(kFullMask, cut.y, from);
-          it.row = __shfl_sync(kFullMask, row, from);
-          const int tiles = (n + per_item - 1) / per_item;
-          const int rem = static_cast<int>(r % (static_cast<long long>(a.Hkv) * it.parts));
-          const int tile = tiles - 1 - static_cast<int>(r / (static_cast<long long>(a.Hkv) * it.parts));
-          it.part = rem / a.Hkv;
-          it.kvh = rem % a.Hkv;
-          it.once = tiles == 1;
-          it.q_row = q0 + tile * per_item;
-          it.ntok = min(per_item, n - tile * per_item);
-          it.two = it.ntok > TPT;
-          it.off = it.L - n + tile * per_item;
-          const int last0 = a.causal ? it.off + min(TPT, it.ntok) - 1 : it.L - 1;
-          const int last1 = a.causal ? it.off + it.ntok - 1 : it.L - 1;
-          it.t0 = it.part * per;
-          const int end = it.t0 + per;
-          it.n0 = max(0, min(end, last0 < 0 ? 0 : last0 / BN + 1) - it.t0);
-          it.n1 = it.two ? max(0, min(end, last1 < 0 ? 0 : last1 / BN + 1) - it.t0) : 0;
-          it.bad_values = 0;
-          if (it.parts > 1 && it.n0 + it.n1 == 0) continue;   // no row sees this partition
-        }
-        if (slot >= 2 && !__all_sync(kFullMask, mbar_wait(bar(LY::I_EMPTY + (slot & 1)), ((slot >> 1) - 1) & 1))) {
+      if (a.cuts != nullptr && lane == 0) a.cuts[blockIdx.x] = cut;
+      if (!fail) {
+        if (published >= 2 &&
+            !__all_sync(kFullMask, mbar_wait_short(bar(LY::I_EMPTY + (published & 1)), ((published >> 1) - 1) & 1)))
           fail = true;
-          break;
+        if (!fail && lane == 0) {
+          item_at(published)->work = 0;
+          mbar_arrive(bar(LY::I_FULL + (published & 1)));
         }
-        if (lane == 0) {
-          *item_at(slot) = it;
-          mbar_arrive(bar(LY::I_FULL + (slot & 1)));
-        }
-        ++slot;
-        if (!it.work) break;
       }
     } else if (warp == SOFT) {
       // -------------------------------------------------------- producer
@@ -405,7 +479,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
       int at = 0, loaded = 0;                       // slot, tiles so far
       uint32_t phase = 0, qs = 0;                   // of the slot; queries loaded so far
       auto wait = [&](int b, uint32_t parity) {
-        if (!__all_sync(kFullMask, mbar_wait(bar(b), parity))) fail = true;
+        if (!__all_sync(kFullMask, mbar_wait_short(bar(b), parity))) fail = true;
       };
       for (int slot = 0; !fail; ++slot) {
         wait(LY::I_FULL + (slot & 1), (slot >> 1) & 1);
@@ -484,7 +558,8 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
     } else if (warp == SOFT + 1) {
       // -------------------------------------------------------- matrix products
       const uint32_t leader = elect_lane();
-      const uint32_t idesc_qk = umma_idesc_f16(BF, 0, 0, BN, 128);
+      // (a negative scale: S of -Q, bit 13)
+      const uint32_t idesc_qk = umma_idesc_f16(BF, 0, 0, BN, 128) | (a.negative ? 1u << 13 : 0u);
       const uint32_t idesc_pv = umma_idesc_f16(BF, 0, 1, D, 128);
       // descriptors: eight rows of 128 bytes an atom (stride 1024), version 1,
       // 128-byte swizzle; V's leading offset is from one 64-channel panel to the next
@@ -515,7 +590,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
       int at = 0;
       uint32_t phase = 0;
       auto landed = [&] {
-        if (!__all_sync(kFullMask, mbar_wait(bar(LY::KV_FULL + at), phase))) fail = true;
+        if (!__all_sync(kFullMask, mbar_wait_short(bar(LY::KV_FULL + at), phase))) fail = true;
         const int slot = at;
         if (++at == ST) {
           at = 0;
@@ -525,31 +600,46 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
       };
       uint32_t qs = 0, su0 = 0, su1 = 0, su2 = 0, ou0 = 0, ou1 = 0;   // uses so far: Q, S buffers, O tiles
       auto have_p = [&](int s, uint32_t& uses) {    // P of S buffer s has been written
-        if (!__all_sync(kFullMask, mbar_wait(bar(LY::P_FULL + s), uses & 1))) fail = true;
+        if (!__all_sync(kFullMask, mbar_wait_short(bar(LY::P_FULL + s), uses & 1))) fail = true;
         ++uses;
       };
+      // V tiles that hide something: the values warp is told of tile i when K(i)
+      // is there (then it may wait for V(i): all tiles before have landed).  That
+      // may be while it works on the one before, hence two barriers each.
+      uint32_t told = 0, cleaned = 0;
+      auto tell = [&](bool some) {
+        if (!some) return;
+        if (lane == 0) mbar_arrive(bar(LY::V_HERE + (told & 1)));
+        ++told;
+      };
+      auto clean = [&] {                            // the V tile's values have been looked over
+        if (!__all_sync(kFullMask, mbar_wait_short(bar(LY::V_CLEAN + (cleaned & 1)), (cleaned >> 1) & 1))) fail = true;
+        ++cleaned;
+      };
       auto have_o = [&](int x, uint32_t& uses) {    // O tile x has been read by the item before
-        if (uses > 0 && !__all_sync(kFullMask, mbar_wait(bar(LY::O_FREE + x), (uses - 1) & 1))) fail = true;
+        if (uses > 0 && !__all_sync(kFullMask, mbar_wait_short(bar(LY::O_FREE + x), (uses - 1) & 1))) fail = true;
         ++uses;
       };
       for (int slot = 0; !fail; ++slot) {
-        if (!__all_sync(kFullMask, mbar_wait(bar(LY::I_FULL + (slot & 1)), (slot >> 1) & 1))) {
+        if (!__all_sync(kFullMask, mbar_wait_short(bar(LY::I_FULL + (slot & 1)), (slot >> 1) & 1))) {
           fail = true;
           break;
         }
         const PrefillItem* item = item_at(slot);
         const int work = item->work, two = item->two, n0 = item->n0, n1 = item->n1, n = max(n0, n1);
+        const int hidden = item->hidden;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(LY::I_EMPTY + (slot & 1)));
         if (!work) break;
         if (n == 0) continue;
-        if (!__all_sync(kFullMask, mbar_wait(bar(LY::Q_FULL), qs & 1))) {
+        if (!__all_sync(kFullMask, mbar_wait_short(bar(LY::Q_FULL), qs & 1))) {
           fail = true;
           break;
         }
         ++qs;
         int k = landed();
         if (fail) break;
+        tell(hidden == 0);
         if (!two || n0 > 0) qk(0, 0, k);
         if (LY::NQ == 2 && n1 > 0) qk(1, 1, k);
         umma_commit_if(bar(LY::KV_EMPTY + k), leader);
@@ -557,7 +647,11 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         if (LY::NQ == 2 && two) {
           for (int i = 0; i < n; ++i) {
             const int v = landed();
-            if (i + 1 < n) k = landed();
+            if (i + 1 < n) {
+              k = landed();
+              tell(i + 1 >= hidden);
+            }
+            if (i >= hidden) clean();
             if (i < n0) {
               have_p(0, su0);
               if (i == 0) have_o(0, ou0);
@@ -582,10 +676,12 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
             const int v = landed();
             if (i + 1 < n) {
               k = landed();
+              tell(i + 1 >= hidden);
               if (fail) break;
               qk(i & 1 ? 0 : 2, 0, k);
               umma_commit_if(bar(LY::KV_EMPTY + k), leader);
             }
+            if (i >= hidden) clean();
             if (i & 1) have_p(2, su2); else have_p(0, su0);
             if (i == 0) have_o(0, ou0);
             if (fail) break;
@@ -594,6 +690,77 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
             if (i + 2 == n) umma_commit_if(bar(LY::Q_EMPTY), leader);
           }
         }
+      }
+    } else {
+      // -------------------------------------------------------- values
+      int ring = 0;
+      uint32_t here = 0;
+      for (int slot = 0; !fail; ++slot) {
+        if (!__all_sync(kFullMask, mbar_wait_short(bar(LY::I_FULL + (slot & 1)), (slot >> 1) & 1))) {
+          fail = true;
+          break;
+        }
+        PrefillItem* item = item_at(slot);
+        if (!item->work) break;
+        const int n = max(item->n0, item->n1), L = item->L, t0 = item->t0;
+        const int seen = a.causal ? min(L, item->off + 1) : L;   // keys that every row sees
+        for (int i = item->hidden; i < n; ++i) {
+          const int rv = ring + 2 * i + 1;
+          if (!__all_sync(kFullMask, mbar_wait_short(bar(LY::V_HERE + (here & 1)), (here >> 1) & 1) &&
+                                         mbar_wait_short(bar(LY::KV_FULL + rv % ST), (rv / ST) & 1))) {
+            fail = true;
+            break;
+          }
+          const uint32_t tile = sb + LY::OFF_KV + (rv % ST) * LY::KV_TILE;
+          const int key0 = (t0 + i) * BN, first = max(0, seen - key0), end = min(BN, L - key0);
+          // rows [first, end): a product with zero is no number where the value is none
+          uint32_t odd[4] = {0, 0, 0, 0};
+          for (int c = 0; c < PANELS; ++c) {
+            const uint32_t from = tile + c * (BN * 128) + first * 128, to = tile + c * (BN * 128) + end * 128;
+#pragma unroll 8
+            for (uint32_t at = from + lane * 16; at < to; at += 512) {
+              uint32_t d[4];
+              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+                           : "r"(at));
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if constexpr (BF)
+                  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(odd[e]) : "r"(d[e]), "r"(0));
+                else
+                  asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(odd[e]) : "r"(d[e]), "r"(0));
+              }
+            }
+          }
+          const uint32_t any = (odd[0] | odd[1] | odd[2] | odd[3]) & 0x7fff7fffu;   // (zeros of either sign are fine)
+          const bool bad = __any_sync(kFullMask, any != 0);
+          if (bad || end < BN) {
+            for (int u = (bad ? first : end) * (D / 8) + lane; u < BN * (D / 8); u += 32) {
+              const int vr = u / (D / 8), ch = u % (D / 8);
+              const uint32_t at = tile + (ch >> 3) * (BN * 128) + vr * 128 + (ch & 7) * 16;
+              uint32_t d[4] = {0, 0, 0, 0};
+              if (vr < end) {
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+                             : "r"(at));
+                constexpr uint32_t kExp = BF ? 0x7f807f80u : 0x7c007c00u, kOne = BF ? 0x00800080u : 0x04000400u;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)         // a half whose exponent is all ones becomes zero
+                  d[e] &= ~(((((d[e] & kExp) + kOne) & 0x80008000u) >> 15) * 0xffffu);
+              }
+              asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(d[0]), "r"(d[1]), "r"(d[2]),
+                           "r"(d[3])
+                           : "memory");
+            }
+            if (bad && lane == 0) item->bad_values = 1;
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(LY::V_CLEAN + (here & 1)));
+          ++here;
+        }
+        if (lane == 0) mbar_arrive(bar(LY::I_EMPTY + (slot & 1)));
+        ring += 2 * n;
       }
     }
   } else {
@@ -612,11 +779,12 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
     float *own = xch + h * 128 + r, *others = xch + (h ^ 1) * 128 + r;
     const int tl = r / a.G;                         // token of the row within its tile
     const bool has_token = tl < TPT;
+    const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
     const float c = a.scale_log2;
-    // ring tiles, S buffers' uses, own O tile's products and its items so far
-    int ring = 0, su = 0, su2 = 0, od = 0, outs = 0;
+    // S buffers' uses, own O tile's products and its items so far
+    int su = 0, su2 = 0, od = 0, outs = 0;
     auto wait = [&](int b, uint32_t parity) {
-      if (!fail && !__all_sync(kFullMask, mbar_wait(bar(b), parity))) fail = true;
+      if (!fail && !__all_sync(kFullMask, mbar_wait_short(bar(b), parity))) fail = true;
     };
     for (int slot = 0;; ++slot) {
       wait(LY::I_FULL + (slot & 1), (slot >> 1) & 1);
@@ -627,10 +795,11 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
       PrefillItem* item = item_at(slot);
       if (!item->work) break;
       const int two = item->two, L = item->L, off = item->off, t0 = item->t0;
-      const int n0 = item->n0, n1 = item->n1, n = w == 0 ? n0 : n1;
+      const int n = w == 0 ? item->n0 : item->n1;
       const int j = w * TPT + tl;                   // token of the row within the item
       const bool valid = has_token && j < item->ntok && (w == 0 || two);
       const int lim = a.causal ? off + j : L - 1;   // last key that the row sees
+      const int all_see = __reduce_min_sync(kFullMask, valid ? lim : 0x7fffffff);   // last key that all of the warp's rows see
       float m = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
       for (int i = 0; i < n; ++i) {
@@ -645,47 +814,10 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         tmem_wait_ld();
 #pragma unroll
         for (int q = 0; q < HN / 32; ++q) tmem_ready32(x + q * 32);
-        const int key0 = (t0 + i) * BN, col0 = key0 + h * HN;
-        if (a.negative) {
-#pragma unroll
-          for (int e = 0; e < HN; ++e) x[e] = -x[e];
-        }
-        if (__any_sync(kFullMask, valid && col0 + HN - 1 > lim)) {
+        const int col0 = (t0 + i) * BN + h * HN;
+        if (col0 + HN - 1 > all_see) {
 #pragma unroll
           for (int e = 0; e < HN; ++e) x[e] = col0 + e <= lim ? x[e] : -INFINITY;
-        }
-        // values that some row must not see (the first row tile's warps that work on the keys)
-        if ((w == 0 || i >= n0) && key0 + BN > (a.causal ? min(L, off + 1) : L)) {
-          const int rv = ring + 2 * i + 1;
-          wait(LY::KV_FULL + rv % ST, (rv / ST) & 1);
-          const uint32_t tile = sb + LY::OFF_KV + (rv % ST) * LY::KV_TILE;
-          const int first = max(0, (a.causal ? min(L, off + 1) : L) - key0), end = L - key0;
-          for (int u = first * (D / 8) + h * 128 + r; u < BN * (D / 8); u += 256) {
-            const int vr = u / (D / 8), ch = u % (D / 8);
-            const uint32_t at = tile + (ch >> 3) * (BN * 128) + vr * 128 + (ch & 7) * 16;
-            uint32_t d[4] = {0, 0, 0, 0};
-            bool store = vr >= end;
-            if (!store) {
-              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                           : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
-                           : "r"(at));
-              constexpr uint32_t kExp = BF ? 0x7f807f80u : 0x7c007c00u, kOne = BF ? 0x00800080u : 0x04000400u;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t odd = ((d[e] & kExp) + kOne) & 0x80008000u;   // a half's exponent is all ones
-                if (odd) {
-                  d[e] &= ~((odd >> 15) * 0xffffu);
-                  store = true;
-                  item->bad_values = 1;
-                }
-              }
-            }
-            if (store)
-              asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(d[0]), "r"(d[1]), "r"(d[2]),
-                           "r"(d[3])
-                           : "memory");
-          }
-          fence_proxy_async_smem();
         }
         float top[4];
 #pragma unroll
@@ -707,7 +839,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
             // there, the one after waits for this tile's P.)
             wait(LY::O_DONE + w, (od + i - 1) & 1);
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < HD / 16; ++q) {
               float o[16];
               tmem_ld16(lanes + LY::O_COL(w) + h * HD + q * 16, o);
@@ -753,65 +885,94 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
       *own = l;
       named_bar_sync(pair, 64);
       l += *others;
-      const int kvh = item->kvh, parts = item->parts;
-      const size_t row = (static_cast<size_t>(item->q_row + j) * a.Hq + kvh * a.G + (r - tl * a.G));
-      size_t prow = 0;
-      if (parts > 1)
-        prow = static_cast<size_t>(item->row) +
-               (row - static_cast<size_t>(a.query_starts[item->seq]) * a.Hq) * parts + item->part;
-      const float inv = parts > 1 ? 1.f : (l > 0.f ? 1.f / l : 0.f);
-      const bool bad_values = n > 0 && item->bad_values;
+      const int kvh = item->kvh, piece = item->piece, head = r - tl * a.G;
+      const size_t row = static_cast<size_t>(item->q_row + j) * a.Hq + kvh * a.G + head;
+      const size_t prow = static_cast<size_t>(max(piece, 0)) * a.rows + j * a.G + head;
+      const float inv = piece >= 0 ? 1.f : (l > 0.f ? 1.f / l : 0.f);
+      // CW channels at a time.  So that a warp's stores fill whole sectors of few
+      // lines, NC lanes exchange their rows' 32-byte chunks first: lane l of them
+      // then has chunk l of each of their rows.
+      constexpr int CW = HD < 64 ? HD : 64, NC = CW / 16;
+      const int sub = lane % NC;
+      size_t rows_at[NC];
+      uint32_t rows_valid = 0;
+#pragma unroll
+      for (int e = 0; e < NC; ++e) {
+        rows_at[e] = __shfl_sync(kFullMask, static_cast<unsigned long long>(row), lane - sub + e);
+        rows_valid |= static_cast<uint32_t>(__shfl_sync(kFullMask, static_cast<int>(valid), lane - sub + e)) << e;
+      }
 #pragma unroll 1
-      for (int q = 0; q < HD / 32; ++q) {
-        const int ch0 = h * HD + q * 32;            // first channel
-        float o[32];
+      for (int q = 0; q < HD / CW; ++q) {
+        const int ch0 = h * HD + q * CW;            // first channel
+        float o[CW];
         if (n > 0) {
-          tmem_ld32(lanes + LY::O_COL(w) + ch0, o);
+#pragma unroll
+          for (int g = 0; g < CW / 32; ++g) tmem_ld32(lanes + LY::O_COL(w) + ch0 + g * 32, o + g * 32);
           tmem_wait_ld();
-          tmem_ready32(o);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] *= inv;
-          if (bad_values && valid) {
-            // cleared values that this row sees
-            const int to = min(min(lim, L - 1), (t0 + n) * BN - 1);
-            for (int key = max(max(off + 1, 0), t0 * BN); key <= to; ++key) {
-              const uint16_t* v;
-              if (a.key_starts != nullptr) {
-                v = a.v + (item->key_base + key) * a.v_stride + static_cast<size_t>(kvh) * D;
-              } else {
-                const int id = a.block_tables[static_cast<size_t>(item->seq) * a.MB + (key >> a.bs_log2)];
-                if (id < 0 || id >= a.NB) continue;
-                v = a.v + (((static_cast<size_t>(id) * a.Hkv + kvh) << a.bs_log2) + (key & ((1 << a.bs_log2) - 1))) * D;
-              }
+          for (int g = 0; g < CW / 32; ++g) tmem_ready32(o + g * 32);
 #pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const float2 y = unpack2<BF>(*reinterpret_cast<const uint32_t*>(v + ch0 + e));
-                if (!(fabsf(y.x) <= 3.402823466e38f)) o[e] += y.x;
-                if (!(fabsf(y.y) <= 3.402823466e38f)) o[e + 1] += y.y;
+          for (int e = 0; e < CW; ++e) o[e] *= inv;
+        } else {
+#pragma unroll
+          for (int e = 0; e < CW; ++e) o[e] = 0.f;
+        }
+        if (piece >= 0) {
+          if (valid) {
+            float* dst = a.part_o + prow * D + ch0;
+#pragma unroll
+            for (int e = 0; e < CW; e += 4)
+              *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        } else {
+          uint32_t pk[NC][8];
+#pragma unroll
+          for (int e = 0; e < CW / 2; ++e) pk[e / 8][e % 8] = pack2<BF>(o[2 * e], o[2 * e + 1]);
+#pragma unroll
+          for (int st = 1; st < NC; st <<= 1) {
+            const bool up = lane & st;
+#pragma unroll
+            for (int g = 0; g < NC; ++g) {
+              if (g & st) continue;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t got = __shfl_xor_sync(kFullMask, up ? pk[g][e] : pk[g | st][e], st);
+                if (up) pk[g][e] = got; else pk[g | st][e] = got;
               }
             }
           }
-        } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          for (int e = 0; e < NC; ++e)
+            if (rows_valid >> e & 1) store32(a.out + rows_at[e] * D + ch0 + sub * 16, pk[e], wide);
         }
-        if (valid) {
-          if (parts > 1) {
-            float* dst = a.part_o + prow * D + ch0;
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      }
+      if (n > 0 && item->bad_values) {
+        // values that were cleared, for the rows that see them
+        __syncwarp();                               // (the row may have been stored by another lane)
+        const int to = valid ? min(min(lim, L - 1), (t0 + n) * BN - 1) : -1;
+        for (int key = max(max(off + 1, 0), t0 * BN); key <= to; ++key) {
+          const uint16_t* v;
+          if (a.key_starts != nullptr) {
+            v = a.v + (item->key_base + key) * a.v_stride + static_cast<size_t>(kvh) * D;
           } else {
-            uint16_t* dst = a.out + row * D + ch0;
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(dst + e) =
-                  make_uint4(pack2<BF>(o[e], o[e + 1]), pack2<BF>(o[e + 2], o[e + 3]),
-                             pack2<BF>(o[e + 4], o[e + 5]), pack2<BF>(o[e + 6], o[e + 7]));
+            const int id = a.block_tables[static_cast<size_t>(item->seq) * a.MB + (key >> a.bs_log2)];
+            if (id < 0 || id >= a.NB) continue;
+            v = a.v + (((static_cast<size_t>(id) * a.Hkv + kvh) << a.bs_log2) + (key & ((1 << a.bs_log2) - 1))) * D;
+          }
+#pragma unroll 1
+          for (int ch = h * HD; ch < h * HD + HD; ++ch) {
+            const float y = unpack2<BF>(v[ch]).x;
+            if (fabsf(y) <= 3.402823466e38f) continue;
+            if (piece >= 0) {
+              a.part_o[prow * D + ch] += y;
+            } else {
+              uint16_t* at = a.out + row * D + ch;
+              *at = to_elem<BF>(unpack2<BF>(*at).x + y);
+            }
           }
         }
       }
-      if (parts > 1 && valid && h == 0)
+      if (piece >= 0 && valid && h == 0)
         a.part_ml[prow] = make_float2(l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m * c) - kShift, l);
       tc_fence_before();
       __syncwarp();
@@ -824,7 +985,6 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         break;
       }
       od += n;
-      ring += 2 * max(n0, n1);
     }
   }
   tc_fence_before();

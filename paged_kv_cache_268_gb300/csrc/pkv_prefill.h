@@ -10,17 +10,18 @@ namespace pkv {
 constexpr int prefill_row_tiles(int D) { return D == 256 ? 1 : 2; }   // of 128 rows, an item
 constexpr int prefill_key_tile(int D) { return D == 256 ? 64 : 128; }
 
-// Where a sequence's keys are cut into partitions (rule at prefill_parts).
-constexpr int kPrefillMinPart = 512;      // keys at least
-constexpr int kPrefillFewRows = 64;       // rows of a key head: cut finer up to here
-constexpr int kPrefillFewUnits = 4;       // partitions a CTA's share of the work makes, few rows
-constexpr int kPrefillUnits = 2;          // and many
+// Keys of the smallest part of an item's keys that a CTA is given, and the cost
+// of an item besides its keys', in keys.
+constexpr int kPrefillMinPart = 512;
+constexpr int kPrefillItemCost = 192;
 
-// What the reduce has to know of a sequence; a last one says whether any was cut.
-struct PrefillPlan {
-  int parts;                     // partitions; below two: none were written
-  int per;                       // key tiles of one
-  long long row;                 // its first partial row
+// What the reduce has to know of an item that CTA c goes on with where another
+// CTA left off (kind 0: CTA c does no such thing).
+struct PrefillCut {
+  int kind;                      // 1: further pieces lie before it, 2: only the first one
+  int first;                     // kind 2: the CTA that has the item's first piece
+  int ends;                      // CTA c's piece is the item's last
+  int kvh, q_row, ntok;
 };
 
 struct PrefillArgs {
@@ -30,17 +31,18 @@ struct PrefillArgs {
   const int32_t* block_tables;   // paged: [B, MB]
   const uint16_t* v;             // packed: [S, Hkv, D]; paged: [NB, Hkv, bs, D]
   uint16_t* out;                 // [T, Hq, D]
-  PrefillPlan* plan;             // [B + 1], or null: no sequence is cut
-  float2* part_ml;               // (exponent, sum) of a partial row
-  float* part_o;                 // its un-normalised output [D]
+  PrefillCut* cuts;              // [CTAs], or null: no item is cut
+  float2* part_ml;               // (exponent, sum) of a partial row, `rows` for a piece:
+  float* part_o;                 //   piece 2c is CTA c's with keys before it, 2c + 1 its
+                                 //   with only keys behind; the un-normalised output [D]
   int* err;
   long long v_stride;            // packed: elements between tokens
   int B, T, Hq, Hkv, G;
   int max_keys;                  // bound of a sequence's keys (paged), S (packed)
   int MB, NB, bs_log2;
   int causal, negative;          // negative: the scale is
-  int part_tiles;                // key tiles of a partition, 0: by the rule
-  int ctas;                      // that share the work
+  int rows;                      // of an item at most
+  int min_part;                  // key tiles of a piece at least
   float scale_log2;              // |softmax scale| * log2(e)
 };
 
