@@ -272,9 +272,9 @@ int cache_map(CUtensorMap* out, const void* base, const pkv_shape& s, bool three
 
 }  // namespace
 
-int block_map(CUtensorMap* out, const void* base, const pkv_shape& s) {
+int block_map(CUtensorMap* out, const void* base, const pkv_shape& s, bool whole) {
   const int rc = get_encoder();
-  return rc != PKV_OK ? rc : cache_map(out, base, s, false);
+  return rc != PKV_OK ? rc : cache_map(out, base, s, whole);
 }
 
 int rows_map(CUtensorMap* out, const void* base, bool bf16, int head_dim, int heads, int64_t tokens,

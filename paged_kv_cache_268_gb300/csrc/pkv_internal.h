@@ -85,9 +85,10 @@ int check_decode_shape(const pkv_shape*);    // the same for a decode batch
 int device_sms(int* sms);                    // SM count of the current device
 // Workspace set for the current device with pkv_set_workspace, or {nullptr, 0}.
 int device_workspace(void** ptr, size_t* bytes);
-// Tensor map of a cache in boxes of one block's rows and 64 channels (x channel,
-// y row of [NB, Hkv, bs]), 128-byte swizzled.
-int block_map(CUtensorMap* out, const void* base, const pkv_shape& s);
+// Tensor map of a cache in boxes of one block's rows, 128-byte swizzled: of 64
+// channels (x channel, y row of [NB, Hkv, bs]), or all of them, 64 by 64 (whole:
+// x channel of 64, y row, z which 64).
+int block_map(CUtensorMap* out, const void* base, const pkv_shape& s, bool whole);
 // Tensor map of packed rows [tokens, heads, head_dim], `stride` elements between
 // tokens, in boxes of 64 channels x box_heads x box_tokens, 128-byte swizzled.
 // What lies past the last token reads as zero.

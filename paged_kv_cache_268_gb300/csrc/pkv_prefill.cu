@@ -11,12 +11,14 @@ namespace pkv {
 namespace {
 
 constexpr int kReduceThreads = 256;
-constexpr int kReduceRows = 32;          // of a CTA
+constexpr int kReduceRows = kReduceThreads / 32;   // of a CTA, a warp each
 
 // Joins the pieces of the items that were cut: out = sum_p 2^(e_p - E) o_p /
 // sum_p 2^(e_p - E) l_p with E the largest exponent, in the keys' order.  CTA
 // (c, y) looks after the item whose second piece attention's CTA c had, if it
-// had one, rows 32 y and up; a warp a row.
+// had one, eight of its rows.  Bound by the latency of its few loads, so each
+// step asks for all that it needs at once: the CTAs behind c, a lane each; the
+// pieces' exponents and sums, a lane each; the outputs, several pieces at a time.
 template <bool BF, int D>
 __global__ void __launch_bounds__(kReduceThreads) prefill_reduce_kernel(const __grid_constant__ PrefillArgs a) {
   constexpr int C = D / 32;
@@ -24,43 +26,66 @@ __global__ void __launch_bounds__(kReduceThreads) prefill_reduce_kernel(const __
   pdl_launch_dependents();
   const int c0 = blockIdx.x, lane = threadIdx.x & 31;
   const PrefillCut cut = a.cuts[c0];
-  const int rows = cut.ntok * a.G;
-  if (cut.kind != 2 || static_cast<int>(blockIdx.y) * kReduceRows >= rows) return;
-  for (int k = threadIdx.x >> 5; k < kReduceRows; k += kReduceThreads / 32) {
-    const int row = blockIdx.y * kReduceRows + k;
-    if (row >= rows) return;
-    float o[C] = {}, l = 0.f, top = -INFINITY;
-    // pieces: the first one, then c0's and those of the CTAs behind it
-    for (int c = c0, piece = 2 * cut.first + 1;;) {
-      const size_t at = static_cast<size_t>(piece) * a.rows + row;
-      const float2 ml = a.part_ml[at];
-      if (ml.y != 0.f) {
-        const float up = fmaxf(top, ml.x), keep = top == -INFINITY ? 0.f : fast_exp2(top - up);
-        const float w = fast_exp2(ml.x - up);
-        top = up;
-        l = fmaf(l, keep, w * ml.y);
-        const float2* src = reinterpret_cast<const float2*>(a.part_o + at * D + lane * C);
+  const int row = blockIdx.y * kReduceRows + (threadIdx.x >> 5);
+  if (cut.kind != 2 || row >= cut.ntok * a.G) return;
+  float o[C] = {}, l = 0.f, top = -INFINITY;
+  // 31 CTAs from c0 up at a time, and before the first of them the item's first piece
+  bool more = true;
+  for (int c = c0 - 1; more; c += 31) {
+    const int mine = lane == 0 ? cut.first : c + lane;      // the CTA of the lane's piece
+    int kind = 0, ends = 0;
+    if (lane > 0 && mine < static_cast<int>(gridDim.x)) {
+      kind = a.cuts[mine].kind;
+      ends = a.cuts[mine].ends;
+    }
+    const uint32_t last = __ballot_sync(0xffffffffu, kind != 0 && ends);
+    more = last == 0 && c + 32 < static_cast<int>(gridDim.x);
+    const int until = last ? __ffs(last) - 1 : 31;          // the last lane with a piece of the item
+    const bool have = lane == 0 ? c == c0 - 1 : kind != 0 && lane <= until;
+    const size_t at = static_cast<size_t>(lane == 0 ? 2 * mine + 1 : 2 * mine) * a.rows + row;
+    const float2 ml = have ? a.part_ml[at] : make_float2(-INFINITY, 0.f);
+    float up = ml.y != 0.f ? fmaxf(top, ml.x) : top;
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, i));
+    const float keep = top == -INFINITY ? 0.f : fast_exp2(top - up);
+    const float w = ml.y != 0.f ? fast_exp2(ml.x - up) : 0.f;
+    float sum = w * ml.y;
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+    l = fmaf(l, keep, sum);
+    top = up;
+#pragma unroll
+    for (int e = 0; e < C; ++e) o[e] *= keep;
+    uint32_t todo = __ballot_sync(0xffffffffu, have && ml.y != 0.f);
+    while (todo != 0) {
+      constexpr int U = D == 256 ? 2 : 4;                   // pieces at a time
+      float2 x[U][C / 2];
+      float wt[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int from = todo != 0 ? __ffs(todo) - 1 : 0;
+        wt[u] = __shfl_sync(0xffffffffu, w, from);
+        if (todo == 0) wt[u] = 0.f;
+        const size_t src = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(at), from);
+        const float2* p = reinterpret_cast<const float2*>(a.part_o + src * D + lane * C);
+#pragma unroll
+        for (int e = 0; e < C / 2; ++e) x[u][e] = todo != 0 ? p[e] : make_float2(0.f, 0.f);
+        todo &= todo - 1;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int e = 0; e < C / 2; ++e) {
-          const float2 x = src[e];
-          o[2 * e] = fmaf(o[2 * e], keep, w * x.x);
-          o[2 * e + 1] = fmaf(o[2 * e + 1], keep, w * x.y);
+          o[2 * e] = fmaf(wt[u], x[u][e].x, o[2 * e]);
+          o[2 * e + 1] = fmaf(wt[u], x[u][e].y, o[2 * e + 1]);
         }
-      }
-      if (piece == 2 * cut.first + 1) {
-        piece = 2 * c;
-        continue;
-      }
-      if (a.cuts[c].ends) break;
-      do ++c; while (a.cuts[c].kind == 0);
-      piece = 2 * c;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const size_t out = static_cast<size_t>(cut.q_row + row / a.G) * a.Hq + cut.kvh * a.G + row % a.G;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + out * D + lane * C);
-#pragma unroll
-    for (int e = 0; e < C / 2; ++e) dst[e] = pack2<BF>(o[2 * e] * inv, o[2 * e + 1] * inv);
   }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const size_t out = static_cast<size_t>(cut.q_row + row / a.G) * a.Hq + cut.kvh * a.G + row % a.G;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + out * D + lane * C);
+#pragma unroll
+  for (int e = 0; e < C / 2; ++e) dst[e] = pack2<BF>(o[2 * e] * inv, o[2 * e + 1] * inv);
 }
 
 template <bool BF>
@@ -209,8 +234,8 @@ extern "C" int pkv_paged_attn_chunk(const pkv_shape* s, const void* q, int64_t q
   CUtensorMap tq, tk, tv;
   rc = rows_map(&tq, q, bf, D, s->num_q_heads, num_tokens,
                 q_stride ? q_stride : static_cast<int64_t>(s->num_q_heads) * D, G, 128 / G);
-  if (rc == PKV_OK) rc = block_map(&tk, k_cache, *s);
-  if (rc == PKV_OK) rc = block_map(&tv, v_cache, *s);
+  if (rc == PKV_OK) rc = block_map(&tk, k_cache, *s, false);
+  if (rc == PKV_OK) rc = block_map(&tv, v_cache, *s, true);
   if (rc != PKV_OK) return rc;
   PrefillArgs a{};
   a.query_starts = query_starts;

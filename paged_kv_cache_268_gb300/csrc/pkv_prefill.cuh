@@ -193,6 +193,26 @@ __device__ __forceinline__ void umma_commit_if(uint32_t bar, uint32_t leader) {
       : "memory");
 }
 
+// TMA loads that the whole warp reaches and the lane with `leader` issues.
+__device__ __forceinline__ void tma_2d_if(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar,
+                                          uint64_t policy, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void tma_3d_if(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar,
+                                          uint64_t policy, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+      "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy), "r"(leader)
+      : "memory");
+}
+
 // 32 bytes to global memory: in one piece where the address is `wide`, aligned
 // to them, else in two.
 __device__ __forceinline__ void store32(uint16_t* p, const uint32_t (&v)[8], bool wide) {
@@ -318,6 +338,9 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + LY::OFF_TMEM);
   const int tid = threadIdx.x, warp = __shfl_sync(kFullMask, tid >> 5, 0), lane = tid & 31;
   const int TPT = 128 / a.G;                       // tokens of a row tile
+  // A V tile lies in runs of keys, all panels of a run one after the other: a
+  // run is a block (paged) or the tile.
+  const int run_log2 = a.key_starts == nullptr ? a.bs_log2 : (BN == 128 ? 7 : 6);
 
   if (tid < LY::NBAR) {
     int count = 1;
@@ -471,6 +494,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
       }
     } else if (warp == SOFT) {
       // -------------------------------------------------------- producer
+      const uint32_t leader = elect_lane();
       const uint64_t stream_policy = l2_policy_evict_first();
       uint64_t keep_policy;
       asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep_policy));
@@ -491,13 +515,12 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         const int n = max(it.n0, it.n1);
         if (n == 0) continue;
         const uint64_t policy = it.once ? stream_policy : keep_policy;
-        // paged: lane l brings 64 columns (l % PANELS) of block l / PANELS of the tile
+        // paged: lane l knows where block l of a key tile is
         const int bs = 1 << a.bs_log2, per_tile = BN >> a.bs_log2, blocks = (it.L + bs - 1) >> a.bs_log2;
-        const int panel = lane % PANELS, blk = lane / PANELS;
         const int32_t* table = paged ? a.block_tables + static_cast<size_t>(it.seq) * a.MB : nullptr;
         auto row_of = [&](int t) {                  // cache row of the lane's block in key tile t
-          const int j = t * per_tile + blk;
-          if (blk >= per_tile || j >= blocks) return past;     // past the end: reads as zero
+          const int j = t * per_tile + lane;
+          if (lane >= per_tile || j >= blocks) return past;    // past the end: reads as zero
           const int id = __ldg(table + j);
           if (id < 0 || id >= a.NB) {
             record_error(a.err, kDevBadBlock);
@@ -514,13 +537,26 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
             if (fail) break;
             const CUtensorMap* map = kv ? &tmV : &tmK;
             const uint32_t full = bar(LY::KV_FULL + at), dst = sb + LY::OFF_KV + at * LY::KV_TILE;
-            if (lane == 0) mbar_arrive_expect_tx(full, LY::KV_TILE);
+            if (leader) mbar_arrive_expect_tx(full, LY::KV_TILE);
             __syncwarp();
-            if (paged) {
-              if (blk < per_tile)
-                tma_load_2d(dst + panel * (BN * 128) + (blk << a.bs_log2) * 128, map, panel * 64, y, full, policy);
-            } else if (lane < PANELS) {
-              tma_load_3d(dst + lane * (BN * 128), map, lane * 64, it.kvh, it.key_base + (it.t0 + i) * BN, full, policy);
+            if (paged && kv == 0) {
+              // 64 channels of a block a load: a tile's panels keep all its keys together
+#pragma unroll 4
+              for (int b = 0; b < per_tile; ++b) {
+                const int row = __shfl_sync(kFullMask, y, b);
+#pragma unroll
+                for (int c = 0; c < PANELS; ++c)
+                  tma_2d_if(dst + c * (BN * 128) + (b << a.bs_log2) * 128, map, c * 64, row, full, policy, leader);
+              }
+            } else if (paged) {
+              // a block a load: its panels one after the other
+#pragma unroll 4
+              for (int b = 0; b < per_tile; ++b)
+                tma_3d_if(dst + (b << a.bs_log2) * (D * 2), map, 0, __shfl_sync(kFullMask, y, b), 0, full, policy, leader);
+            } else {
+#pragma unroll
+              for (int c = 0; c < PANELS; ++c)
+                tma_3d_if(dst + c * (BN * 128), map, c * 64, it.kvh, it.key_base + (it.t0 + i) * BN, full, policy, leader);
             }
             ++loaded;
             if (++at == ST) {
@@ -531,13 +567,13 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
               const int tiles = it.two ? 2 : 1;
               wait(LY::Q_EMPTY, (qs & 1) ^ 1);
               if (fail) break;
-              if (lane == 0) mbar_arrive_expect_tx(bar(LY::Q_FULL), tiles * PANELS * TPT * a.G * 128);
+              if (leader) mbar_arrive_expect_tx(bar(LY::Q_FULL), tiles * PANELS * TPT * a.G * 128);
               __syncwarp();
-              if (lane < tiles * PANELS) {
-                const int x = lane / PANELS, c = lane % PANELS;
-                tma_load_3d(sb + x * LY::Q_TILE + c * 16384, &tmQ, c * 64, it.kvh * a.G, it.q_row + x * TPT,
-                            bar(LY::Q_FULL), stream_policy);
-              }
+              for (int x = 0; x < tiles; ++x)
+#pragma unroll
+                for (int c = 0; c < PANELS; ++c)
+                  tma_3d_if(sb + x * LY::Q_TILE + c * 16384, &tmQ, c * 64, it.kvh * a.G, it.q_row + x * TPT,
+                            bar(LY::Q_FULL), stream_policy, leader);
               ++qs;
             }
           }
@@ -565,7 +601,11 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
       // 128-byte swizzle; V's leading offset is from one 64-channel panel to the next
       constexpr uint32_t kHi = (1024 >> 4) | 1u << 14 | 2u << 29;
       const uint32_t q_lo = (sb >> 4) | 1u << 16, k_lo = ((sb + LY::OFF_KV) >> 4) | 1u << 16;
-      const uint32_t v_lo = ((sb + LY::OFF_KV) >> 4) | (BN * 128u >> 4) << 16;
+      const uint32_t v_lo = ((sb + LY::OFF_KV) >> 4) | (128u << run_log2 >> 4) << 16;
+      uint32_t v_step[BN / 16];                     // where 16 keys begin in a V tile
+#pragma unroll
+      for (int kk = 0; kk < BN / 16; ++kk)
+        v_step[kk] = ((kk >> (run_log2 - 4)) * (D * 2u << run_log2) + (kk & ((1 << (run_log2 - 4)) - 1)) * 2048u) >> 4;
       auto qk = [&](int s, int x, int at) {         // S buffer s = Q tile x . K of slot `at`
         tc_fence_after();
         const uint32_t a_lo = q_lo + x * (LY::Q_TILE >> 4), b_lo = k_lo + at * (LY::KV_TILE >> 4);
@@ -580,7 +620,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         const uint32_t b_lo = v_lo + at * (LY::KV_TILE >> 4);
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
-          umma_ts(tmem + LY::O_COL(x), tmem + LY::S_COL(s) + LY::P_COL(kk), b_lo + kk * (2048 >> 4), kHi, idesc_pv,
+          umma_ts(tmem + LY::O_COL(x), tmem + LY::S_COL(s) + LY::P_COL(kk), b_lo + v_step[kk], kHi, idesc_pv,
                   !first || kk > 0, leader);
         umma_commit_if(bar(LY::O_DONE + x), leader);
         if (last) umma_commit_if(bar(LY::O_LAST + x), leader);
@@ -715,20 +755,24 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
           const int key0 = (t0 + i) * BN, first = max(0, seen - key0), end = min(BN, L - key0);
           // rows [first, end): a product with zero is no number where the value is none
           uint32_t odd[4] = {0, 0, 0, 0};
-          for (int c = 0; c < PANELS; ++c) {
-            const uint32_t from = tile + c * (BN * 128) + first * 128, to = tile + c * (BN * 128) + end * 128;
-#pragma unroll 8
-            for (uint32_t at = from + lane * 16; at < to; at += 512) {
-              uint32_t d[4];
-              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                           : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
-                           : "r"(at));
+          for (int r0 = first; r0 < end; r0 = ((r0 >> run_log2) + 1) << run_log2) {
+            const int run = r0 >> run_log2, in = r0 & ((1 << run_log2) - 1), rows = min(end - r0, (1 << run_log2) - in);
+            const uint32_t from = tile + run * (D * 2 << run_log2) + in * 128;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if constexpr (BF)
-                  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(odd[e]) : "r"(d[e]), "r"(0));
-                else
-                  asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(odd[e]) : "r"(d[e]), "r"(0));
+            for (int c = 0; c < PANELS; ++c) {
+#pragma unroll 4
+              for (int b = lane * 16; b < rows * 128; b += 512) {
+                uint32_t d[4];
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+                             : "r"(from + (c << run_log2) * 128 + b));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if constexpr (BF)
+                    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(odd[e]) : "r"(d[e]), "r"(0));
+                  else
+                    asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(odd[e]) : "r"(d[e]), "r"(0));
+                }
               }
             }
           }
@@ -737,7 +781,8 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
           if (bad || end < BN) {
             for (int u = (bad ? first : end) * (D / 8) + lane; u < BN * (D / 8); u += 32) {
               const int vr = u / (D / 8), ch = u % (D / 8);
-              const uint32_t at = tile + (ch >> 3) * (BN * 128) + vr * 128 + (ch & 7) * 16;
+              const uint32_t at = tile + (vr >> run_log2) * (D * 2 << run_log2) + ((ch >> 3) << run_log2) * 128 +
+                                  (vr & ((1 << run_log2) - 1)) * 128 + (ch & 7) * 16;
               uint32_t d[4] = {0, 0, 0, 0};
               if (vr < end) {
                 asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
