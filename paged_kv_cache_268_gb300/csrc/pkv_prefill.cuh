@@ -56,8 +56,8 @@ struct PrefillLayout {
   static constexpr int STAGES = D == 64 ? 8 : 5;
   static constexpr int OFF_KV = NQ * Q_TILE;
   static constexpr int OFF_BAR = OFF_KV + STAGES * KV_TILE;
-  static constexpr int KV_FULL = 0, KV_EMPTY = STAGES, Q_FULL = 2 * STAGES, Q_EMPTY = Q_FULL + 1,
-                       S_FULL = Q_FULL + 2, P_FULL = S_FULL + 3, O_DONE = P_FULL + 3,
+  static constexpr int KV_FULL = 0, KV_EMPTY = STAGES, Q_FULL = 2 * STAGES, Q_EMPTY = Q_FULL + 2,
+                       S_FULL = Q_EMPTY + 2, P_FULL = S_FULL + 3, O_DONE = P_FULL + 3,
                        O_LAST = O_DONE + 2, O_FREE = O_LAST + 2, I_FULL = O_FREE + 2,
                        I_EMPTY = I_FULL + 2, V_HERE = I_EMPTY + 2, V_CLEAN = V_HERE + 2,
                        NBAR = V_CLEAN + 2;
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
       const bool paged = a.key_starts == nullptr;
       const int past = paged ? static_cast<int>((static_cast<long long>(a.NB) * a.Hkv) << a.bs_log2) : 0;
       int at = 0, loaded = 0;                       // slot, tiles so far
-      uint32_t phase = 0, qs = 0;                   // of the slot; queries loaded so far
+      uint32_t phase = 0, qs0 = 0, qs1 = 0;         // of the slot; row tiles' loads so far
       auto wait = [&](int b, uint32_t parity) {
         if (!__all_sync(kFullMask, mbar_wait_short(bar(b), parity))) fail = true;
       };
@@ -563,18 +563,17 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
               at = 0;
               phase ^= 1;
             }
-            if (kv == 0 && i == 0) {
-              const int tiles = it.two ? 2 : 1;
-              wait(LY::Q_EMPTY, (qs & 1) ^ 1);
+            if (i == 0 && (kv == 0 || it.two)) {    // row tile 0 after the first keys, 1 after their values
+              uint32_t& uses = kv ? qs1 : qs0;
+              wait(LY::Q_EMPTY + kv, (uses & 1) ^ 1);
+              ++uses;
               if (fail) break;
-              if (leader) mbar_arrive_expect_tx(bar(LY::Q_FULL), tiles * PANELS * TPT * a.G * 128);
+              if (leader) mbar_arrive_expect_tx(bar(LY::Q_FULL + kv), PANELS * TPT * a.G * 128);
               __syncwarp();
-              for (int x = 0; x < tiles; ++x)
 #pragma unroll
-                for (int c = 0; c < PANELS; ++c)
-                  tma_3d_if(sb + x * LY::Q_TILE + c * 16384, &tmQ, c * 64, it.kvh * a.G, it.q_row + x * TPT,
-                            bar(LY::Q_FULL), stream_policy, leader);
-              ++qs;
+              for (int c = 0; c < PANELS; ++c)
+                tma_3d_if(sb + kv * LY::Q_TILE + c * 16384, &tmQ, c * 64, it.kvh * a.G, it.q_row + kv * TPT,
+                          bar(LY::Q_FULL + kv), stream_policy, leader);
             }
           }
           if (fail) break;
@@ -587,9 +586,11 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         const bool landed = mbar_wait(bar(LY::KV_FULL + r % ST), (r / ST) & 1, 100000000ull);
         if (!fail && landed) mbar_wait(bar(LY::KV_EMPTY + r % ST), (r / ST) & 1, 100000000ull);
       }
-      if (qs > 0) {
-        mbar_wait(bar(LY::Q_FULL), (qs - 1) & 1, 100000000ull);
-        if (!fail) mbar_wait(bar(LY::Q_EMPTY), (qs - 1) & 1, 100000000ull);
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t uses = x ? qs1 : qs0;
+        if (uses == 0) continue;
+        mbar_wait(bar(LY::Q_FULL + x), (uses - 1) & 1, 100000000ull);
+        if (!fail) mbar_wait(bar(LY::Q_EMPTY + x), (uses - 1) & 1, 100000000ull);
       }
     } else if (warp == SOFT + 1) {
       // -------------------------------------------------------- matrix products
@@ -638,7 +639,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         }
         return slot;
       };
-      uint32_t qs = 0, su0 = 0, su1 = 0, su2 = 0, ou0 = 0, ou1 = 0;   // uses so far: Q, S buffers, O tiles
+      uint32_t qs0 = 0, qs1 = 0, su0 = 0, su1 = 0, su2 = 0, ou0 = 0, ou1 = 0;   // uses so far: Q, S buffers, O tiles
       auto have_p = [&](int s, uint32_t& uses) {    // P of S buffer s has been written
         if (!__all_sync(kFullMask, mbar_wait_short(bar(LY::P_FULL + s), uses & 1))) fail = true;
         ++uses;
@@ -660,6 +661,12 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         if (uses > 0 && !__all_sync(kFullMask, mbar_wait_short(bar(LY::O_FREE + x), (uses - 1) & 1))) fail = true;
         ++uses;
       };
+      auto have_q = [&](int x, uint32_t& uses) {
+        if (!__all_sync(kFullMask, mbar_wait_short(bar(LY::Q_FULL + x), uses & 1))) fail = true;
+        ++uses;
+      };
+      uint32_t ring = 0;                            // tiles of the items before
+      bool ahead = false;                           // S0 of the item's first keys is under way already
       for (int slot = 0; !fail; ++slot) {
         if (!__all_sync(kFullMask, mbar_wait_short(bar(LY::I_FULL + (slot & 1)), (slot >> 1) & 1))) {
           fail = true;
@@ -672,18 +679,22 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         if (lane == 0) mbar_arrive(bar(LY::I_EMPTY + (slot & 1)));
         if (!work) break;
         if (n == 0) continue;
-        if (!__all_sync(kFullMask, mbar_wait_short(bar(LY::Q_FULL), qs & 1))) {
-          fail = true;
-          break;
-        }
-        ++qs;
         int k = landed();
-        if (fail) break;
         tell(hidden == 0);
-        if (!two || n0 > 0) qk(0, 0, k);
-        if (LY::NQ == 2 && n1 > 0) qk(1, 1, k);
+        if (!ahead) {
+          have_q(0, qs0);
+          if (fail) break;
+          if (n0 > 0) qk(0, 0, k);
+        }
+        if (n0 <= 1) umma_commit_if(bar(LY::Q_EMPTY), leader);
+        if (LY::NQ == 2 && two) {
+          have_q(1, qs1);
+          if (fail) break;
+          qk(1, 1, k);
+          if (n1 == 1) umma_commit_if(bar(LY::Q_EMPTY + 1), leader);
+        }
         umma_commit_if(bar(LY::KV_EMPTY + k), leader);
-        if (n == 1) umma_commit_if(bar(LY::Q_EMPTY), leader);
+        ahead = false;
         if (LY::NQ == 2 && two) {
           for (int i = 0; i < n; ++i) {
             const int v = landed();
@@ -699,7 +710,26 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
               pv(0, 0, v, i == 0, i + 1 == n0);
             }
             if (fail) break;
-            if (i + 1 < n0) qk(0, 0, k);
+            if (i + 1 < n0) {
+              qk(0, 0, k);
+              if (i + 2 == n0) umma_commit_if(bar(LY::Q_EMPTY), leader);
+            } else if (i + 2 >= n && !ahead) {
+              // Row tile 0 is through: on to the next item's first keys, if they
+              // and its row tile are there.  (Every ring tile but the last two
+              // or three of this item has landed, so the slot of those keys is
+              // at their phase or the one before.)
+              const uint32_t next = ring + 2 * n;
+              const PrefillItem* then = item_at(slot + 1);
+              bool go = mbar_test_wait(bar(LY::I_FULL + ((slot + 1) & 1)), ((slot + 1) >> 1) & 1) && then->work &&
+                        then->n0 > 0 && mbar_test_wait(bar(LY::Q_FULL), qs0 & 1) &&
+                        mbar_test_wait(bar(LY::KV_FULL + next % ST), (next / ST) & 1);
+              go = __all_sync(kFullMask, go);
+              if (go) {
+                ++qs0;
+                ahead = true;
+                qk(0, 0, next % ST);
+              }
+            }
             if (i < n1) {
               have_p(1, su1);
               if (i == 0) have_o(1, ou1);
@@ -707,9 +737,11 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
               pv(1, 1, v, i == 0, i + 1 == n1);
             }
             umma_commit_if(bar(LY::KV_EMPTY + v), leader);
-            if (i + 1 < n1) qk(1, 1, k);
+            if (i + 1 < n1) {
+              qk(1, 1, k);
+              if (i + 2 == n1) umma_commit_if(bar(LY::Q_EMPTY + 1), leader);
+            }
             if (i + 1 < n) umma_commit_if(bar(LY::KV_EMPTY + k), leader);
-            if (i + 2 == n) umma_commit_if(bar(LY::Q_EMPTY), leader);
           }
         } else {
           for (int i = 0; i < n; ++i) {
@@ -719,6 +751,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
               tell(i + 1 >= hidden);
               if (fail) break;
               qk(i & 1 ? 0 : 2, 0, k);
+              if (i + 2 == n) umma_commit_if(bar(LY::Q_EMPTY), leader);
               umma_commit_if(bar(LY::KV_EMPTY + k), leader);
             }
             if (i >= hidden) clean();
@@ -727,9 +760,9 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
             if (fail) break;
             pv(i & 1 ? 2 : 0, 0, v, i == 0, i + 1 == n);
             umma_commit_if(bar(LY::KV_EMPTY + v), leader);
-            if (i + 2 == n) umma_commit_if(bar(LY::Q_EMPTY), leader);
           }
         }
+        ring += 2 * n;
       }
     } else {
       // -------------------------------------------------------- values
