@@ -286,38 +286,45 @@ __device__ __forceinline__ PrefillSeq prefill_seq(const PrefillArgs& a, int b) {
   return s;
 }
 
-// The work of one key head of a sequence, as a line: its row tiles (of `per`
-// tokens) one after the other, each as long as its keys and a constant.
+// The work of one key head of a sequence, as a line: its items, of `per` tokens
+// each (two row tiles of `half`, or one), one after the other, as long as they
+// take.
 struct PrefillLine {
-  int n, L, per, tiles, causal;
-  __device__ __forceinline__ PrefillLine(int n_, int L_, int per_, int causal_)
-      : n(n_), L(L_), per(per_), tiles((n_ + per_ - 1) / per_), causal(causal_) {}
-  // keys that row tile t sees
+  int n, L, per, half, tiles, causal;
+  __device__ __forceinline__ PrefillLine(int n_, int L_, int per_, int half_, int causal_)
+      : n(n_), L(L_), per(per_), half(half_), tiles((n_ + per_ - 1) / per_), causal(causal_) {}
+  // keys that item t sees
   __device__ __forceinline__ int keys(int t) const {
     if (!causal) return L;
     const long long last = static_cast<long long>(t + 1) * per;
     return max(0, L - n + static_cast<int>(min(last, static_cast<long long>(n))));
   }
-  __device__ __forceinline__ long long cost(int t) const { return static_cast<long long>(keys(t)) + kPrefillItemCost; }
-  // where row tile t begins
-  __device__ __forceinline__ long long begin(int t) const {
-    const long long own = static_cast<long long>(t) * kPrefillItemCost;
-    if (!causal) return own + static_cast<long long>(t) * L;
-    const long long d = static_cast<long long>(L) - n, blind = d < 0 ? -d / per : 0;   // tiles that see none
-    if (t <= blind) return own;
-    long long sum = (t - blind) * d + per * (t * (t + 1ll) - blind * (blind + 1)) / 2;
-    if (t == tiles) sum -= d + static_cast<long long>(t) * per - L;      // the last one is not whole
-    return own + sum;
+  __device__ __forceinline__ long long cost(int t) const {
+    const long long k = keys(t);
+    const bool one = half < per && n - static_cast<long long>(t) * per <= half;
+    return one ? k * kPrefillKeyCost1 + kPrefillItemCost1 : k * kPrefillKeyCost + kPrefillItemCost;
   }
-  __device__ __forceinline__ long long length() const { return begin(tiles); }
+  // where item t begins (all before the last are whole)
+  __device__ __forceinline__ long long begin(int t) const {
+    long long sum;                                  // of the keys before
+    if (!causal) {
+      sum = static_cast<long long>(t) * L;
+    } else {
+      const long long d = static_cast<long long>(L) - n, blind = d < 0 ? (n - L) / per : 0;   // items that see none
+      sum = t <= blind ? 0 : (t - blind) * d + per * ((t * (t + 1ll) - blind * (blind + 1)) / 2);
+    }
+    return static_cast<long long>(t) * kPrefillItemCost + sum * kPrefillKeyCost;
+  }
+  __device__ __forceinline__ long long length() const { return tiles > 0 ? begin(tiles - 1) + cost(tiles - 1) : 0; }
 };
 
 // Key tile of an item of `tiles` of them at which the line is cut `x` into the
-// item's `cost`: no piece is shorter than `least` tiles.
+// item's `cost`: no piece is shorter than `least` tiles.  (Both CTAs at a cut
+// work out the same.)
 __device__ __forceinline__ int prefill_cut(long long x, long long cost, int tiles, int least) {
   if (x <= 0) return 0;
   if (x >= cost) return tiles;
-  const int p = static_cast<int>((x * tiles + cost / 2) / cost);
+  const int p = min(tiles, __float2int_rn(__ll2float_rn(x) * __int2float_rn(tiles) / __ll2float_rn(cost)));
   if (tiles < 2 * least) return 2 * p <= tiles ? 0 : tiles;
   if (p < least) return 2 * p <= least ? 0 : least;
   if (tiles - p < least) return 2 * (tiles - p) <= least ? tiles : tiles - least;
@@ -380,51 +387,64 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
       // Sequences are looked at 32 at a time, a lane each.
       const int per_item = TPT * LY::NQ;            // tokens
       const int least = a.cuts != nullptr ? a.min_part : 0x3fffffff;
-      long long total = 0;
-#pragma unroll 4
-      for (int b = lane; b < a.B; b += 32) {
-        const PrefillSeq s = prefill_seq(a, b);
-        if (s.code != 0 && blockIdx.x == 0) record_error(a.err, s.code);
-        total += PrefillLine(s.n, s.L, per_item, a.causal).length();
-      }
-#pragma unroll
-      for (int i = 16; i > 0; i >>= 1) total += __shfl_xor_sync(kFullMask, total, i);
-      total *= a.Hkv;
-      auto cut_at = [&](int c) { return total * c / static_cast<int>(gridDim.x); };
-      const long long x0 = cut_at(blockIdx.x), x1 = cut_at(blockIdx.x + 1);
-
-      int chunk = -32, seq = 31;                    // sequences [chunk, chunk + 32) are looked at; of them
-      long long start = 0;                          // where the line of sequence `seq` begins
       PrefillSeq s;
-      long long length = 0;                         // of the lane's sequence, all key heads
-      // The next sequence with any row; false at the end.
-      auto next_seq = [&] {
-        start += __shfl_sync(kFullMask, length, seq);
-        for (;;) {
-          const uint32_t some = seq < 31 ? __ballot_sync(kFullMask, length > 0) >> (seq + 1) : 0;
-          if (some != 0) {
-            seq += __ffs(some);
-            return true;
-          }
-          chunk += 32;
-          if (chunk >= a.B) return false;
-          s = prefill_seq(a, chunk + lane);
-          length = PrefillLine(s.n, s.L, per_item, a.causal).length() * a.Hkv;
-          seq = -1;
+      long long mine = 0, upto = 0;                 // length of the lane's sequence, all key heads; to its end
+      auto length_of = [&](const PrefillSeq& q) {
+        return PrefillLine(q.n, q.L, per_item, TPT, a.causal).length() * a.Hkv;
+      };
+      auto look = [&](int b) {
+        s = prefill_seq(a, b + lane);
+        upto = mine = length_of(s);
+#pragma unroll
+        for (int i = 1; i < 32; i <<= 1) {
+          const long long u = __shfl_up_sync(kFullMask, upto, i);
+          if (lane >= i) upto += u;
         }
       };
+      look(0);
+      if (s.code != 0 && blockIdx.x == 0) record_error(a.err, s.code);
+      long long total = __shfl_sync(kFullMask, upto, 31);
+      if (a.B > 32) {
+        long long more = 0;
+#pragma unroll 4
+        for (int b = 32 + lane; b < a.B; b += 32) {
+          const PrefillSeq q = prefill_seq(a, b);
+          if (q.code != 0 && blockIdx.x == 0) record_error(a.err, q.code);
+          more += length_of(q);
+        }
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) more += __shfl_xor_sync(kFullMask, more, i);
+        total += more;
+      }
+      const long long share = total / gridDim.x, extra = total - share * gridDim.x;
+      auto cut_at = [&](int c) { return share * c + min(static_cast<long long>(c), extra); };
+      const long long x0 = cut_at(blockIdx.x), x1 = cut_at(blockIdx.x + 1);
+
+      // sequences [chunk, chunk + 32) are looked at; their line begins at `before`
+      int chunk = 0;
+      long long before = 0;
+      auto next_chunk = [&] {
+        before += __shfl_sync(kFullMask, upto, 31);
+        chunk += 32;
+        if (chunk < a.B) look(chunk);
+        return chunk < a.B;
+      };
       int published = 0;
-      bool more = x1 > x0 && next_seq();
-      while (more && start + __shfl_sync(kFullMask, length, seq) <= x0) more = next_seq();
+      bool more = x1 > x0;
+      while (more && before + __shfl_sync(kFullMask, upto, 31) <= x0) more = next_chunk();
       PrefillCut cut{};
       if (more) {
-        // the item that x0 is in: key head, then row tile
-        PrefillLine line(__shfl_sync(kFullMask, s.n, seq), __shfl_sync(kFullMask, s.L, seq), per_item, a.causal);
+        // the item that x0 is in: sequence, key head, item of the head's line
+        int seq = __ffs(__ballot_sync(kFullMask, before + upto > x0)) - 1;
+        const long long start = before + __shfl_sync(kFullMask, upto - mine, seq);
+        PrefillLine line(__shfl_sync(kFullMask, s.n, seq), __shfl_sync(kFullMask, s.L, seq), per_item, TPT, a.causal);
         const long long head_length = line.length();
-        int kvh = static_cast<int>((x0 - start) / head_length);
+        int kvh = min(a.Hkv - 1, __float2int_rz(__ll2float_rn(x0 - start) / __ll2float_rn(head_length)));
+        while (start + kvh * head_length > x0) --kvh;         // (the quotient was rounded)
+        while (kvh + 1 < a.Hkv && start + (kvh + 1) * head_length <= x0) ++kvh;
         long long at = start + kvh * head_length;   // where the item begins
         int tile = 0, step = line.tiles;
-        while (step > 1) {                          // the last tile that begins at or before x0
+        while (step > 1) {                          // the last one that begins at or before x0
           step = (step + 31) / 32;
           const int t = tile + lane * step;
           tile += (__popc(__ballot_sync(kFullMask, t < line.tiles && at + line.begin(t) <= x0)) - 1) * step;
@@ -476,8 +496,11 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
             tile = 0;
             if (++kvh == a.Hkv) {
               kvh = 0;
-              if (!next_seq()) break;
-              line = PrefillLine(__shfl_sync(kFullMask, s.n, seq), __shfl_sync(kFullMask, s.L, seq), per_item, a.causal);
+              uint32_t rest = seq < 31 ? __ballot_sync(kFullMask, mine > 0) >> (seq + 1) << (seq + 1) : 0;
+              while (rest == 0 && next_chunk()) rest = __ballot_sync(kFullMask, mine > 0);
+              if (rest == 0) break;
+              seq = __ffs(rest) - 1;
+              line = PrefillLine(__shfl_sync(kFullMask, s.n, seq), __shfl_sync(kFullMask, s.L, seq), per_item, TPT, a.causal);
             }
           }
         }
