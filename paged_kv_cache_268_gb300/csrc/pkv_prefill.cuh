@@ -57,7 +57,7 @@ struct PrefillLayout {
   static constexpr int OFF_KV = NQ * Q_TILE;
   static constexpr int OFF_BAR = OFF_KV + STAGES * KV_TILE;
   static constexpr int KV_FULL = 0, KV_EMPTY = STAGES, Q_FULL = 2 * STAGES, Q_EMPTY = Q_FULL + 2,
-                       S_FULL = Q_EMPTY + 2, P_FULL = S_FULL + 3, O_DONE = P_FULL + 3,
+                       S_FULL = Q_EMPTY + 2, P_FULL = S_FULL + 3, O_DONE = P_FULL + 6,
                        O_LAST = O_DONE + 2, O_FREE = O_LAST + 2, I_FULL = O_FREE + 2,
                        I_EMPTY = I_FULL + 2, V_HERE = I_EMPTY + 2, V_CLEAN = V_HERE + 2,
                        NBAR = V_CLEAN + 2;
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
 
   if (tid < LY::NBAR) {
     int count = 1;
-    if (tid >= LY::P_FULL && tid < LY::P_FULL + 3) count = 8;
+    if (tid >= LY::P_FULL && tid < LY::P_FULL + 6) count = 8;
     if (tid >= LY::O_FREE && tid < LY::O_FREE + 2) count = 8;
     if (tid >= LY::I_EMPTY && tid < LY::I_EMPTY + 2) count = SOFT + 3;
     mbar_init(bar(tid), count);
@@ -639,13 +639,23 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
                   b_lo + (kk >> 2) * (BN * 128 >> 4) + (kk & 3) * 2, kHi, idesc_qk, kk > 0, leader);
         umma_commit_if(bar(LY::S_FULL + s), leader);
       };
-      auto pv = [&](int s, int x, int at, bool first, bool last) {   // O tile x += P of buffer s . V of slot `at`
+      auto pv = [&](int s, int x, int at, uint32_t parity, bool first, bool last) {   // O tile x += P of buffer s . V of slot `at`
         tc_fence_after();
         const uint32_t b_lo = v_lo + at * (LY::KV_TILE >> 4);
+        constexpr int PARTS = BN / 64, PER = 2;     // of P; groups of 16 keys of a part, in each half
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
-          umma_ts(tmem + LY::O_COL(x), tmem + LY::S_COL(s) + LY::P_COL(kk), b_lo + v_step[kk], kHi, idesc_pv,
-                  !first || kk > 0, leader);
+        for (int q = 0; q < PARTS; ++q) {
+          if (q > 0) {
+            if (!__all_sync(kFullMask, mbar_wait_short(bar(LY::P_FULL + s + q * 3), parity))) fail = true;
+            tc_fence_after();
+          }
+#pragma unroll
+          for (int g = 0; g < 2 * PER; ++g) {
+            const int kk = (g / PER) * (BN / 32) + q * PER + g % PER;
+            umma_ts(tmem + LY::O_COL(x), tmem + LY::S_COL(s) + LY::P_COL(kk), b_lo + v_step[kk], kHi, idesc_pv,
+                    !first || g > 0 || q > 0, leader);
+          }
+        }
         umma_commit_if(bar(LY::O_DONE + x), leader);
         if (last) umma_commit_if(bar(LY::O_LAST + x), leader);
       };
@@ -730,7 +740,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
               have_p(0, su0);
               if (i == 0) have_o(0, ou0);
               if (fail) break;
-              pv(0, 0, v, i == 0, i + 1 == n0);
+              pv(0, 0, v, (su0 - 1) & 1, i == 0, i + 1 == n0);
             }
             if (fail) break;
             if (i + 1 < n0) {
@@ -757,7 +767,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
               have_p(1, su1);
               if (i == 0) have_o(1, ou1);
               if (fail) break;
-              pv(1, 1, v, i == 0, i + 1 == n1);
+              pv(1, 1, v, (su1 - 1) & 1, i == 0, i + 1 == n1);
             }
             umma_commit_if(bar(LY::KV_EMPTY + v), leader);
             if (i + 1 < n1) {
@@ -781,7 +791,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
             if (i & 1) have_p(2, su2); else have_p(0, su0);
             if (i == 0) have_o(0, ou0);
             if (fail) break;
-            pv(i & 1 ? 2 : 0, 0, v, i == 0, i + 1 == n);
+            pv(i & 1 ? 2 : 0, 0, v, (i & 1 ? su2 - 1 : su0 - 1) & 1, i == 0, i + 1 == n);
             umma_commit_if(bar(LY::KV_EMPTY + v), leader);
           }
         }
@@ -968,12 +978,13 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
             pk[e] = pack2<BF>(p.x, p.y);
           }
           tmem_st16u(mine + q * 16, pk);
+          // (a part at a time, so that the products with the first one begin)
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(LY::P_FULL + s + q * 3));
         }
         l2 = add2(sum[0], sum[1]);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(LY::P_FULL + s));
       }
       // -------------------------------------------------------- the item's rows out
       if (n > 0) {
