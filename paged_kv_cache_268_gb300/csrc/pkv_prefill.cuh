@@ -257,32 +257,20 @@ struct PrefillSeq {
   int q0, n, k0, L, code;
 };
 __device__ __forceinline__ PrefillSeq prefill_seq(const PrefillArgs& a, int b) {
-  PrefillSeq s{0, 0, 0, 0, 0};
-  if (b >= a.B) return s;
-  s.q0 = a.query_starts[b];
-  const int q1 = a.query_starts[b + 1];
-  if (s.q0 < 0 || q1 < s.q0 || q1 > a.T) {
-    s.code = kDevBadStarts;
-    return s;
-  }
-  int L;
-  if (a.key_starts != nullptr) {
-    s.k0 = a.key_starts[b];
-    const int k1 = a.key_starts[b + 1];
-    if (s.k0 < 0 || k1 < s.k0 || k1 > a.max_keys) {
-      s.code = kDevBadStarts;
-      return s;
-    }
-    L = k1 - s.k0;
-  } else {
-    L = a.context_lens[b];
-    if (L < 0 || L > a.max_keys) {
-      s.code = kDevBadContext;
-      return s;
-    }
-  }
-  s.L = L;
-  s.n = q1 - s.q0;
+  // (all loads at once)
+  const int i = min(b, a.B - 1);
+  const int q0 = a.query_starts[i], q1 = a.query_starts[i + 1];
+  const bool packed = a.key_starts != nullptr;
+  const int32_t* keys = packed ? a.key_starts : a.context_lens;
+  const int k0 = packed ? keys[i] : 0, k1 = keys[packed ? i + 1 : i];
+  const bool rows = q0 >= 0 && q1 >= q0 && q1 <= a.T, cols = k0 >= 0 && k1 >= k0 && k1 <= a.max_keys;
+  const bool fine = rows && cols && b < a.B;
+  PrefillSeq s;
+  s.q0 = q0;
+  s.n = fine ? q1 - q0 : 0;
+  s.k0 = k0;
+  s.L = fine ? k1 - k0 : 0;
+  s.code = b >= a.B || fine ? 0 : (rows && !packed ? kDevBadContext : kDevBadStarts);
   return s;
 }
 
