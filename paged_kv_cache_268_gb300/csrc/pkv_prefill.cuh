@@ -867,8 +867,8 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
     // Warps w and w + 4 of a row tile have the same rows and a half of the keys
     // each (and of the output's channels); they meet at a barrier of their own.
     // So none of them leaves an item early: after a failed wait a warp skips its
-    // later waits and runs on with whatever is there, and at the item's end the
-    // two leave together.
+    // later waits and runs on with whatever is there, and before the next item
+    // the two leave together.
     constexpr float kShift = BF ? 0.f : 7.f;        // P is 2^kShift times the weight
     constexpr int HN = BN / 2, HD = D / 2;
     const int w = warp >> 3, h = (warp >> 2) & 1, pair = 1 + w * 4 + (warp & 3);
@@ -901,6 +901,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
       const int all_see = __reduce_min_sync(kFullMask, valid ? lim : 0x7fffffff);   // last key that all of the warp's rows see
       float m = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
+      bool raised = true;                           // by the last key tile (or the item before used the exchange)
       for (int i = 0; i < n; ++i) {
         const int s = two ? w : (i & 1 ? 2 : 0);
         wait(LY::S_FULL + s, (s == 2 ? su2 : su) & 1);
@@ -927,7 +928,8 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
           for (int q = 0; q < 4; ++q) top[q] = fmaxf(top[q], fmaxf(x[e + q], x[e + 4 + q]));
         }
         const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        if (named_bar_or(pair, 64, i == 0 || (mt - m) * c > 8.f)) {
+        raised = named_bar_or(pair, 64, i == 0 || (mt - m) * c > 8.f);
+        if (raised) {
           // raise the reference to the whole row's maximum
           *own = mt;
           named_bar_sync(pair, 64);
@@ -975,12 +977,8 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         l2 = add2(sum[0], sum[1]);
       }
       // -------------------------------------------------------- the item's rows out
-      if (n > 0) {
-        wait(LY::O_LAST + w, outs & 1);
-        ++outs;
-        tc_fence_after();
-      }
-      const bool left = named_bar_or(pair, 64, fail);   // (and the last maximum has been read)
+      // (while the last products are under way)
+      if (raised) named_bar_sync(pair, 64);         // the last maximum has been read
       float l = l2.x + l2.y;
       *own = l;
       named_bar_sync(pair, 64);
@@ -1000,6 +998,11 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
       for (int e = 0; e < NC; ++e) {
         rows_at[e] = __shfl_sync(kFullMask, static_cast<unsigned long long>(row), lane - sub + e);
         rows_valid |= static_cast<uint32_t>(__shfl_sync(kFullMask, static_cast<int>(valid), lane - sub + e)) << e;
+      }
+      if (n > 0) {
+        wait(LY::O_LAST + w, outs & 1);
+        ++outs;
+        tc_fence_after();
       }
 #pragma unroll 1
       for (int q = 0; q < HD / CW; ++q) {
@@ -1079,10 +1082,6 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
       if (lane == 0) {
         if (n > 0) mbar_arrive(bar(LY::O_FREE + w));
         mbar_arrive(bar(LY::I_EMPTY + (slot & 1)));
-      }
-      if (left) {
-        fail = true;
-        break;
       }
       od += n;
     }

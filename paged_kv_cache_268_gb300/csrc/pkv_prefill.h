@@ -14,8 +14,8 @@ constexpr int prefill_key_tile(int D) { return D == 256 ? 64 : 128; }
 constexpr int kPrefillMinPart = 512;
 // What an item costs a CTA: so much a key, and so much besides (a third of what
 // a key of two row tiles takes is the unit).
-constexpr int kPrefillKeyCost = 3, kPrefillItemCost = 3 * 448;
-constexpr int kPrefillKeyCost1 = 2, kPrefillItemCost1 = 2 * 256;   // with one row tile of two
+constexpr int kPrefillKeyCost = 3, kPrefillItemCost = 3 * 512;
+constexpr int kPrefillKeyCost1 = 2, kPrefillItemCost1 = 2 * 384;   // with one row tile of two
 
 // What the reduce has to know of an item that CTA c goes on with where another
 // CTA left off (kind 0: CTA c does no such thing).
