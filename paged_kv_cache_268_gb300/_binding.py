@@ -447,7 +447,7 @@ def _kv4_dims(k_cache: torch.Tensor, v_cache: torch.Tensor) -> tuple[int, int, i
 def _sized(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
            max_blocks_per_seq, max_context_len, dtype, split_tokens=0) -> Shape:
     """A Shape, made once for the same sizes.  Read only.  It carries a reference
-    to itself for calls and, per device, the 4-bit decode's workspace size."""
+    to itself for calls and, per device, the workspace sizes of the calls that ask."""
     sizes = dict(num_seqs=num_seqs, num_q_heads=num_q_heads, num_kv_heads=num_kv_heads,
                  head_dim=head_dim, block_size=block_size, num_blocks=num_blocks,
                  max_blocks_per_seq=max_blocks_per_seq, max_context_len=max_context_len,
@@ -456,7 +456,7 @@ def _sized(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks
         if not -2 ** 31 <= x < 2 ** 31:      # the struct would hold other numbers
             raise ValueError(f"{n} must fit 32 bits, got {x}")
     shape = make_shape(**sizes, dtype=dtype)
-    shape.ref, shape.kv4_workspace = ctypes.byref(shape), {}
+    shape.ref, shape.kv4_workspace, shape.chunk_workspace = ctypes.byref(shape), {}, {}
     return shape
 
 
@@ -590,8 +590,9 @@ def _append(fn: str, kv4: bool, q, k, v, positions, cos_sin, slot_mapping, k_cac
     dims = None
     if sections is not None:
         sections = tuple(sections)
-        if any(type(n) is not int for n in sections):       # (8.0 would find the cached 8)
-            raise ValueError("sections must be whole numbers")
+        for n in sections:
+            if type(n) is not int:                          # (8.0 would find the cached 8)
+                raise ValueError("sections must be whole numbers")
     if q_out is None:
         dims = _append_plain(kv4, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, sections)
     if dims is not None:
@@ -876,6 +877,54 @@ def _check_out(out, q, workspace):
         _dense(workspace, "workspace")
 
 
+def _chunk_plain(q, k_cache, v_cache, block_tables, context_lens, query_starts) -> bool:
+    """Whether a call is the usual one, with a dense q: _check_chunk would find
+    nothing.  Looks at each tensor once (a model makes this call for every layer)."""
+    dev, qs, ks, bt, dtype = q.get_device(), q.shape, k_cache.shape, block_tables.shape, q.dtype
+    return (dev >= 0 and len(qs) == 3 and len(ks) == 4 and len(bt) == 2 and dtype in _DT
+            and ks[3] == qs[2] and v_cache.shape == ks and context_lens.shape == (bt[0],)
+            and query_starts.shape == (bt[0] + 1,) and k_cache.dtype is dtype
+            and v_cache.dtype is dtype and block_tables.dtype is _I32 and context_lens.dtype is _I32
+            and query_starts.dtype is _I32 and k_cache.get_device() == dev
+            and v_cache.get_device() == dev and block_tables.get_device() == dev
+            and context_lens.get_device() == dev and query_starts.get_device() == dev
+            and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and block_tables.is_contiguous() and context_lens.is_contiguous()
+            and query_starts.is_contiguous())
+
+
+def _check_chunk(q, k_cache, v_cache, block_tables, context_lens, query_starts, out, workspace):
+    """Refuse what does not fit together."""
+    _dense(k_cache, "k_cache")
+    _dense(v_cache, "v_cache", k_cache.dtype)
+    _dtype_code(k_cache.dtype)
+    _dense(block_tables, "block_tables", _I32)
+    _dense(context_lens, "context_lens", _I32)
+    _starts(query_starts, "query_starts")
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("caches must be [NB, Hkv, bs, D] tensors of one shape")
+    if q.dim() != 3 or q.shape[2] != k_cache.shape[3]:
+        raise ValueError("q must be [T, Hq, D] with the caches' head_dim")
+    B = query_starts.shape[0] - 1
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
+        raise ValueError("block_tables must be [B, MB], context_lens [B], query_starts [B + 1]")
+    if q.dtype != k_cache.dtype:
+        raise ValueError(f"q must be {k_cache.dtype} like the caches, got {q.dtype}")
+    _check_out(out, q, workspace)
+    _one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                context_lens=context_lens, query_starts=query_starts, out=out, workspace=workspace)
+
+
+def _chunk_memory(q, n, workspace, out):
+    """The workspace of n bytes (n = 0: as given) and out of a prompt-side call,
+    allocated where not given."""
+    if n:
+        workspace = torch.empty(n, dtype=_U8, device=q.device)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    return workspace, out
+
+
 def paged_attn_chunk(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                      block_tables: torch.Tensor, context_lens: torch.Tensor,
                      query_starts: torch.Tensor, scale: float, out: torch.Tensor | None = None, *,
@@ -893,23 +942,14 @@ def paged_attn_chunk(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     of no sequence are not written).  workspace as for paged_attn_decode
     (chunk_workspace_bytes).
     """
-    _dense(k_cache, "k_cache")
-    _dense(v_cache, "v_cache", k_cache.dtype)
-    _dense(block_tables, "block_tables", _I32)
-    _dense(context_lens, "context_lens", _I32)
-    _starts(query_starts, "query_starts")
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
-        raise ValueError("caches must be [NB, Hkv, bs, D] tensors of one shape")
-    if q.dim() != 3 or q.shape[2] != k_cache.shape[3]:
-        raise ValueError("q must be [T, Hq, D] with the caches' head_dim")
-    B = query_starts.shape[0] - 1
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
-        raise ValueError("block_tables must be [B, MB], context_lens [B], query_starts [B + 1]")
-    T, Hq, D = q.shape
-    q_stride = _token_stride(q, "q", Hq, D, T, k_cache.dtype)
-    _check_out(out, q, workspace)
-    dev = _one_device(q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                      context_lens=context_lens, query_starts=query_starts, out=out, workspace=workspace)
+    if out is not None or workspace is not None or not _chunk_plain(
+            q, k_cache, v_cache, block_tables, context_lens, query_starts):
+        _check_chunk(q, k_cache, v_cache, block_tables, context_lens, query_starts, out, workspace)
+        T, Hq, D = q.shape
+        q_stride = _token_stride(q, "q", Hq, D, T, k_cache.dtype)
+    else:
+        T, q_stride = q.shape[0], 0
+    dev = q.device
     if torch.cuda.current_device() != dev.index:
         with torch.cuda.device(dev):
             return paged_attn_chunk(q, k_cache, v_cache, block_tables, context_lens, query_starts, scale,
@@ -919,11 +959,16 @@ def paged_attn_chunk(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     shape = _chunk_sized(q, k_cache, block_tables, max_context_len, split_tokens)
     n = 0
     if workspace is None and dev.index not in _SET_WS:
-        n = chunk_workspace_bytes(shape, T)
-    if n or out is None:
-        with _allocating_on(stream):
-            workspace = torch.empty(n, dtype=_U8, device=dev) if n else workspace
-            out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev) if out is None else out
+        n = shape.chunk_workspace.get((dev.index, T))
+        if n is None:
+            if len(shape.chunk_workspace) > 4096:
+                shape.chunk_workspace.clear()
+            n = shape.chunk_workspace[dev.index, T] = chunk_workspace_bytes(shape, T)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            workspace, out = _chunk_memory(q, n, workspace, out)
+    elif n or out is None:
+        workspace, out = _chunk_memory(q, n, workspace, out)
     rc = (_LIB or load_library()).pkv_paged_attn_chunk(
         shape.ref, q.data_ptr(), q_stride, T, query_starts.data_ptr(), k_cache.data_ptr(),
         v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), float(scale),
@@ -931,6 +976,32 @@ def paged_attn_chunk(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     if rc:
         raise PkvError("pkv_paged_attn_chunk", rc)
     return out
+
+
+def _prompt_plain(q, k, v, query_starts, key_starts) -> bool:
+    """Whether a call is the usual one, everything dense: _check_prompt would
+    find nothing."""
+    dev, qs, ks, st, dtype = q.get_device(), q.shape, k.shape, query_starts.shape, q.dtype
+    return (dev >= 0 and len(qs) == 3 and len(ks) == 3 and len(st) == 1 and st[0] > 0 and dtype in _DT
+            and ks[2] == qs[2] and v.shape == ks and key_starts.shape == st and k.dtype is dtype
+            and v.dtype is dtype and query_starts.dtype is _I32 and key_starts.dtype is _I32
+            and k.get_device() == dev and v.get_device() == dev and query_starts.get_device() == dev
+            and key_starts.get_device() == dev and q.is_contiguous() and k.is_contiguous()
+            and v.is_contiguous() and query_starts.is_contiguous() and key_starts.is_contiguous())
+
+
+def _check_prompt(q, k, v, query_starts, key_starts, out, workspace):
+    """Refuse what does not fit together."""
+    _starts(query_starts, "query_starts")
+    _starts(key_starts, "key_starts")
+    if key_starts.shape != query_starts.shape:
+        raise ValueError("key_starts must be [B + 1] like query_starts")
+    if q.dim() != 3 or k.dim() != 3 or v.shape != k.shape or q.shape[2] != k.shape[2]:
+        raise ValueError("q must be [T, Hq, D]; k, v [S, Hkv, D]")
+    _dtype_code(q.dtype)
+    _check_out(out, q, workspace)
+    _one_device(q=q, k=k, v=v, query_starts=query_starts, key_starts=key_starts, out=out,
+                workspace=workspace)
 
 
 def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, query_starts: torch.Tensor,
@@ -951,20 +1022,16 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, query_starts:
     """
     if key_starts is None:
         key_starts = query_starts
-    _starts(query_starts, "query_starts")
-    _starts(key_starts, "key_starts")
-    if key_starts.shape != query_starts.shape:
-        raise ValueError("key_starts must be [B + 1] like query_starts")
-    if q.dim() != 3 or k.dim() != 3:
-        raise ValueError("q must be [T, Hq, D]; k, v [S, Hkv, D]")
-    (T, Hq, D), (S, Hkv, _) = q.shape, k.shape
-    code = _dtype_code(q.dtype)
-    qs = _token_stride(q, "q", Hq, D, T, q.dtype)
-    ks = _token_stride(k, "k", Hkv, D, S, q.dtype)
-    vs = _token_stride(v, "v", Hkv, D, S, q.dtype)
-    _check_out(out, q, workspace)
-    dev = _one_device(q=q, k=k, v=v, query_starts=query_starts, key_starts=key_starts, out=out,
-                      workspace=workspace)
+    if out is not None or workspace is not None or not _prompt_plain(q, k, v, query_starts, key_starts):
+        _check_prompt(q, k, v, query_starts, key_starts, out, workspace)
+        (T, Hq, D), (S, Hkv, _) = q.shape, k.shape
+        qs = _token_stride(q, "q", Hq, D, T, q.dtype)
+        ks = _token_stride(k, "k", Hkv, D, S, q.dtype)
+        vs = _token_stride(v, "v", Hkv, D, S, q.dtype)
+    else:
+        (T, Hq, D), (S, Hkv, _) = q.shape, k.shape
+        qs = ks = vs = 0
+    code, dev = _DT[q.dtype], q.device
     if torch.cuda.current_device() != dev.index:
         with torch.cuda.device(dev):
             return prompt_attn(q, k, v, query_starts, scale, out, key_starts=key_starts, causal=causal,
@@ -977,10 +1044,11 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, query_starts:
         n = prompt.workspace.get(dev.index)
         if n is None:
             n = prompt.workspace[dev.index] = prompt_workspace_bytes(prompt)
-    if n or out is None:
-        with _allocating_on(stream):
-            workspace = torch.empty(n, dtype=_U8, device=dev) if n else workspace
-            out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev) if out is None else out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            workspace, out = _chunk_memory(q, n, workspace, out)
+    elif n or out is None:
+        workspace, out = _chunk_memory(q, n, workspace, out)
     rc = (_LIB or load_library()).pkv_prompt_attn(
         prompt.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), query_starts.data_ptr(),
         key_starts.data_ptr(), float(scale), out.data_ptr(),
