@@ -159,31 +159,37 @@ int launch(PrefillArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUt
   return PKV_OK;
 }
 
-// What both entry points check of a batch's sizes.
-int check_sizes(int64_t q_stride, int D, int Hq, int num_tokens) {
-  if (num_tokens < 0 || (q_stride != 0 && q_stride < static_cast<int64_t>(Hq) * D)) return PKV_ERR_INVALID;
-  if (num_tokens > (1 << 30)) return PKV_ERR_UNSUPPORTED;
-  return PKV_OK;
+// A token stride (0: dense) of rows of `row` elements.
+int check_stride(int64_t stride, int64_t row) {
+  if (stride != 0 && stride < row) return PKV_ERR_INVALID;
+  // what a tensor map holds, in bytes
+  return stride >= (1ll << 39) ? PKV_ERR_UNSUPPORTED : PKV_OK;
 }
+
+// Rows and keys are counted in 32 bits, with room for the tiles' ends.
+constexpr int kMostRows = 1 << 30;
 
 int check_prompt(const pkv_prompt* p) {
   if (!p) return PKV_ERR_NULL;
-  if (p->num_seqs < 0 || p->num_q_heads < 1 || p->num_kv_heads < 1 || p->num_keys < 0 ||
-      p->split_tokens < 0 || p->num_q_heads % p->num_kv_heads != 0)
+  if (p->num_seqs < 0 || p->num_q_heads < 1 || p->num_kv_heads < 1 || p->num_tokens < 0 ||
+      p->num_keys < 0 || p->split_tokens < 0 || p->num_q_heads % p->num_kv_heads != 0)
     return PKV_ERR_INVALID;
   if (p->dtype != PKV_F16 && p->dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
   if (p->head_dim != 64 && p->head_dim != 128 && p->head_dim != 256) return PKV_ERR_UNSUPPORTED;
-  if (p->num_q_heads / p->num_kv_heads > 32 || p->num_keys > (1 << 30)) return PKV_ERR_UNSUPPORTED;
+  if (p->num_q_heads / p->num_kv_heads > 32 || p->num_tokens > kMostRows || p->num_keys > kMostRows)
+    return PKV_ERR_UNSUPPORTED;
   const int64_t kd = static_cast<int64_t>(p->num_kv_heads) * p->head_dim;
-  if ((p->k_stride != 0 && p->k_stride < kd) || (p->v_stride != 0 && p->v_stride < kd)) return PKV_ERR_INVALID;
-  return check_sizes(p->q_stride, p->head_dim, p->num_q_heads, p->num_tokens);
+  int rc = check_stride(p->q_stride, static_cast<int64_t>(p->num_q_heads) * p->head_dim);
+  if (rc == PKV_OK) rc = check_stride(p->k_stride, kd);
+  return rc == PKV_OK ? check_stride(p->v_stride, kd) : rc;
 }
 
 int check_chunk(const pkv_shape* s, int64_t q_stride, int num_tokens) {
   const int rc = check_decode_shape(s);
   if (rc != PKV_OK) return rc;
-  if (s->kernel != 0) return PKV_ERR_UNSUPPORTED;
-  return check_sizes(q_stride, s->head_dim, s->num_q_heads, num_tokens);
+  if (num_tokens < 0) return PKV_ERR_INVALID;
+  if (s->kernel != 0 || num_tokens > kMostRows || s->max_context_len > kMostRows) return PKV_ERR_UNSUPPORTED;
+  return check_stride(q_stride, static_cast<int64_t>(s->num_q_heads) * s->head_dim);
 }
 
 }  // namespace
