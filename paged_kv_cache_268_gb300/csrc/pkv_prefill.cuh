@@ -287,10 +287,12 @@ struct PrefillLine {
     const long long last = static_cast<long long>(t + 1) * per;
     return max(0, L - n + static_cast<int>(min(last, static_cast<long long>(n))));
   }
+  __device__ __forceinline__ bool one(int t) const {          // one row tile of two
+    return half < per && n - static_cast<long long>(t) * per <= half;
+  }
   __device__ __forceinline__ long long cost(int t) const {
     const long long k = keys(t);
-    const bool one = half < per && n - static_cast<long long>(t) * per <= half;
-    return one ? k * kPrefillKeyCost1 + kPrefillItemCost1 : k * kPrefillKeyCost + kPrefillItemCost;
+    return one(t) ? k * kPrefillKeyCost1 + kPrefillItemCost1 : k * kPrefillKeyCost + kPrefillItemCost;
   }
   // where item t begins (all before the last are whole)
   __device__ __forceinline__ long long begin(int t) const {
@@ -306,13 +308,16 @@ struct PrefillLine {
   __device__ __forceinline__ long long length() const { return tiles > 0 ? begin(tiles - 1) + cost(tiles - 1) : 0; }
 };
 
-// Key tile of an item of `tiles` of them at which the line is cut `x` into the
-// item's `cost`: no piece is shorter than `least` tiles.  (Both CTAs at a cut
-// work out the same.)
-__device__ __forceinline__ int prefill_cut(long long x, long long cost, int tiles, int least) {
-  if (x <= 0) return 0;
-  if (x >= cost) return tiles;
-  const int p = min(tiles, __float2int_rn(__ll2float_rn(x) * __int2float_rn(tiles) / __ll2float_rn(cost)));
+// Key tile, of BN keys, of an item at which the line is cut `x` into it: what
+// comes before costs x, the item's own cost included (which the part behind pays
+// once more, as that of every CTA that starts amid an item).  No part is shorter
+// than `least` tiles.
+template <int BN>
+__device__ __forceinline__ int prefill_cut(long long x, bool one, int tiles, int least) {
+  const int key = BN * (one ? kPrefillKeyCost1 : kPrefillKeyCost), item = one ? kPrefillItemCost1 : kPrefillItemCost;
+  const long long most = static_cast<long long>(tiles) * key;
+  const uint32_t keys = static_cast<uint32_t>(min(max(x - item + key / 2, 0ll), most));   // below 2^32: 3 a key, 2^30 keys
+  const int p = static_cast<int>(one ? keys / (BN * kPrefillKeyCost1) : keys / (BN * kPrefillKeyCost));
   if (tiles < 2 * least) return 2 * p <= tiles ? 0 : tiles;
   if (p < least) return 2 * p <= least ? 0 : least;
   if (tiles - p < least) return 2 * (tiles - p) <= least ? tiles : tiles - least;
@@ -441,7 +446,11 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         while (at < x1) {
           const long long cost = line.cost(tile);
           const int keys = line.keys(tile), tiles = (keys + BN - 1) / BN;
-          const int from = prefill_cut(x0 - at, cost, tiles, least), to = prefill_cut(x1 - at, cost, tiles, least);
+          const bool one = line.one(tile);
+          auto cut_in = [&](long long x) {          // (the item's end belongs to it)
+            return x - at >= cost ? tiles : prefill_cut<BN>(x - at, one, tiles, least);
+          };
+          const int from = cut_in(x0), to = cut_in(x1);
           if (from < to || (tiles == 0 && at >= x0)) {
             PrefillItem it;
             it.work = 1;
@@ -464,8 +473,8 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
             it.bad_values = 0;
             if (from > 0) {                         // another CTA has the keys before
               int c = blockIdx.x - 1;
-              while (prefill_cut(cut_at(c) - at, cost, tiles, least) == from) --c;
-              const bool first = prefill_cut(cut_at(c) - at, cost, tiles, least) == 0;
+              while (cut_in(cut_at(c)) == from) --c;
+              const bool first = cut_in(cut_at(c)) == 0;
               cut = PrefillCut{first ? 2 : 1, c, to == tiles, kvh, it.q_row, it.ntok};
             }
             if (published >= 2 &&
