@@ -117,8 +117,8 @@ CallSizes call_sizes(int B, int T, int Hq, int Hkv, int D, int max_keys, int spl
   const long long pieces = items * (cuts ? tiles / c.min_part : 1);
   c.grid = static_cast<unsigned>(pieces < sms ? pieces : sms);
   if (cuts && c.grid > 1) {
-    c.cut_bytes = (c.grid * sizeof(PrefillCut) + 15) / 16 * 16;
-    c.bytes = c.cut_bytes + 2ull * c.grid * c.rows * (D * 4 + 8);
+    c.cut_bytes = (c.grid * sizeof(PrefillCut) + 31) / 32 * 32;
+    c.bytes = 16 + c.cut_bytes + 2ull * c.grid * c.rows * (D * 4 + 8);   // 16: to a 32-byte boundary
   }
   return c;
 }
@@ -135,7 +135,7 @@ int launch(PrefillArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUt
       if (rc != PKV_OK) return rc;
     }
     if (!workspace || workspace_bytes < c.bytes || !aligned(workspace, 16)) return PKV_ERR_WORKSPACE;
-    uint8_t* w = static_cast<uint8_t*>(workspace);
+    uint8_t* w = static_cast<uint8_t*>(workspace) + (reinterpret_cast<uintptr_t>(workspace) & 16);
     a.cuts = reinterpret_cast<PrefillCut*>(w);
     a.part_o = reinterpret_cast<float*>(w + c.cut_bytes);
     a.part_ml = reinterpret_cast<float2*>(w + c.cut_bytes + 2ull * c.grid * c.rows * D * 4);

@@ -148,6 +148,20 @@ __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Whether both phases have ended; asked at once.
+__device__ __forceinline__ bool mbar_try_both(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1) {
+  uint32_t r0, r1;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%2], %3;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%4], %5;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\tselp.u32 %1, 1, 0, q;\n\t}"
+      : "=r"(r0), "=r"(r1)
+      : "r"(b0), "r"(p0), "r"(b1), "r"(p1)
+      : "memory");
+  return (r0 & r1) != 0;
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_lane() {
   uint32_t r;
@@ -215,7 +229,7 @@ __device__ __forceinline__ void tma_3d_if(uint32_t dst, const CUtensorMap* map, 
 
 // 32 bytes to global memory: in one piece where the address is `wide`, aligned
 // to them, else in two.
-__device__ __forceinline__ void store32(uint16_t* p, const uint32_t (&v)[8], bool wide) {
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8], bool wide) {
   if (wide) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                  "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
@@ -669,6 +683,20 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         }
         return slot;
       };
+      // Two tiles in turn: their barriers are asked at once, as an answer takes long.
+      auto landed_two = [&](int& v, int& k) {
+        v = at;
+        k = at + 1 == ST ? 0 : at + 1;
+        const uint32_t next = at + 1 == ST ? phase ^ 1 : phase;
+        const bool both = mbar_try_both(bar(LY::KV_FULL + v), phase, bar(LY::KV_FULL + k), next);
+        if (!__all_sync(kFullMask, both)) {
+          landed();
+          landed();
+          return;
+        }
+        at = k + 1 == ST ? 0 : k + 1;
+        phase = k + 1 == ST ? next ^ 1 : next;
+      };
       uint32_t qs0 = 0, qs1 = 0, su0 = 0, su1 = 0, su2 = 0, ou0 = 0, ou1 = 0;   // uses so far: Q, S buffers, O tiles
       auto have_p = [&](int s, uint32_t& uses) {    // P of S buffer s has been written
         if (!__all_sync(kFullMask, mbar_wait_short(bar(LY::P_FULL + s), uses & 1))) fail = true;
@@ -727,10 +755,12 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         ahead = false;
         if (LY::NQ == 2 && two) {
           for (int i = 0; i < n; ++i) {
-            const int v = landed();
+            int v;
             if (i + 1 < n) {
-              k = landed();
+              landed_two(v, k);
               tell(i + 1 >= hidden);
+            } else {
+              v = landed();
             }
             if (i >= hidden) clean();
             if (i < n0) {
@@ -775,9 +805,11 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
           }
         } else {
           for (int i = 0; i < n; ++i) {
-            const int v = landed();
-            if (i + 1 < n) {
-              k = landed();
+            int v;
+            if (i + 1 == n) {
+              v = landed();
+            } else {
+              landed_two(v, k);
               tell(i + 1 >= hidden);
               if (fail) break;
               qk(i & 1 ? 0 : 2, 0, k);
@@ -1033,8 +1065,12 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
           if (valid) {
             float* dst = a.part_o + prow * D + ch0;
 #pragma unroll
-            for (int e = 0; e < CW; e += 4)
-              *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < CW; e += 8) {
+              uint32_t v[8];
+#pragma unroll
+              for (int g = 0; g < 8; ++g) v[g] = __float_as_uint(o[e + g]);
+              store32(dst + e, v, true);
+            }
           }
         } else {
           uint32_t pk[NC][8];
