@@ -11,24 +11,27 @@ namespace pkv {
 namespace {
 
 constexpr int kReduceThreads = 256;
-constexpr int kReduceRows = kReduceThreads / 32;   // of a CTA, a warp each
+constexpr int kReduceRows = 2;                        // of a warp, at once (one or four: 1-2% of a call more)
+constexpr int kReduceCtaRows = kReduceThreads / 32 * kReduceRows;
 
 // Joins the pieces of the items that were cut: out = sum_p 2^(e_p - E) o_p /
 // sum_p 2^(e_p - E) l_p with E the largest exponent, in the keys' order.  CTA
 // (c, y) looks after the item whose second piece attention's CTA c had, if it
-// had one, eight of its rows.  Bound by the latency of its few loads, so each
-// step asks for all that it needs at once: the CTAs behind c, a lane each; the
-// pieces' exponents and sums, a lane each; the outputs, several pieces at a time.
+// had one, rows 16 y and up.  Bound by the latency of its few loads, so each step
+// asks for all that it needs at once: the CTAs behind c, a lane each; the pieces'
+// exponents and sums, a lane each, of two rows; these rows' outputs.
 template <bool BF, int D>
 __global__ void __launch_bounds__(kReduceThreads) prefill_reduce_kernel(const __grid_constant__ PrefillArgs a) {
-  constexpr int C = D / 32;
+  constexpr int C = D / 32, R = kReduceRows;
   pdl_wait();
   pdl_launch_dependents();
   const int c0 = blockIdx.x, lane = threadIdx.x & 31;
   const PrefillCut cut = a.cuts[c0];
-  const int row = blockIdx.y * kReduceRows + (threadIdx.x >> 5);
-  if (cut.kind != 2 || row >= cut.ntok * a.G) return;
-  float o[C] = {}, l = 0.f, top = -INFINITY;
+  const int rows = cut.ntok * a.G, row0 = blockIdx.y * kReduceCtaRows + (threadIdx.x >> 5) * R;
+  if (cut.kind != 2 || row0 >= rows) return;
+  float o[R][C] = {}, l[R] = {}, top[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) top[r] = -INFINITY;
   // 31 CTAs from c0 up at a time, and before the first of them the item's first piece
   bool more = true;
   for (int c = c0 - 1; more; c += 31) {
@@ -42,50 +45,59 @@ __global__ void __launch_bounds__(kReduceThreads) prefill_reduce_kernel(const __
     more = last == 0 && c + 32 < static_cast<int>(gridDim.x);
     const int until = last ? __ffs(last) - 1 : 31;          // the last lane with a piece of the item
     const bool have = lane == 0 ? c == c0 - 1 : kind != 0 && lane <= until;
-    const size_t at = static_cast<size_t>(lane == 0 ? 2 * mine + 1 : 2 * mine) * a.rows + row;
-    const float2 ml = have ? a.part_ml[at] : make_float2(-INFINITY, 0.f);
-    float up = ml.y != 0.f ? fmaxf(top, ml.x) : top;
+    const size_t at = static_cast<size_t>(lane == 0 ? 2 * mine + 1 : 2 * mine) * a.rows + row0;
+    float2 ml[R];
 #pragma unroll
-    for (int i = 16; i > 0; i >>= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, i));
-    const float keep = top == -INFINITY ? 0.f : fast_exp2(top - up);
-    const float w = ml.y != 0.f ? fast_exp2(ml.x - up) : 0.f;
-    float sum = w * ml.y;
+    for (int r = 0; r < R; ++r)
+      ml[r] = have && row0 + r < rows ? a.part_ml[at + r] : make_float2(-INFINITY, 0.f);
+    float w[R];
 #pragma unroll
-    for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
-    l = fmaf(l, keep, sum);
-    top = up;
+    for (int r = 0; r < R; ++r) {
+      float up = ml[r].y != 0.f ? fmaxf(top[r], ml[r].x) : top[r];
 #pragma unroll
-    for (int e = 0; e < C; ++e) o[e] *= keep;
-    uint32_t todo = __ballot_sync(0xffffffffu, have && ml.y != 0.f);
-    while (todo != 0) {
-      constexpr int U = D == 256 ? 2 : 4;                   // pieces at a time
-      float2 x[U][C / 2];
-      float wt[U];
+      for (int i = 16; i > 0; i >>= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, i));
+      const float keep = top[r] == -INFINITY ? 0.f : fast_exp2(top[r] - up);
+      w[r] = ml[r].y != 0.f ? fast_exp2(ml[r].x - up) : 0.f;
+      float sum = w[r] * ml[r].y;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int from = todo != 0 ? __ffs(todo) - 1 : 0;
-        wt[u] = __shfl_sync(0xffffffffu, w, from);
-        if (todo == 0) wt[u] = 0.f;
-        const size_t src = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(at), from);
-        const float2* p = reinterpret_cast<const float2*>(a.part_o + src * D + lane * C);
+      for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+      l[r] = fmaf(l[r], keep, sum);
+      top[r] = up;
 #pragma unroll
-        for (int e = 0; e < C / 2; ++e) x[u][e] = todo != 0 ? p[e] : make_float2(0.f, 0.f);
-        todo &= todo - 1;
+      for (int e = 0; e < C; ++e) o[r][e] *= keep;
+    }
+    for (uint32_t todo = __ballot_sync(0xffffffffu, have); todo != 0; todo &= todo - 1) {
+      const int from = __ffs(todo) - 1;
+      const size_t src = __shfl_sync(0xffffffffu, static_cast<unsigned long long>(at), from);
+      float2 x[R][C / 2];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float2* p = reinterpret_cast<const float2*>(a.part_o + (src + r) * D + lane * C);
+#pragma unroll
+        for (int e = 0; e < C / 2; ++e) x[r][e] = row0 + r < rows ? p[e] : make_float2(0.f, 0.f);
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int r = 0; r < R; ++r) {
+        const float wt = __shfl_sync(0xffffffffu, w[r], from);
+        if (__shfl_sync(0xffffffffu, ml[r].y, from) == 0.f) continue;   // sees none of its keys
 #pragma unroll
         for (int e = 0; e < C / 2; ++e) {
-          o[2 * e] = fmaf(wt[u], x[u][e].x, o[2 * e]);
-          o[2 * e + 1] = fmaf(wt[u], x[u][e].y, o[2 * e + 1]);
+          o[r][2 * e] = fmaf(wt, x[r][e].x, o[r][2 * e]);
+          o[r][2 * e + 1] = fmaf(wt, x[r][e].y, o[r][2 * e + 1]);
         }
+      }
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const size_t out = static_cast<size_t>(cut.q_row + row / a.G) * a.Hq + cut.kvh * a.G + row % a.G;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + out * D + lane * C);
 #pragma unroll
-  for (int e = 0; e < C / 2; ++e) dst[e] = pack2<BF>(o[2 * e] * inv, o[2 * e + 1] * inv);
+  for (int r = 0; r < R; ++r) {
+    const int row = row0 + r;
+    if (row >= rows) return;
+    const float inv = l[r] > 0.f ? 1.f / l[r] : 0.f;
+    const size_t out = static_cast<size_t>(cut.q_row + row / a.G) * a.Hq + cut.kvh * a.G + row % a.G;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + out * D + lane * C);
+#pragma unroll
+    for (int e = 0; e < C / 2; ++e) dst[e] = pack2<BF>(o[r][2 * e] * inv, o[r][2 * e + 1] * inv);
+  }
 }
 
 template <bool BF>
@@ -93,7 +105,7 @@ cudaError_t launch_reduce(const PrefillArgs& a, int D, unsigned ctas, cudaStream
   auto kern = prefill_reduce_kernel<BF, 64>;
   if (D == 128) kern = prefill_reduce_kernel<BF, 128>;
   if (D == 256) kern = prefill_reduce_kernel<BF, 256>;
-  return launch_pdl(kern, dim3(ctas, (a.rows + kReduceRows - 1) / kReduceRows), kReduceThreads, 0, stream, a);
+  return launch_pdl(kern, dim3(ctas, (a.rows + kReduceCtaRows - 1) / kReduceCtaRows), kReduceThreads, 0, stream, a);
 }
 
 // Sizes of a call: the grid, and the workspace where items may be cut.
