@@ -457,7 +457,8 @@ int pkv_kv4_workspace_bytes(const pkv_shape* shape, size_t* bytes);
  *   out           [T, Hq, D] dense, 16-byte aligned, not overlapping q
  *   workspace     as for pkv_paged_attn_decode, pkv_chunk_workspace_bytes long
  * A sequence whose length (PKV_DEV_BAD_CONTEXT) or rows (PKV_DEV_BAD_STARTS)
- * are out of range is skipped and its out rows are left as they were.  An
+ * are out of range is skipped and its out rows are left as they were; where
+ * query_starts fall, so that rows would be several sequences', nothing is done.  An
  * out-of-range block id among a sequence's ceil(L / bs) is not read
  * (PKV_DEV_BAD_BLOCK_ID), and that sequence's out rows are undefined.
  * num_seqs == 0 or num_tokens == 0 is a no-op.
@@ -513,7 +514,8 @@ typedef struct {
  *   out           [T, Hq, D] dense, 16-byte aligned, not overlapping q, k, v
  *   workspace     pkv_prompt_workspace_bytes long; NULL takes the workspace
  *                 set with pkv_set_workspace
- * A sequence whose starts fall or pass T or S (PKV_DEV_BAD_STARTS) is skipped.
+ * A sequence whose starts pass T or S, or whose key_starts fall, is skipped;
+ * where query_starts fall, nothing is done (PKV_DEV_BAD_STARTS).
  */
 int pkv_prompt_attn(const pkv_prompt* prompt, const void* q, const void* k, const void* v,
                     const int32_t* query_starts, const int32_t* key_starts, float scale,

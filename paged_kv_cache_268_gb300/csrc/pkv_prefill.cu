@@ -114,6 +114,7 @@ struct CallSizes {
   int rows;                      // of an item at most
   size_t cut_bytes, bytes;
   unsigned grid;
+  int small;                     // PrefillArgs
 };
 
 CallSizes call_sizes(int B, int T, int Hq, int Hkv, int D, int max_keys, int split_tokens, int sms) {
@@ -128,6 +129,9 @@ CallSizes call_sizes(int B, int T, int Hq, int Hkv, int D, int max_keys, int spl
   const long long items = (static_cast<long long>(T) / per_item + B) * Hkv;
   const long long pieces = items * (cuts ? tiles / c.min_part : 1);
   c.grid = static_cast<unsigned>(pieces < sms ? pieces : sms);
+  const double longest = static_cast<double>(max_keys) * kPrefillKeyCost + kPrefillItemCost +
+                         static_cast<double>(per_item) * kPrefillTokenCost;
+  c.small = T / per_item < kPrefillSmallItems && static_cast<double>(items) * longest < 2147483648.0;
   if (cuts && c.grid > 1) {
     c.cut_bytes = (c.grid * sizeof(PrefillCut) + 31) / 32 * 32;
     c.bytes = 16 + c.cut_bytes + 2ull * c.grid * c.rows * (D * 4 + 8);   // 16: to a 32-byte boundary
@@ -156,6 +160,7 @@ int launch(PrefillArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUt
   if (!a.err) return PKV_ERR_CUDA;
   a.rows = c.rows;
   a.min_part = c.min_part;
+  a.small = c.small;
   a.negative = scale < 0.f;
   // (a factor of zero would turn a hidden key's minus infinity into no number)
   a.scale_log2 = fmaxf(fabsf(scale) * 1.4426950408889634f, 0x1p-126f);

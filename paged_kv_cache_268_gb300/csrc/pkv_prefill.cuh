@@ -37,6 +37,8 @@
 // the device error word is set.
 #pragma once
 
+#include <type_traits>
+
 #include "pkv_prefill.h"
 #include "pkv_ptx.cuh"
 
@@ -290,6 +292,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // `code` then says what is wrong.
 struct PrefillSeq {
   int q0, n, k0, L, code;
+  bool falls;                    // its rows end before they begin: rows may be several sequences'
 };
 __device__ __forceinline__ PrefillSeq prefill_seq(const PrefillArgs& a, int b) {
   // (all loads at once)
@@ -305,17 +308,26 @@ __device__ __forceinline__ PrefillSeq prefill_seq(const PrefillArgs& a, int b) {
   s.n = fine ? q1 - q0 : 0;
   s.k0 = k0;
   s.L = fine ? k1 - k0 : 0;
+  s.falls = b < a.B && q1 < q0;
   s.code = b >= a.B || fine ? 0 : (rows && !packed ? kDevBadContext : kDevBadStarts);
   return s;
 }
 
 // The work of one key head of a sequence, as a line: its items, of `per` tokens
 // each (two row tiles of `half`, or one), one after the other, as long as they
-// take.
+// take.  I: the integers of lengths.
+template <typename I>
 struct PrefillLine {
-  int n, L, per, half, tiles, causal;
+  int n, L, per, half, tiles, causal, item, item1;
   __device__ __forceinline__ PrefillLine(int n_, int L_, int per_, int half_, int causal_)
-      : n(n_), L(L_), per(per_), half(half_), tiles((n_ + per_ - 1) / per_), causal(causal_) {}
+      : n(n_), L(L_), per(per_), half(half_), tiles((n_ + per_ - 1) / per_), causal(causal_),
+        item(kPrefillItemCost + (causal_ ? per_ * kPrefillTokenCost : 0)),
+        item1(kPrefillItemCost1 + (causal_ ? half_ * kPrefillTokenCost : 0)) {}
+  // (products that wrap in 32 bits where their sum does not)
+  static __device__ __forceinline__ I mul(I a, I b) {
+    using U = std::make_unsigned_t<I>;
+    return static_cast<I>(static_cast<U>(a) * static_cast<U>(b));
+  }
   // keys that item t sees
   __device__ __forceinline__ int keys(int t) const {
     if (!causal) return L;
@@ -325,33 +337,34 @@ struct PrefillLine {
   __device__ __forceinline__ bool one(int t) const {          // one row tile of two
     return half < per && n - static_cast<long long>(t) * per <= half;
   }
-  __device__ __forceinline__ long long cost(int t) const {
-    const long long k = keys(t);
-    return one(t) ? k * kPrefillKeyCost1 + kPrefillItemCost1 : k * kPrefillKeyCost + kPrefillItemCost;
+  __device__ __forceinline__ I cost(int t) const {
+    const I k = keys(t);
+    return one(t) ? k * kPrefillKeyCost1 + item1 : k * kPrefillKeyCost + item;
   }
   // where item t begins (all before the last are whole)
-  __device__ __forceinline__ long long begin(int t) const {
-    long long sum;                                  // of the keys before
+  __device__ __forceinline__ I begin(int t) const {
+    I sum;                                          // of the keys before
     if (!causal) {
-      sum = static_cast<long long>(t) * L;
+      sum = mul(t, L);
     } else {
-      const long long d = static_cast<long long>(L) - n, blind = d < 0 ? (n - L) / per : 0;   // items that see none
-      sum = t <= blind ? 0 : (t - blind) * d + per * ((t * (t + 1ll) - blind * (blind + 1)) / 2);
+      const int d = L - n, blind = d < 0 ? -d / per : 0;      // items that see none
+      const I i = t, b = blind;
+      sum = t <= blind ? 0 : static_cast<I>(static_cast<std::make_unsigned_t<I>>(mul(i - b, d)) + mul(per, (i * (i + 1) - b * (b + 1)) / 2));
     }
-    return static_cast<long long>(t) * kPrefillItemCost + sum * kPrefillKeyCost;
+    return t * static_cast<I>(item) + sum * kPrefillKeyCost;
   }
-  __device__ __forceinline__ long long length() const { return tiles > 0 ? begin(tiles - 1) + cost(tiles - 1) : 0; }
+  __device__ __forceinline__ I length() const { return tiles > 0 ? begin(tiles - 1) + cost(tiles - 1) : 0; }
 };
 
 // Key tile, of BN keys, of an item at which the line is cut `x` into it: what
 // comes before costs x, the item's own cost included (which the part behind pays
 // once more, as that of every CTA that starts amid an item).  No part is shorter
 // than `least` tiles.
-template <int BN>
-__device__ __forceinline__ int prefill_cut(long long x, bool one, int tiles, int least) {
-  const int key = BN * (one ? kPrefillKeyCost1 : kPrefillKeyCost), item = one ? kPrefillItemCost1 : kPrefillItemCost;
-  const long long most = static_cast<long long>(tiles) * key;
-  const uint32_t keys = static_cast<uint32_t>(min(max(x - item + key / 2, 0ll), most));   // below 2^32: 3 a key, 2^30 keys
+template <int BN, typename I>
+__device__ __forceinline__ int prefill_cut(I x, bool one, int item, int tiles, int least) {
+  const int key = BN * (one ? kPrefillKeyCost1 : kPrefillKeyCost);
+  const I most = static_cast<I>(tiles) * key;
+  const uint32_t keys = static_cast<uint32_t>(min(max(x - item + key / 2, static_cast<I>(0)), most));   // below 2^32: 3 a key, 2^30 keys
   const int p = static_cast<int>(one ? keys / (BN * kPrefillKeyCost1) : keys / (BN * kPrefillKeyCost));
   if (tiles < 2 * least) return 2 * p <= tiles ? 0 : tiles;
   if (p < least) return 2 * p <= least ? 0 : least;
@@ -415,42 +428,46 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
       // Sequences are looked at 32 at a time, a lane each.
       const int per_item = TPT * LY::NQ;            // tokens
       const int least = a.cuts != nullptr ? a.min_part : 0x3fffffff;
+      auto schedule = [&](auto zero) {
+      using I = decltype(zero);
       PrefillSeq s;
-      long long mine = 0, upto = 0;                 // length of the lane's sequence, all key heads; to its end
+      I mine = 0, upto = 0;                 // length of the lane's sequence, all key heads; to its end
       auto length_of = [&](const PrefillSeq& q) {
-        return PrefillLine(q.n, q.L, per_item, TPT, a.causal).length() * a.Hkv;
+        return PrefillLine<I>(q.n, q.L, per_item, TPT, a.causal).length() * a.Hkv;
       };
       auto look = [&](int b) {
         s = prefill_seq(a, b + lane);
         upto = mine = length_of(s);
 #pragma unroll
         for (int i = 1; i < 32; i <<= 1) {
-          const long long u = __shfl_up_sync(kFullMask, upto, i);
+          const I u = __shfl_up_sync(kFullMask, upto, i);
           if (lane >= i) upto += u;
         }
       };
       look(0);
       if (s.code != 0 && blockIdx.x == 0) record_error(a.err, s.code);
-      long long total = __shfl_sync(kFullMask, upto, 31);
+      I total = __shfl_sync(kFullMask, upto, 31);
+      bool falls = s.falls;
       if (a.B > 32) {
-        long long more = 0;
+        I more = 0;
 #pragma unroll 4
         for (int b = 32 + lane; b < a.B; b += 32) {
           const PrefillSeq q = prefill_seq(a, b);
           if (q.code != 0 && blockIdx.x == 0) record_error(a.err, q.code);
+          falls |= q.falls;
           more += length_of(q);
         }
 #pragma unroll
         for (int i = 16; i > 0; i >>= 1) more += __shfl_xor_sync(kFullMask, more, i);
         total += more;
       }
-      const long long share = total / gridDim.x, extra = total - share * gridDim.x;
-      auto cut_at = [&](int c) { return share * c + min(static_cast<long long>(c), extra); };
-      const long long x0 = cut_at(blockIdx.x), x1 = cut_at(blockIdx.x + 1);
+      const I share = total / static_cast<int>(gridDim.x), extra = total - share * static_cast<int>(gridDim.x);
+      auto cut_at = [&](int c) { return share * c + min(static_cast<I>(c), extra); };
+      const I x0 = cut_at(blockIdx.x), x1 = cut_at(blockIdx.x + 1);
 
       // sequences [chunk, chunk + 32) are looked at; their line begins at `before`
       int chunk = 0;
-      long long before = 0;
+      I before = 0;
       auto next_chunk = [&] {
         before += __shfl_sync(kFullMask, upto, 31);
         chunk += 32;
@@ -458,19 +475,20 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         return chunk < a.B;
       };
       int published = 0;
-      bool more = x1 > x0;
+      // (without a fall the sequences' rows are T at most, which bounds the total)
+      bool more = !__any_sync(kFullMask, falls) && x1 > x0;
       while (more && before + __shfl_sync(kFullMask, upto, 31) <= x0) more = next_chunk();
       PrefillCut cut{};
       if (more) {
         // the item that x0 is in: sequence, key head, item of the head's line
         int seq = __ffs(__ballot_sync(kFullMask, before + upto > x0)) - 1;
-        const long long start = before + __shfl_sync(kFullMask, upto - mine, seq);
-        PrefillLine line(__shfl_sync(kFullMask, s.n, seq), __shfl_sync(kFullMask, s.L, seq), per_item, TPT, a.causal);
-        const long long head_length = line.length();
-        int kvh = min(a.Hkv - 1, __float2int_rz(__ll2float_rn(x0 - start) / __ll2float_rn(head_length)));
+        const I start = before + __shfl_sync(kFullMask, upto - mine, seq);
+        PrefillLine<I> line(__shfl_sync(kFullMask, s.n, seq), __shfl_sync(kFullMask, s.L, seq), per_item, TPT, a.causal);
+        const I head_length = line.length();
+        int kvh = min(a.Hkv - 1, __float2int_rz(static_cast<float>(x0 - start) / static_cast<float>(head_length)));
         while (start + kvh * head_length > x0) --kvh;         // (the quotient was rounded)
         while (kvh + 1 < a.Hkv && start + (kvh + 1) * head_length <= x0) ++kvh;
-        long long at = start + kvh * head_length;   // where the item begins
+        I at = start + kvh * head_length;           // where the item begins
         int tile = 0, step = line.tiles;
         while (step > 1) {                          // the last one that begins at or before x0
           step = (step + 31) / 32;
@@ -479,11 +497,11 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         }
         at += line.begin(tile);
         while (at < x1) {
-          const long long cost = line.cost(tile);
+          const I cost = line.cost(tile);
           const int keys = line.keys(tile), tiles = (keys + BN - 1) / BN;
           const bool one = line.one(tile);
-          auto cut_in = [&](long long x) {          // (the item's end belongs to it)
-            return x - at >= cost ? tiles : prefill_cut<BN>(x - at, one, tiles, least);
+          auto cut_in = [&](I x) {                  // (the item's end belongs to it)
+            return x - at >= cost ? tiles : prefill_cut<BN>(x - at, one, one ? line.item1 : line.item, tiles, least);
           };
           const int from = cut_in(x0), to = cut_in(x1);
           if (from < to || (tiles == 0 && at >= x0)) {
@@ -532,7 +550,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
               while (rest == 0 && next_chunk()) rest = __ballot_sync(kFullMask, mine > 0);
               if (rest == 0) break;
               seq = __ffs(rest) - 1;
-              line = PrefillLine(__shfl_sync(kFullMask, s.n, seq), __shfl_sync(kFullMask, s.L, seq), per_item, TPT, a.causal);
+              line = PrefillLine<I>(__shfl_sync(kFullMask, s.n, seq), __shfl_sync(kFullMask, s.L, seq), per_item, TPT, a.causal);
             }
           }
         }
@@ -547,6 +565,8 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
           mbar_arrive(bar(LY::I_FULL + (published & 1)));
         }
       }
+      };
+      if (a.small) schedule(0); else schedule(0ll);
     } else if (warp == SOFT) {
       // -------------------------------------------------------- producer
       const uint32_t leader = elect_lane();

@@ -13,9 +13,13 @@ constexpr int prefill_key_tile(int D) { return D == 256 ? 64 : 128; }
 // Keys of the smallest part of an item's keys that a CTA is given.
 constexpr int kPrefillMinPart = 512;
 // What an item costs a CTA: so much a key, and so much besides (a third of what
-// a key of two row tiles takes is the unit).
-constexpr int kPrefillKeyCost = 3, kPrefillItemCost = 3 * 512;
-constexpr int kPrefillKeyCost1 = 2, kPrefillItemCost1 = 2 * 384;   // with one row tile of two
+// a key of two row tiles takes is the unit), where it is causal more for its
+// tokens, as key tiles that hide something take longer.
+constexpr int kPrefillKeyCost = 3, kPrefillItemCost = 3 * 320, kPrefillTokenCost = 3;
+constexpr int kPrefillKeyCost1 = 2, kPrefillItemCost1 = 2 * 320;   // with one row tile of two
+// Below so many items a key head, and lines of less than 2^31 in all, the
+// scheduler counts in 32 bits.
+constexpr int kPrefillSmallItems = 30000;
 
 // What the reduce has to know of an item that CTA c goes on with where another
 // CTA left off (kind 0: CTA c does no such thing).
@@ -45,6 +49,7 @@ struct PrefillArgs {
   int causal, negative;          // negative: the scale is
   int rows;                      // of an item at most
   int min_part;                  // key tiles of a piece at least
+  int small;                     // the scheduler may count in 32 bits
   float scale_log2;              // |softmax scale| * log2(e)
 };
 

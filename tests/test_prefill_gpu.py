@@ -227,6 +227,34 @@ def test_bad_device_values_are_reported_and_harmless(pkv):
     x = torch.full_like(q, 7.0)
     pkv.prompt_attn(q, k, v, _i32([0, 20, 10, 30]), 0.1, x, key_starts=_i32([0, 100, 50, 361]))
     assert pkv.get_device_error() == 6
+    # starts that fall: rows would be several sequences', nothing is done
+    assert bool((x == 7).all())
+    many = torch.randint(-5, 40, (200,), generator=g).tolist()
+    pkv.prompt_attn(q, k, v, _i32(many), 0.1, x, key_starts=_i32([0] * 100 + [360] * 100))
+    assert pkv.get_device_error() == 6 and bool((x == 7).all())
+    # keys that fall leave out their sequence only
+    pkv.prompt_attn(q, k, v, _i32([0, 10, 20, 30]), 0.1, x, key_starts=_i32([0, 100, 50, 360]))
+    assert pkv.get_device_error() == 6 and bool((x[10:20] == 7).all())
+    ref, bound = R.attend(q[:10], k[:100], v[:100], 0.1)
+    R.check(x[:10], ref, bound)
+    ref, bound = R.attend(q[20:], k[50:], v[50:], 0.1)
+    R.check(x[20:], ref, bound)
+
+
+def test_lengths_counted_in_64_bits(pkv):
+    """A bound of the lengths that is far above them: the work is counted in 64
+    bits, the rows are the same."""
+    g = torch.Generator().manual_seed(13)
+    for D, new, lens in ((128, [300, 1, 40], [900, 3000, 40]), (256, [70, 9], [400, 1500]), (64, [500], [600])):
+        q = _rows(sum(new), 8, 2, D, F16, g)[0]
+        _, k, v = _rows(sum(lens), 8, 2, D, F16, g)
+        kc, vc, tables = R.paged(k, v, lens, 32, g)
+        wide = torch.full((len(new), 1 << 23), -1, dtype=torch.int32)
+        wide[:, :tables.shape[1]] = tables
+        out = pkv.paged_attn_chunk(q, kc.cuda(), vc.cuda(), wide.cuda(), _i32(lens), _i32(R.starts(new)), 0.1)
+        ref, bound = R.packed(q, k, v, R.starts(new), R.starts(lens), 0.1)
+        assert pkv.get_device_error() == 0
+        R.check(out, ref, bound)
 
 
 def test_offsets_past_32_bits(pkv):

@@ -188,7 +188,7 @@ def test_sizes_past_32_bits_are_refused():
 # The scheduler's arithmetic once more, in Python integers: items of a key head
 # lie on a line, the lines one after the other are cut into equal lengths, one a
 # CTA, and a cut is moved to a key tile that leaves no piece too short.
-KEY, ITEM, KEY1, ITEM1 = 3, 3 * 512, 2, 2 * 384
+KEY, ITEM, TOKEN, KEY1, ITEM1 = 3, 3 * 320, 3, 2, 2 * 320
 
 
 def _keys(n, L, per, t, causal):
@@ -197,7 +197,9 @@ def _keys(n, L, per, t, causal):
 
 def _cost(n, L, per, half, t, causal):
     k = _keys(n, L, per, t, causal)
-    return k * KEY1 + ITEM1 if half < per and n - t * per <= half else k * KEY + ITEM
+    if half < per and n - t * per <= half:
+        return k * KEY1 + ITEM1 + causal * half * TOKEN
+    return k * KEY + ITEM + causal * per * TOKEN
 
 
 def _begin(n, L, per, t, causal):
@@ -207,7 +209,7 @@ def _begin(n, L, per, t, causal):
         d = L - n
         blind = (n - L) // per if d < 0 else 0
         keys = 0 if t <= blind else (t - blind) * d + per * ((t * (t + 1) - blind * (blind + 1)) // 2)
-    return t * ITEM + keys * KEY
+    return t * (ITEM + causal * per * TOKEN) + keys * KEY
 
 
 @pytest.mark.parametrize("causal", [True, False])
@@ -226,5 +228,6 @@ def test_the_constants_are_the_kernels():
     import os
     import re
     text = open(os.path.join(build.CSRC, "pkv_prefill.h")).read()
-    got = {k: eval(v) for k, v in re.findall(r"(kPrefill(?:Key|Item)Cost1?) = ([0-9* ]+)[,;]", text)}
-    assert got == dict(kPrefillKeyCost=KEY, kPrefillItemCost=ITEM, kPrefillKeyCost1=KEY1, kPrefillItemCost1=ITEM1)
+    got = {k: eval(v) for k, v in re.findall(r"(kPrefill(?:Key|Item|Token)Cost1?) = ([0-9* ]+)[,;]", text)}
+    assert got == dict(kPrefillKeyCost=KEY, kPrefillItemCost=ITEM, kPrefillTokenCost=TOKEN,
+                       kPrefillKeyCost1=KEY1, kPrefillItemCost1=ITEM1)
