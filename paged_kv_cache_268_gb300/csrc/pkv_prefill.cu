@@ -117,11 +117,16 @@ struct CallSizes {
   int small;                     // PrefillArgs
 };
 
+// Keys that a CTA is asked to take of a sequence at most: its warps wait for one
+// another for half a second, which longer pieces could take.
+constexpr int kMostPart = 1 << 20;
+
 CallSizes call_sizes(int B, int T, int Hq, int Hkv, int D, int max_keys, int split_tokens, int sms) {
   CallSizes c{};
   const int BN = prefill_key_tile(D), G = Hq / Hkv;
   const int per_item = 128 / G * prefill_row_tiles(D);
-  c.min_part = ((split_tokens > 0 ? split_tokens : kPrefillMinPart) - 1) / BN + 1;
+  const int part = split_tokens > 0 ? (split_tokens < kMostPart ? split_tokens : kMostPart) : kPrefillMinPart;
+  c.min_part = (part - 1) / BN + 1;
   c.rows = (T < per_item ? T : per_item) * G;
   const int tiles = max_keys > 0 ? (max_keys - 1) / BN + 1 : 1;
   const bool cuts = tiles >= 2ll * c.min_part;
@@ -163,7 +168,8 @@ int launch(PrefillArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUt
   a.small = c.small;
   a.negative = scale < 0.f;
   // (a factor of zero would turn a hidden key's minus infinity into no number)
-  a.scale_log2 = fmaxf(fabsf(scale) * 1.4426950408889634f, 0x1p-126f);
+  a.scale_log2 = fabsf(scale) * 1.4426950408889634f;
+  if (a.scale_log2 < 0x1p-126f) a.scale_log2 = 0x1p-126f;
   cudaError_t e = bf ? launch_prefill_bf16(a, q, k, v, D, c.grid, stream)
                      : launch_prefill_f16(a, q, k, v, D, c.grid, stream);
   if (e != cudaSuccess) return PKV_ERR_CUDA;

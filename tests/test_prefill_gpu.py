@@ -82,6 +82,11 @@ def test_chunk_scales(pkv, scale):
         _chunk(pkv, [70, 1], [300, 200], 6, 2, D, 16, F16, scale=scale)
 
 
+def test_a_scale_that_is_no_number(pkv):
+    x = torch.randn((9, 2, 64), device="cuda").half()
+    assert bool(pkv.prompt_attn(x, x, x, _i32([0, 9]), float("nan")).isnan().all())
+
+
 def _prompt(pkv, nq, nk, hq, hkv, D, dt, causal, seed=0, fused=False, scale=None, **kw):
     g = torch.Generator().manual_seed(seed)
     scale = D ** -0.5 if scale is None else scale
