@@ -512,13 +512,22 @@ def _token_stride(t: torch.Tensor, name: str, heads: int, D: int, T: int, dtype)
     return t.stride(0) if T > 1 else 0
 
 
+def _plain_stride(t: torch.Tensor, heads: int, D: int) -> int:
+    """_token_stride of a tensor [T, heads, D] that is dense (0) or a slice of
+    wider rows; -1 for any other, which _token_stride looks at in full."""
+    if t.is_contiguous():
+        return 0
+    a, b, c = t.stride()
+    return a if c == 1 and b == D and a >= heads * D else -1
+
+
 _I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
 
 
 def _append_plain(kv4: bool, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, sections):
-    """(NB, Hkv, bs, D) of the usual call (everything dense, on one GPU, of
-    fitting sizes), of which _check_append would find nothing to refuse; else
-    None.  A decode step makes this call for every layer, so it looks at each
+    """(NB, Hkv, bs, D) and the token strides of q, k and v of the usual call
+    (rows dense or slices of wider ones, the rest dense, on one GPU, of fitting
+    sizes), of which _check_append would find nothing to refuse; else None.  A decode step makes this call for every layer, so it looks at each
     tensor once."""
     if q is None or cos_sin is None or positions is None:
         return None
@@ -539,11 +548,12 @@ def _append_plain(kv4: bool, q, k, v, positions, cos_sin, slot_mapping, k_cache,
             and q.get_device() == dev and k.get_device() == dev and v.get_device() == dev
             and v_cache.get_device() == dev and slot_mapping.get_device() == dev
             and positions.get_device() == dev and cos_sin.get_device() == dev
-            and q.is_contiguous() and k.is_contiguous() and v.is_contiguous()
             and k_cache.is_contiguous() and v_cache.is_contiguous()
             and slot_mapping.is_contiguous() and positions.is_contiguous()
             and cos_sin.is_contiguous()):
-        return NB, Hkv, bs, D
+        strides = _plain_stride(q, qs[1], D), _plain_stride(k, Hkv, D), _plain_stride(v, Hkv, D)
+        if min(strides) >= 0:
+            return (NB, Hkv, bs, D), strides
     return None
 
 
@@ -596,7 +606,8 @@ def _append(fn: str, kv4: bool, q, k, v, positions, cos_sin, slot_mapping, k_cac
     if q_out is None:
         dims = _append_plain(kv4, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, sections)
     if dims is not None:
-        dtype, qs, ks, vs = k.dtype, 0, 0, 0
+        dims, (qs, ks, vs) = dims
+        dtype = k.dtype
     else:
         if kv4:
             dims, dtype = _kv4_dims(k_cache, v_cache), k.dtype
@@ -878,7 +889,7 @@ def _check_out(out, q, workspace):
 
 
 def _chunk_plain(q, k_cache, v_cache, block_tables, context_lens, query_starts) -> bool:
-    """Whether a call is the usual one, with a dense q: _check_chunk would find
+    """Whether a call is the usual one, q's rows aside: _check_chunk would find
     nothing.  Looks at each tensor once (a model makes this call for every layer)."""
     dev, qs, ks, bt, dtype = q.get_device(), q.shape, k_cache.shape, block_tables.shape, q.dtype
     return (dev >= 0 and len(qs) == 3 and len(ks) == 4 and len(bt) == 2 and dtype in _DT
@@ -888,9 +899,8 @@ def _chunk_plain(q, k_cache, v_cache, block_tables, context_lens, query_starts) 
             and query_starts.dtype is _I32 and k_cache.get_device() == dev
             and v_cache.get_device() == dev and block_tables.get_device() == dev
             and context_lens.get_device() == dev and query_starts.get_device() == dev
-            and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
-            and block_tables.is_contiguous() and context_lens.is_contiguous()
-            and query_starts.is_contiguous())
+            and k_cache.is_contiguous() and v_cache.is_contiguous() and block_tables.is_contiguous()
+            and context_lens.is_contiguous() and query_starts.is_contiguous())
 
 
 def _check_chunk(q, k_cache, v_cache, block_tables, context_lens, query_starts, out, workspace):
@@ -942,13 +952,15 @@ def paged_attn_chunk(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     of no sequence are not written).  workspace as for paged_attn_decode
     (chunk_workspace_bytes).
     """
-    if out is not None or workspace is not None or not _chunk_plain(
-            q, k_cache, v_cache, block_tables, context_lens, query_starts):
+    q_stride = -1
+    if out is None and workspace is None and _chunk_plain(q, k_cache, v_cache, block_tables, context_lens,
+                                                          query_starts):
+        T, Hq, D = q.shape
+        q_stride = _plain_stride(q, Hq, D)
+    if q_stride < 0:
         _check_chunk(q, k_cache, v_cache, block_tables, context_lens, query_starts, out, workspace)
         T, Hq, D = q.shape
         q_stride = _token_stride(q, "q", Hq, D, T, k_cache.dtype)
-    else:
-        T, q_stride = q.shape[0], 0
     dev = q.device
     if torch.cuda.current_device() != dev.index:
         with torch.cuda.device(dev):
@@ -979,15 +991,15 @@ def paged_attn_chunk(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
 
 
 def _prompt_plain(q, k, v, query_starts, key_starts) -> bool:
-    """Whether a call is the usual one, everything dense: _check_prompt would
-    find nothing."""
+    """Whether a call is the usual one, its rows' strides aside: _check_prompt
+    would find nothing."""
     dev, qs, ks, st, dtype = q.get_device(), q.shape, k.shape, query_starts.shape, q.dtype
     return (dev >= 0 and len(qs) == 3 and len(ks) == 3 and len(st) == 1 and st[0] > 0 and dtype in _DT
             and ks[2] == qs[2] and v.shape == ks and key_starts.shape == st and k.dtype is dtype
             and v.dtype is dtype and query_starts.dtype is _I32 and key_starts.dtype is _I32
             and k.get_device() == dev and v.get_device() == dev and query_starts.get_device() == dev
-            and key_starts.get_device() == dev and q.is_contiguous() and k.is_contiguous()
-            and v.is_contiguous() and query_starts.is_contiguous() and key_starts.is_contiguous())
+            and key_starts.get_device() == dev and query_starts.is_contiguous()
+            and key_starts.is_contiguous())
 
 
 def _check_prompt(q, k, v, query_starts, key_starts, out, workspace):
@@ -1022,15 +1034,16 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, query_starts:
     """
     if key_starts is None:
         key_starts = query_starts
-    if out is not None or workspace is not None or not _prompt_plain(q, k, v, query_starts, key_starts):
+    qs = -1
+    if out is None and workspace is None and _prompt_plain(q, k, v, query_starts, key_starts):
+        (T, Hq, D), (S, Hkv, _) = q.shape, k.shape
+        qs, ks, vs = _plain_stride(q, Hq, D), _plain_stride(k, Hkv, D), _plain_stride(v, Hkv, D)
+    if qs < 0 or ks < 0 or vs < 0:
         _check_prompt(q, k, v, query_starts, key_starts, out, workspace)
         (T, Hq, D), (S, Hkv, _) = q.shape, k.shape
         qs = _token_stride(q, "q", Hq, D, T, q.dtype)
         ks = _token_stride(k, "k", Hkv, D, S, q.dtype)
         vs = _token_stride(v, "v", Hkv, D, S, q.dtype)
-    else:
-        (T, Hq, D), (S, Hkv, _) = q.shape, k.shape
-        qs = ks = vs = 0
     code, dev = _DT[q.dtype], q.device
     if torch.cuda.current_device() != dev.index:
         with torch.cuda.device(dev):
