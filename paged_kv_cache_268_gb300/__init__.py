@@ -1,4 +1,4 @@
-"""Paged KV-cache decode attention for GB300 (sm_103a).
+"""Paged KV-cache attention, prompts and decode, for GB300 (sm_103a).
 
 The compute lives in ``lib/libpkv.so`` (hand-written CUDA behind the C ABI in
 ``include/pkv.h``); this package is a thin ctypes binding over it, plus the

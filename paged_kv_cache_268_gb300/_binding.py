@@ -949,8 +949,9 @@ def paged_attn_chunk(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     bs, D]; block_tables [B, MB] int32; context_lens [B] int32 count the new
     tokens.  Row j of a sequence's n sees the tokens up to position
     context_len - n + j.  Returns out [T, Hq, D] (allocated if not given; rows
-    of no sequence are not written).  workspace as for paged_attn_decode
-    (chunk_workspace_bytes).
+    of no sequence are not written).  split_tokens: the keys of the smallest part
+    of a sequence that a CTA takes, 0 = library's choice.  workspace as for
+    paged_attn_decode (chunk_workspace_bytes).
     """
     q_stride = -1
     if out is None and workspace is None and _chunk_plain(q, k_cache, v_cache, block_tables, context_lens,
@@ -1029,8 +1030,8 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, query_starts:
     causal: a query sees the keys up to its position, the last query standing
     at the last key (more keys than queries: a prefix).  A row that sees no key
     is zero.  Returns out [T, Hq, D] (allocated if not given; rows of no
-    sequence are not written).  workspace as for paged_attn_decode
-    (prompt_workspace_bytes).
+    sequence are not written).  split_tokens as for paged_attn_chunk; workspace
+    as for paged_attn_decode (prompt_workspace_bytes).
     """
     if key_starts is None:
         key_starts = query_starts

@@ -1,8 +1,8 @@
 """Build libpkv.so (sm_103a) in-tree with nvcc.
 
 The decode kernels are split over four translation units (element type x
-kernel variant) plus the C-ABI front end, the rotation append and the 4-bit
-cache's kernels, compiled in parallel and linked into ``paged_kv_cache_268_gb300/lib/libpkv.so``.  Run ``python -m
+kernel variant) plus the C-ABI front end, the rotation append, the 4-bit
+cache's kernels and prompt-side attention, compiled in parallel and linked into ``paged_kv_cache_268_gb300/lib/libpkv.so``.  Run ``python -m
 paged_kv_cache_268_gb300.build`` or call ``build()``.
 """
 from __future__ import annotations

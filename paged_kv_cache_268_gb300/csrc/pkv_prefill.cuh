@@ -22,7 +22,12 @@
 // the next keys, P1 V, S1 of the next keys.  With a single row tile the two S
 // buffers take the key tiles in turn instead, S one tile ahead of P.
 // m follows the row's running maximum only where that grows by more than 2^8;
-// then O and the sum are rescaled (rare: the first key tile sets it).  P in
+// then O and the sum are rescaled (rare: the first key tile sets it).  P is held
+// in the inputs' type, as the tensor cores want both operands alike; that adds
+// half a step of the type to each weight (the whole result of bfloat16 rows is
+// then off by 1.4 times the store's own rounding, in the mean; a second product
+// with the rest of P, which the decode kernels can afford as bytes bound them,
+// would cost half of the rate here).  P in
 // binary16 is scaled by 2^7 so that weights of down to 2^-21 of the largest
 // keep all their bits; the largest, 2^15, is still in range.  The sums are of
 // P in FP32, before its rounding.
@@ -32,6 +37,27 @@
 // cleared, and those that are no numbers as well (and kept in mind: at the
 // end they are added for the rows that see them, whose weights are positive).
 // A warp does so as the tiles land, before their products.
+//
+// What bounds it.  Long rows: 128 keys of 2 x 128 rows are 2048 cycles of matrix
+// products (128 channels) and take about 2650, of which no part of the softmax
+// alone is worth more than 3% (its exponentials, its maximum or its meeting
+// left out one at a time); an item costs 6000 cycles besides (first scores, O to
+// memory), a call 5 us until its first loads and the reduce after it.  Few rows:
+// the cache's bytes.  Measured on one GB300, graph-timed, bfloat16, 32 heads of 128
+// on 8: a prompt of 8192 tokens 331 us, 1660 TFLOP/s, 0.85 of the library's
+// 8192^3 product; 2048 tokens after 8192 in blocks of 16 191 us, 1620; 4 x 8 tokens of
+// 64/8 heads after 32760 each 88 us, 6.1 TB/s, 0.90 of a copy; without a mask,
+// 4096 tokens, head_dim 64 / 128 / 256: 1010, 1595, 1485 TFLOP/s (at 64 the softmax
+// of both row tiles is all there is).
+// On the way (a prompt of 8192): 729 us with one issuing lane that worked out its
+// descriptors, 501 with descriptors in uniform registers, 411 with two threads a
+// row, 371 with items cut evenly over the CTAs, V looked over by a warp of its
+// own and O exchanged between lanes, 352 with the next item's scores early, 344 with
+// two barriers asked at once, 337 with an issuer that does not sleep.
+// Tried and slower: P beside S with scores that need not wait for it (head_dim 64,
+// 138 to 160 us); four output warps (80 registers for the softmax, 337 to 367);
+// a quarter of the exponentials by polynomial (175 to 200 of 4096 tokens); the
+// exponents before the two warps of a row agree on the maximum (2% slower).
 //
 // Every wait is bounded; a role that gives up leaves, the others follow, and
 // the device error word is set.
