@@ -360,9 +360,8 @@ int pkv_kv4_append(const pkv_shape* shape, const pkv_rope* rope, const void* q,
  * consecutive sections, one an axis; pairs of axis x turn by the position in
  * row x of `positions`.
  *   num_axes      1 .. 4
- *   sections      channel pairs of each axis, not negative, R / 2 in all (rows
- *                 of multiples of eight pairs, of four when interleaved, are
- *                 read faster)
+ *   sections      channel pairs of each axis, not negative, R / 2 in all
+ *                 (multiples of four are read faster)
  */
 typedef struct {
   int32_t num_axes;
@@ -371,7 +370,8 @@ typedef struct {
 
 /* pkv_rope_append and pkv_kv4_append with positions [num_axes][num_tokens]:
  * pair i's c_i and s_i come from the row of its axis' position.  rot_dim must
- * not be 0.  A token is skipped when any of its positions is out of range. */
+ * not be 0.  A token is skipped when a position that turns any of its pairs is
+ * out of range. */
 int pkv_rope_append_axes(const pkv_shape* shape, const pkv_rope* rope,
                          const pkv_rope_axes* axes, const void* q, const void* k,
                          const void* v, const int32_t* positions, const float* cos_sin,

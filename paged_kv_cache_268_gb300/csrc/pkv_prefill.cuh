@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
       // The lines of all sequences and key heads, one after the other, are cut
       // into equal lengths, one a CTA; every CTA finds its own from the lengths
       // on the device.  An item that a cut goes through is done in pieces, which
-      // the reduce joins (where a->cuts is null cuts move to the items' ends).
+      // the reduce joins (where there is no workspace for that, cuts move to the items' ends).
       // Sequences are looked at 32 at a time, a lane each.
       const int per_item = TPT * LY::NQ;            // tokens
       const int least = a.cuts != nullptr ? a.min_part : 0x3fffffff;

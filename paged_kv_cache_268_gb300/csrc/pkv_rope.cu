@@ -141,10 +141,10 @@ struct TokenMeta {
   int known;   // the position has a table row
 };
 
-// AXES: positions of up to four axes; thread 0 stages the table row of each.  Pairs
-// take their row by the axis that they are of, a lane's pairs all at once where
-// they are of one.  8192 tokens as above with three axes: 38.8 us (33.7 with one: two
-// table rows more, 8 of 205 MB, and less room for head rows); 256 tokens 4.1.
+// AXES: positions of up to four axes; the first warp's lanes put a token's table
+// row together from those of its axes, sixteen bytes each.  8192 tokens as above,
+// three axes: 34.6 us (37.6 with each axis' whole row staged by thread 0), 36.2 with
+// sections that are no multiples of four pairs (four bytes a copy).
 template <bool BF, int D, bool KV4, bool AXES>
 __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int LPR = D / 8;              // lanes per row
@@ -153,27 +153,22 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(cons
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[kStages];
   __shared__ TokenMeta meta[kStages];
-  __shared__ int axis_pos[kMaxAxes - 1];
   const int all = a.Hq + 2 * a.Hkv;
   const int ua = a.rows * blockIdx.y, n = min(a.rows, all - ua);   // rows of the slice
-  const int stage_bytes = a.rows * ROW + (AXES ? a.axes : 1) * a.rot * 4;
+  const int stage_bytes = a.rows * ROW + a.rot * 4;
   const uint32_t base = smem_u32(smem);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&bars[i]), 1);
+    for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&bars[i]), AXES ? 33 : 1);
     fence_mbar_init();
   }
   __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
 
-  // Thread 0: stage token `t`, whose position, further axes' positions and slot
-  // are given.
-  auto issue = [&](int t, int pos, const int (&more)[kMaxAxes - 1], int slot, int st) {
+  // Thread 0: stage token `t`, whose position and slot are given.  (Several axes:
+  // `known` says whether all positions are, and the table row is not of these copies.)
+  auto issue = [&](int t, int pos, bool known, int slot, int st) {
     const uint32_t bar = smem_u32(&bars[st]);
-    bool known = a.rot == 0 || (pos >= 0 && pos < a.max_pos);
-    if constexpr (AXES)
-#pragma unroll
-      for (int x = 1; x < kMaxAxes; ++x) known &= x >= a.axes || (more[x - 1] >= 0 && more[x - 1] < a.max_pos);
     const bool beyond = slot >= 0 && static_cast<long long>(slot) >= static_cast<long long>(a.NB) * a.bs;
     if (blockIdx.y == 0) {
       if (!known) record_error(a.err, kDevBadPosition);
@@ -186,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(cons
       return;
     }
     const int end = meta[st].slot >= 0 ? ua + n : min(ua + n, a.Hq);   // rows to fetch: [ua, end)
-    mbar_arrive_expect_tx(bar, max(end - ua, 0) * ROW + (AXES ? a.axes : 1) * a.rot * 4);
+    mbar_arrive_expect_tx(bar, max(end - ua, 0) * ROW + (AXES ? 0 : a.rot * 4));
     const uint32_t dst = base + st * stage_bytes;
     // rows [from, to) of one tensor whose first row is row `zero` of the token
     auto rows = [&](const uint16_t* x, long long stride, int zero, int heads) {
@@ -197,42 +192,72 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(cons
     rows(a.q, a.q_stride, 0, a.Hq);
     rows(a.k, a.k_stride, a.Hq, a.Hkv);
     rows(a.v, a.v_stride, a.Hq + a.Hkv, a.Hkv);
-    if (a.rot > 0)
+    if (!AXES && a.rot > 0)
       bulk_load(dst + a.rows * ROW, a.cos_sin + static_cast<size_t>(pos) * a.rot, a.rot * 4, bar);
-    if constexpr (AXES)
+  };
+  // Several axes, the first warp: the token's table row is put together from its
+  // axes' rows, lane l bringing the cosines and sines of pairs 4 l .. 4 l + 3.
+  const int pair0 = threadIdx.x * 4;
+  const bool brings = pair0 < a.rot / 2;
+  auto axis_of = [&](int i) { return (i >= a.bound[0]) + (i >= a.bound[1]) + (i >= a.bound[2]); };
+  const int axis0 = AXES && brings ? axis_of(pair0) : 0;
+  const bool one_axis = !AXES || !brings || axis0 == axis_of(pair0 + 3);
+  auto known_at = [&](int pos) { return pos >= 0 && pos < a.max_pos; };
+  auto issue_axes = [&](int t, int pos, int slot, int st) {
+    const uint32_t bar = smem_u32(&bars[st]), dst = base + st * stage_bytes + a.rows * ROW + pair0 * 4;
+    bool known = !brings || known_at(pos);
+    int more[3] = {pos, pos, pos};                  // of the lane's further pairs
+    if (brings && !one_axis) {
 #pragma unroll
-      for (int x = 1; x < kMaxAxes; ++x)
-        if (x < a.axes)
-          bulk_load(dst + a.rows * ROW + x * a.rot * 4, a.cos_sin + static_cast<size_t>(more[x - 1]) * a.rot, a.rot * 4, bar);
+      for (int j = 1; j < 4; ++j) {
+        more[j - 1] = a.positions[static_cast<size_t>(axis_of(pair0 + j)) * a.T + t];
+        known &= known_at(more[j - 1]);
+      }
+    }
+    known = __all_sync(0xffffffffu, known);
+    if (threadIdx.x == 0) issue(t, 0, known, slot, st);
+    __syncwarp();
+    if (!known) {
+      mbar_arrive(bar);
+      return;
+    }
+    if (brings) {
+      const float* row = a.cos_sin + static_cast<size_t>(pos) * a.rot + pair0;
+      if (one_axis) {
+        copy_async16(dst, row);
+        copy_async16(dst + a.rot * 2, row + a.rot / 2);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j > 0) row = a.cos_sin + static_cast<size_t>(more[j - 1]) * a.rot + pair0 + j;
+          copy_async4(dst + j * 4, row);
+          copy_async4(dst + a.rot * 2 + j * 4, row + a.rot / 2);
+        }
+      }
+    }
+    copy_async_arrive(bar);
   };
   const int gx = gridDim.x;
-  int npos = 0, nslot = 0;                // of the next token to stage (thread 0)
+  int npos = 0, nslot = 0;                // of the next token to stage (thread 0; several axes: the first warp)
   auto look = [&](int t) {
     if (t < a.T) {
-      npos = a.rot > 0 ? a.positions[t] : 0;
+      npos = a.rot > 0 ? a.positions[static_cast<size_t>(axis0) * a.T + t] : 0;
       nslot = a.slots[t];
-      if constexpr (AXES)                 // the further axes' positions, by way of shared memory
-        for (int x = 1; x < a.axes; ++x)
-          copy_async4(smem_u32(&axis_pos[x - 1]), a.positions + static_cast<size_t>(x) * a.T + t);
     }
   };
-  auto looked = [&](int (&more)[kMaxAxes - 1]) {
-    if constexpr (AXES) {
-      copy_async_wait();
-#pragma unroll
-      for (int x = 0; x < kMaxAxes - 1; ++x) more[x] = axis_pos[x];
-    }
+  auto stage = [&](int t, int st) {       // the token looked at last; then look at the next
+    const int pos = npos, slot = nslot;
+    look(t + gx);
+    if constexpr (AXES) issue_axes(t, pos, slot, st);
+    else issue(t, pos, a.rot == 0 || known_at(pos), slot, st);
   };
-  if (threadIdx.x == 0) {
+  const bool stages = threadIdx.x < (AXES ? 32 : 1);
+  if (stages) {
     look(blockIdx.x);
     for (int i = 0; i < kStages; ++i) {
       const int t = blockIdx.x + i * gx;
       if (t >= a.T) break;
-      const int pos = npos, slot = nslot;
-      int more[kMaxAxes - 1];
-      looked(more);
-      look(t + gx);
-      issue(t, pos, more, slot, i);
+      stage(t, i);
     }
   }
 
@@ -241,11 +266,6 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(cons
   const int partner = (first ? c * 8 + a.rot / 2 : c * 8 - a.rot / 2) * 2;   // byte of the other half's chunk
   const int i0 = a.inter ? c * 4 : (first ? c * 8 : c * 8 - a.rot / 2);
   const int g = c >> 2;
-  // The axis whose position turns pair i.  Sections of multiples of eight pairs
-  // (of four, interleaved) leave each lane's pairs in one axis.
-  auto axis_of = [&](int i) { return (i >= a.bound[0]) + (i >= a.bound[1]) + (i >= a.bound[2]); };
-  const int axis0 = AXES ? axis_of(i0) : 0;
-  const bool one_axis = !AXES || axis0 == axis_of(i0 + (a.inter ? 3 : 7));
   int st = 0;
   uint32_t phase = 0;
   bool failed = false;
@@ -260,7 +280,6 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(cons
       float cs[8], sn[8];
       if (turned) {
         const float* row = reinterpret_cast<const float*>(stage + a.rows * ROW) + i0;
-        if constexpr (AXES) row += axis0 * a.rot;
         const float4 c0 = *reinterpret_cast<const float4*>(row);
         const float4 s0 = *reinterpret_cast<const float4*>(row + a.rot / 2);
         cs[0] = c0.x; cs[1] = c0.y; cs[2] = c0.z; cs[3] = c0.w;
@@ -270,18 +289,6 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(cons
           const float4 s1 = *reinterpret_cast<const float4*>(row + a.rot / 2 + 4);
           cs[4] = c1.x; cs[5] = c1.y; cs[6] = c1.z; cs[7] = c1.w;
           sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
-        }
-        if constexpr (AXES) {
-          if (!one_axis) {                    // some of the lane's pairs are of a later axis
-#pragma unroll
-            for (int j = 1; j < 8; ++j) {
-              const int x = axis_of(i0 + j);
-              if (x != axis0 && (j < 4 || !a.inter)) {
-                cs[j] = row[(x - axis0) * a.rot + j];
-                sn[j] = row[(x - axis0) * a.rot + a.rot / 2 + j];
-              }
-            }
-          }
         }
       }
       uint16_t* q_out = a.q_out + static_cast<size_t>(t) * a.Hq * D + c * 8;
@@ -343,15 +350,11 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) rope_append_kernel(cons
     }
     failed = __syncthreads_or(!ok);       // every lane is done with the stage
     if (failed) break;
-    if (threadIdx.x == 0) {
+    if (stages) {
       const int next = t + kStages * gx;
       if (next < a.T) {
-        const int pos = npos, slot = nslot;
-        int more[kMaxAxes - 1];
-        looked(more);
-        look(next + gx);
         fence_proxy_async_smem();
-        issue(next, pos, more, slot, st);
+        stage(next, st);
       }
     }
     if (++st == kStages) {
@@ -565,9 +568,7 @@ int append(const pkv_shape* s, const pkv_rope* rope, const pkv_rope_axes* axes, 
   // kAppendCtas CTAs per SM walk the tokens.  A slice has at most 24 KB of rows
   // (the CTAs' stages fit an SM's shared memory), and fewer where there are
   // not tokens enough for every CTA: down to one pass of the CTA's threads.
-  const int pass = kThreads / (D / 8), all = a.Hq + 2 * a.Hkv;
-  // (further axes' table rows take their place from the head rows)
-  const int most = (kSliceBytes - (a.axes > 1 ? (a.axes - 1) * a.rot * 4 : 0)) / (D * 2) / pass * pass;
+  const int pass = kThreads / (D / 8), all = a.Hq + 2 * a.Hkv, most = kSliceBytes / (D * 2);
   const int resident = kAppendCtas * sms;
   long long slices = (all + most - 1) / most;
   if (num_tokens * slices < resident) {
@@ -583,7 +584,7 @@ int append(const pkv_shape* s, const pkv_rope* rope, const pkv_rope_axes* axes, 
   if (walkers < 1) walkers = 1;
   const dim3 grid(static_cast<unsigned>(num_tokens < walkers ? num_tokens : walkers),
                   static_cast<unsigned>(slices));
-  const size_t smem = static_cast<size_t>(kStages) * (static_cast<size_t>(a.rows) * D * 2 + a.axes * a.rot * 4);   // axes is 0 where rot is
+  const size_t smem = static_cast<size_t>(kStages) * (static_cast<size_t>(a.rows) * D * 2 + a.rot * 4);
   cudaError_t e = raise_smem(reinterpret_cast<const void*>(kern), KV4, a.axes > 1, bf, D);
   if (e != cudaSuccess) return PKV_ERR_CUDA;
   e = launch_pdl(kern, grid, kThreads, smem, reinterpret_cast<cudaStream_t>(stream), a);

@@ -110,6 +110,17 @@ def test_a_bad_position_of_any_axis_skips_the_token(pkv, axis, bad):
     assert torch.equal(a[0], b[0])
 
 
+def test_positions_of_an_axis_without_pairs_do_not_matter(pkv):
+    T, D = 20, 128
+    q, k, v, pos, slots, NB = _case(T, 8, 2, D, 16, torch.float16, (0, 40, 24))
+    table = pkv.rope_table(4096, D)
+    a, b = ([torch.zeros((NB, 2, 16, D), dtype=torch.float16, device="cuda") for _ in range(2)] for _ in range(2))
+    want = pkv.rope_append(q, k, v, pos, table, slots, *a, sections=(0, 40, 24))
+    pos[0] = -1
+    got = pkv.rope_append(q, k, v, pos, table, slots, *b, sections=(0, 40, 24))
+    assert torch.equal(got, want) and torch.equal(a[0], b[0]) and pkv.get_device_error() == 0
+
+
 def test_refusals(pkv):
     T, D = 4, 64
     q, k, v, pos, slots, NB = _case(T, 8, 2, D, 16, torch.float16, (8, 12, 12))
