@@ -82,15 +82,18 @@ struct PrefillLayout {
   static constexpr int Q_TILE = 128 * D * 2;
   static constexpr int KV_TILE = BN * D * 2;
   static constexpr int STAGES = D == 64 ? 8 : 5;
+  // Items that the scheduler has told of and that are not through: with two, the
+  // producer had none to load while short items ended (2% of such a batch).
+  static constexpr int ITEMS_LOG2 = 2, ITEMS = 1 << ITEMS_LOG2;
   static constexpr int OFF_KV = NQ * Q_TILE;
   static constexpr int OFF_BAR = OFF_KV + STAGES * KV_TILE;
   static constexpr int KV_FULL = 0, KV_EMPTY = STAGES, Q_FULL = 2 * STAGES, Q_EMPTY = Q_FULL + 2,
                        S_FULL = Q_EMPTY + 2, P_FULL = S_FULL + 3, O_DONE = P_FULL + 6,
                        O_LAST = O_DONE + 2, O_FREE = O_LAST + 2, I_FULL = O_FREE + 2,
-                       I_EMPTY = I_FULL + 2, V_HERE = I_EMPTY + 2, V_CLEAN = V_HERE + 2,
+                       I_EMPTY = I_FULL + ITEMS, V_HERE = I_EMPTY + ITEMS, V_CLEAN = V_HERE + 2,
                        NBAR = V_CLEAN + 2;
   static constexpr int OFF_ITEM = OFF_BAR + NBAR * 8;
-  static constexpr int OFF_TMEM = OFF_ITEM + 2 * 80;
+  static constexpr int OFF_TMEM = OFF_ITEM + ITEMS * 80;
   static constexpr int OFF_XCH = OFF_TMEM + 16;     // [NQ][2][128] floats
   static constexpr int BYTES = OFF_XCH + NQ * 1024;
   // S buffer 0, 1: of row tile 0, 1; 2: buffer 1 with a single row tile (a
@@ -408,7 +411,10 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
   extern __shared__ __align__(1024) uint8_t smem[];   // swizzle atoms are 1024 bytes
   const uint32_t sb = smem_u32(smem);
   auto bar = [&](int i) { return sb + LY::OFF_BAR + 8 * i; };
-  auto item_at = [&](int i) { return reinterpret_cast<PrefillItem*>(smem + LY::OFF_ITEM + (i & 1) * 80); };
+  auto i_full = [&](int i) { return LY::I_FULL + (i & (LY::ITEMS - 1)); };
+  auto i_empty = [&](int i) { return LY::I_EMPTY + (i & (LY::ITEMS - 1)); };
+  auto i_phase = [&](int i) { return static_cast<uint32_t>(i >> LY::ITEMS_LOG2) & 1; };
+  auto item_at = [&](int i) { return reinterpret_cast<PrefillItem*>(smem + LY::OFF_ITEM + (i & (LY::ITEMS - 1)) * 80); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + LY::OFF_TMEM);
   const int tid = threadIdx.x, warp = __shfl_sync(kFullMask, tid >> 5, 0), lane = tid & 31;
   const int TPT = 128 / a.G;                       // tokens of a row tile
@@ -420,7 +426,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
     int count = 1;
     if (tid >= LY::P_FULL && tid < LY::P_FULL + 6) count = 8;
     if (tid >= LY::O_FREE && tid < LY::O_FREE + 2) count = 8;
-    if (tid >= LY::I_EMPTY && tid < LY::I_EMPTY + 2) count = SOFT + 3;
+    if (tid >= LY::I_EMPTY && tid < LY::I_EMPTY + LY::ITEMS) count = SOFT + 3;
     mbar_init(bar(tid), count);
   }
   if (sb & 1023) {                                 // (never: the array is aligned)
@@ -556,14 +562,14 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
               const bool first = cut_in(cut_at(c)) == 0;
               cut = PrefillCut{first ? 2 : 1, c, to == tiles, kvh, it.q_row, it.ntok};
             }
-            if (published >= 2 &&
-                !__all_sync(kFullMask, mbar_wait_short(bar(LY::I_EMPTY + (published & 1)), ((published >> 1) - 1) & 1))) {
+            if (published >= LY::ITEMS &&
+                !__all_sync(kFullMask, mbar_wait_short(bar(i_empty(published)), i_phase(published) ^ 1))) {
               fail = true;
               break;
             }
             if (lane == 0) {
               *item_at(published) = it;
-              mbar_arrive(bar(LY::I_FULL + (published & 1)));
+              mbar_arrive(bar(i_full(published)));
             }
             ++published;
           }
@@ -583,12 +589,12 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
       }
       if (a.cuts != nullptr && lane == 0) a.cuts[blockIdx.x] = cut;
       if (!fail) {
-        if (published >= 2 &&
-            !__all_sync(kFullMask, mbar_wait_short(bar(LY::I_EMPTY + (published & 1)), ((published >> 1) - 1) & 1)))
+        if (published >= LY::ITEMS &&
+            !__all_sync(kFullMask, mbar_wait_short(bar(i_empty(published)), i_phase(published) ^ 1)))
           fail = true;
         if (!fail && lane == 0) {
           item_at(published)->work = 0;
-          mbar_arrive(bar(LY::I_FULL + (published & 1)));
+          mbar_arrive(bar(i_full(published)));
         }
       }
       };
@@ -607,11 +613,11 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         if (!__all_sync(kFullMask, mbar_wait_short(bar(b), parity))) fail = true;
       };
       for (int slot = 0; !fail; ++slot) {
-        wait(LY::I_FULL + (slot & 1), (slot >> 1) & 1);
+        wait(i_full(slot), i_phase(slot));
         if (fail) break;
         const PrefillItem it = *item_at(slot);
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(LY::I_EMPTY + (slot & 1)));
+        if (lane == 0) mbar_arrive(bar(i_empty(slot)));
         if (!it.work) break;
         const int n = max(it.n0, it.n1);
         if (n == 0) continue;
@@ -793,7 +799,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
       uint32_t ring = 0;                            // tiles of the items before
       bool ahead = false;                           // S0 of the item's first keys is under way already
       for (int slot = 0; !fail; ++slot) {
-        if (!__all_sync(kFullMask, mbar_wait_spin(bar(LY::I_FULL + (slot & 1)), (slot >> 1) & 1))) {
+        if (!__all_sync(kFullMask, mbar_wait_spin(bar(i_full(slot)), i_phase(slot)))) {
           fail = true;
           break;
         }
@@ -801,7 +807,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         const int work = item->work, two = item->two, n0 = item->n0, n1 = item->n1, n = max(n0, n1);
         const int hidden = item->hidden;
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(LY::I_EMPTY + (slot & 1)));
+        if (lane == 0) mbar_arrive(bar(i_empty(slot)));
         if (!work) break;
         if (n == 0) continue;
         int k = landed();
@@ -847,7 +853,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
               // at their phase or the one before.)
               const uint32_t next = ring + 2 * n;
               const PrefillItem* then = item_at(slot + 1);
-              bool go = mbar_test_wait(bar(LY::I_FULL + ((slot + 1) & 1)), ((slot + 1) >> 1) & 1) && then->work &&
+              bool go = mbar_test_wait(bar(i_full(slot + 1)), i_phase(slot + 1)) && then->work &&
                         then->n0 > 0 && mbar_test_wait(bar(LY::Q_FULL), qs0 & 1) &&
                         mbar_test_wait(bar(LY::KV_FULL + next % ST), (next / ST) & 1);
               go = __all_sync(kFullMask, go);
@@ -898,7 +904,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
       int ring = 0;
       uint32_t here = 0;
       for (int slot = 0; !fail; ++slot) {
-        if (!__all_sync(kFullMask, mbar_wait_short(bar(LY::I_FULL + (slot & 1)), (slot >> 1) & 1))) {
+        if (!__all_sync(kFullMask, mbar_wait_short(bar(i_full(slot)), i_phase(slot)))) {
           fail = true;
           break;
         }
@@ -966,7 +972,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
           if (lane == 0) mbar_arrive(bar(LY::V_CLEAN + (here & 1)));
           ++here;
         }
-        if (lane == 0) mbar_arrive(bar(LY::I_EMPTY + (slot & 1)));
+        if (lane == 0) mbar_arrive(bar(i_empty(slot)));
         ring += 2 * n;
       }
     }
@@ -994,7 +1000,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
       if (!fail && !__all_sync(kFullMask, mbar_wait_short(bar(b), parity))) fail = true;
     };
     for (int slot = 0;; ++slot) {
-      wait(LY::I_FULL + (slot & 1), (slot >> 1) & 1);
+      wait(i_full(slot), i_phase(slot));
       if (named_bar_or(pair, 64, fail)) {
         fail = true;
         break;
@@ -1122,6 +1128,11 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int g = 0; g < CW / 32; ++g) tmem_ready32(o + g * 32);
+          if (q + 1 == HD / CW) {                   // the next item's products may go there
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(LY::O_FREE + w));
+          }
 #pragma unroll
           for (int e = 0; e < CW; ++e) o[e] *= inv;
         } else {
@@ -1189,11 +1200,9 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
       }
       if (piece >= 0 && valid && h == 0)
         a.part_ml[prow] = make_float2(l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m * c) - kShift, l);
-      tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (n > 0) mbar_arrive(bar(LY::O_FREE + w));
-        mbar_arrive(bar(LY::I_EMPTY + (slot & 1)));
+        mbar_arrive(bar(i_empty(slot)));
       }
       od += n;
     }
