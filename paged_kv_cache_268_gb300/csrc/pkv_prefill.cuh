@@ -923,24 +923,23 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
           const int key0 = (t0 + i) * BN, first = max(0, seen - key0), end = min(BN, L - key0);
           // rows [first, end): a product with zero is no number where the value is none
           uint32_t odd[4] = {0, 0, 0, 0};
-          for (int r0 = first; r0 < end; r0 = ((r0 >> run_log2) + 1) << run_log2) {
-            const int run = r0 >> run_log2, in = r0 & ((1 << run_log2) - 1), rows = min(end - r0, (1 << run_log2) - in);
-            const uint32_t from = tile + run * (D * 2 << run_log2) + in * 128;
+          // (four rows at a time; rows past either end are read as the last one there)
+#pragma unroll 4
+          for (int r0 = first < end ? first & ~3 : end; r0 < end; r0 += 4) {
+            const int vr = min(max(r0 + (lane >> 3), first), end - 1);
+            const uint32_t from = tile + (vr >> run_log2) * (D * 2 << run_log2) + (vr & ((1 << run_log2) - 1)) * 128 + (lane & 7) * 16;
 #pragma unroll
             for (int c = 0; c < PANELS; ++c) {
-#pragma unroll 4
-              for (int b = lane * 16; b < rows * 128; b += 512) {
-                uint32_t d[4];
-                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
-                             : "r"(from + (c << run_log2) * 128 + b));
+              uint32_t d[4];
+              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+                           : "r"(from + (c << run_log2) * 128));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  if constexpr (BF)
-                    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(odd[e]) : "r"(d[e]), "r"(0));
-                  else
-                    asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(odd[e]) : "r"(d[e]), "r"(0));
-                }
+              for (int e = 0; e < 4; ++e) {
+                if constexpr (BF)
+                  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(odd[e]) : "r"(d[e]), "r"(0));
+                else
+                  asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(odd[e]) : "r"(d[e]), "r"(0));
               }
             }
           }
@@ -1030,8 +1029,9 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         for (int q = 0; q < HN / 32; ++q) tmem_ready32(x + q * 32);
         const int col0 = (t0 + i) * BN + h * HN;
         if (col0 + HN - 1 > all_see) {
+          const int sees = lim - col0;              // (then a comparison has a constant: 2% of short prompts)
 #pragma unroll
-          for (int e = 0; e < HN; ++e) x[e] = col0 + e <= lim ? x[e] : -INFINITY;
+          for (int e = 0; e < HN; ++e) x[e] = e <= sees ? x[e] : -INFINITY;
         }
         float top[4];
 #pragma unroll
