@@ -279,17 +279,24 @@ __device__ __forceinline__ void tma_3d_if(uint32_t dst, const CUtensorMap* map, 
       : "memory");
 }
 
-// 32 bytes to global memory: in one piece where the address is `wide`, aligned
-// to them, else in two.
+// 32 bytes to global memory, which nobody here reads again: L1 is passed by (1-3%
+// of the kernel's time).  Rows of the output (to an address that is `wide`,
+// aligned to them: in one piece, else in two) are the first to leave L2.
 __device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8], bool wide) {
   if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+    asm volatile("st.global.L1::no_allocate.L2::evict_first.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
   } else {
     reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
   }
+}
+// The same for partial rows, which the reduce finds in L2.
+__device__ __forceinline__ void store32_part(float* p, const float* v) {
+  asm volatile("st.global.L1::no_allocate.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]),
+               "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
 }
 
 // Pairs of floats in one instruction.
@@ -300,6 +307,17 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       "fma.rn.f32x2 %0, x, y, z;\n\t}"
       : "=l"(d)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+      "mul.rn.f32x2 %0, x, y;\n\t}"
+      : "=l"(d)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   float2 r;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
   return r;
@@ -1103,16 +1121,13 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
       const float inv = piece >= 0 ? 1.f : (l > 0.f ? 1.f / l : 0.f);
       // CW channels at a time.  So that a warp's stores fill whole sectors of few
       // lines, NC lanes exchange their rows' 32-byte chunks first: lane l of them
-      // then has chunk l of each of their rows.
+      // then has chunk l of each of their rows, that of the row of lane l ^ e as its e-th.
       constexpr int CW = HD < 64 ? HD : 64, NC = CW / 16;
       const int sub = lane % NC;
-      size_t rows_at[NC];
-      uint32_t rows_valid = 0;
+      uint32_t rows_at[NC];                         // (fewer than 2^32 - 1 rows of 128 bytes or more fit into the memory)
 #pragma unroll
-      for (int e = 0; e < NC; ++e) {
-        rows_at[e] = __shfl_sync(kFullMask, static_cast<unsigned long long>(row), lane - sub + e);
-        rows_valid |= static_cast<uint32_t>(__shfl_sync(kFullMask, static_cast<int>(valid), lane - sub + e)) << e;
-      }
+      for (int e = 0; e < NC; ++e)
+        rows_at[e] = __shfl_xor_sync(kFullMask, valid ? static_cast<uint32_t>(row) : 0xffffffffu, e);
       if (n > 0) {
         wait(LY::O_LAST + w, outs & 1);
         ++outs;
@@ -1134,7 +1149,11 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
             if (lane == 0) mbar_arrive(bar(LY::O_FREE + w));
           }
 #pragma unroll
-          for (int e = 0; e < CW; ++e) o[e] *= inv;
+          for (int e = 0; e < CW; e += 2) {
+            const float2 y = mul2(make_float2(o[e], o[e + 1]), make_float2(inv, inv));
+            o[e] = y.x;
+            o[e + 1] = y.y;
+          }
         } else {
 #pragma unroll
           for (int e = 0; e < CW; ++e) o[e] = 0.f;
@@ -1143,33 +1162,34 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
           if (valid) {
             float* dst = a.part_o + prow * D + ch0;
 #pragma unroll
-            for (int e = 0; e < CW; e += 8) {
-              uint32_t v[8];
-#pragma unroll
-              for (int g = 0; g < 8; ++g) v[g] = __float_as_uint(o[e + g]);
-              store32(dst + e, v, true);
-            }
+            for (int e = 0; e < CW; e += 8) store32_part(dst + e, o + e);
           }
         } else {
           uint32_t pk[NC][8];
 #pragma unroll
           for (int e = 0; e < CW / 2; ++e) pk[e / 8][e % 8] = pack2<BF>(o[2 * e], o[2 * e + 1]);
 #pragma unroll
-          for (int st = 1; st < NC; st <<= 1) {
-            const bool up = lane & st;
+          for (int st = 1; st < NC; st <<= 1) {     // chunk sub ^ e to the e-th place
+            const bool up = sub & st;
 #pragma unroll
             for (int g = 0; g < NC; ++g) {
               if (g & st) continue;
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const uint32_t got = __shfl_xor_sync(kFullMask, up ? pk[g][e] : pk[g | st][e], st);
-                if (up) pk[g][e] = got; else pk[g | st][e] = got;
+                const uint32_t lo = pk[g][e], hi = pk[g | st][e];
+                pk[g][e] = up ? hi : lo;
+                pk[g | st][e] = up ? lo : hi;
               }
             }
           }
 #pragma unroll
-          for (int e = 0; e < NC; ++e)
-            if (rows_valid >> e & 1) store32(a.out + rows_at[e] * D + ch0 + sub * 16, pk[e], wide);
+          for (int g = 0; g < NC; ++g) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (g > 0) pk[g][e] = __shfl_xor_sync(kFullMask, pk[g][e], g);
+            if (rows_at[g] != 0xffffffffu)
+              store32(a.out + static_cast<size_t>(rows_at[g]) * D + ch0 + sub * 16, pk[g], wide);
+          }
         }
       }
       if (n > 0 && item->bad_values) {
