@@ -12,7 +12,7 @@
 //   softmax     eight warps a row tile: a thread has a row and half of the keys
 //   producer    a warp: Q by TMA, K and V tiles into a ring of slots
 //   issuer      a warp that issues the matrix products
-//   scheduler   a warp that finds the CTA's next item, one ahead
+//   scheduler   a warp that finds the CTA's next items, up to four of them
 //   values      a warp that looks V tiles over which hide something (below)
 //
 // S = Q K^T (both K-major in shared memory) goes to TMEM; a softmax thread
@@ -41,23 +41,29 @@
 // What bounds it.  Long rows: 128 keys of 2 x 128 rows are 2048 cycles of matrix
 // products (128 channels) and take about 2650, of which no part of the softmax
 // alone is worth more than 3% (its exponentials, its maximum or its meeting
-// left out one at a time); an item costs 6000 cycles besides (first scores, O to
+// left out one at a time); an item costs 5500 cycles besides (first scores, O to
 // memory), a call 5 us until its first loads and the reduce after it.  Few rows:
 // the cache's bytes.  Measured on one GB300, graph-timed, bfloat16, 32 heads of 128
-// on 8: a prompt of 8192 tokens 331 us, 1660 TFLOP/s, 0.85 of the library's
-// 8192^3 product; 2048 tokens after 8192 in blocks of 16 191 us, 1620; 4 x 8 tokens of
+// on 8: a prompt of 8192 tokens 328 us, 1675 TFLOP/s, 0.86 of the library's
+// 8192^3 product; 2048 tokens after 8192 in blocks of 16 189 us, 1640; 4 x 8 tokens of
 // 64/8 heads after 32760 each 88 us, 6.1 TB/s, 0.90 of a copy; without a mask,
-// 4096 tokens, head_dim 64 / 128 / 256: 1010, 1595, 1485 TFLOP/s (at 64 the softmax
+// 4096 tokens, head_dim 64 / 128 / 256: 1010, 1630, 1505 TFLOP/s (at 64 the softmax
 // of both row tiles is all there is).
 // On the way (a prompt of 8192): 729 us with one issuing lane that worked out its
 // descriptors, 501 with descriptors in uniform registers, 411 with two threads a
 // row, 371 with items cut evenly over the CTAs, V looked over by a warp of its
 // own and O exchanged between lanes, 352 with the next item's scores early, 344 with
-// two barriers asked at once, 337 with an issuer that does not sleep.
+// two barriers asked at once, 337 with an issuer that does not sleep.  32 prompts
+// of 1-2048 tokens, 32 heads of 128: 371 us, 365 with items told of further ahead,
+// 354 with masks against constants and a quicker look at the values, 348 with
+// output stores that pass L1 by.
 // Tried and slower: P beside S with scores that need not wait for it (head_dim 64,
 // 138 to 160 us); four output warps (80 registers for the softmax, 337 to 367);
 // a quarter of the exponentials by polynomial (175 to 200 of 4096 tokens); the
-// exponents before the two warps of a row agree on the maximum (2% slower).
+// exponents before the two warps of a row agree on the maximum (2% slower); an
+// item's output after the next one's first weights (none to 2% slower); the row
+// tiles' order by which is through first (one-to-one heads end a key tile apart;
+// the choice costs the issuer 2%, which is what it saves).
 //
 // Every wait is bounded; a role that gives up leaves, the others follow, and
 // the device error word is set.
