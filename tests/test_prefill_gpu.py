@@ -297,6 +297,40 @@ def test_the_same_call_gives_the_same_bits(pkv):
         assert torch.equal(one, pkv.prompt_attn(q, k, v, st, 0.1, split_tokens=128))
 
 
+# many items a CTA: one row tile and two in turn, some without keys
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_short_items(pkv, D):
+    g = torch.Generator().manual_seed(11)
+    new = torch.randint(0, 4, (1200,), generator=g).tolist()
+    ctx = torch.randint(0, 9, (1200,), generator=g).tolist()
+    _chunk(pkv, new, ctx, 16, 16, D, 16, F16)
+
+
+@pytest.mark.parametrize("hq,hkv", [(24, 24), (24, 8)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_ragged_prompts(pkv, hq, hkv, D):
+    g = torch.Generator().manual_seed(12)
+    nq = torch.randint(0, 420, (48,), generator=g).tolist()
+    nk = [max(0, n + d) for n, d in zip(nq, torch.randint(-60, 150, (48,), generator=g).tolist())]
+    _prompt(pkv, nq, nk, hq, hkv, D, BF16, True, seed=D)
+
+
+# rows that begin at 16 bytes, not at 32
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("split", [0, 128])
+def test_output_at_16_bytes(pkv, D, split):
+    g = torch.Generator().manual_seed(13)
+    q, k, v = _rows(333, 6, 2, D, F16, g)
+    st = _i32([0, 33, 333])
+    one = pkv.prompt_attn(q, k, v, st, 0.1, split_tokens=split)
+    room = torch.full((q.numel() + 32,), 7.0, dtype=F16, device="cuda")
+    out = room[8:8 + q.numel()].view_as(q)
+    assert out.data_ptr() % 32 == 16
+    pkv.prompt_attn(q, k, v, st, 0.1, out, split_tokens=split)
+    assert torch.equal(one, out)
+    assert bool((room[:8] == 7).all()) and bool((room[8 + q.numel():] == 7).all())
+
+
 # ---------------------------------------------------------------- streams, graphs, workspaces
 def test_on_another_stream(pkv):
     g = torch.Generator().manual_seed(10)
