@@ -45,7 +45,7 @@
 // memory), a call 5 us until its first loads and the reduce after it.  Few rows:
 // the cache's bytes.  Measured on one GB300, graph-timed, bfloat16, 32 heads of 128
 // on 8: a prompt of 8192 tokens 328 us, 1675 TFLOP/s, 0.86 of the library's
-// 8192^3 product; 2048 tokens after 8192 in blocks of 16 189 us, 1640; 4 x 8 tokens of
+// 8192^3 product; 2048 tokens after 8192 in blocks of 16 190 us, 1630; 4 x 8 tokens of
 // 64/8 heads after 32760 each 88 us, 6.1 TB/s, 0.90 of a copy; without a mask,
 // 4096 tokens, head_dim 64 / 128 / 256: 1010, 1630, 1505 TFLOP/s (at 64 the softmax
 // of both row tiles is all there is).

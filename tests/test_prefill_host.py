@@ -188,7 +188,7 @@ def test_sizes_past_32_bits_are_refused():
 # The scheduler's arithmetic once more, in Python integers: items of a key head
 # lie on a line, the lines one after the other are cut into equal lengths, one a
 # CTA, and a cut is moved to a key tile that leaves no piece too short.
-KEY, ITEM, TOKEN, KEY1, ITEM1 = 3, 3 * 320, 3, 2, 2 * 320
+KEY, ITEM, TOKEN, KEY1, ITEM1 = 3, 3 * 320, 3, 2, 3 * 320
 
 
 def _keys(n, L, per, t, causal):
