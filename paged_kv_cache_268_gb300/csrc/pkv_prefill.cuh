@@ -1066,7 +1066,9 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
           for (int q = 0; q < 4; ++q) top[q] = fmaxf(top[q], fmaxf(x[e + q], x[e + 4 + q]));
         }
         const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        raised = named_bar_or(pair, 64, i == 0 || (mt - m) * c > 8.f);
+        // (rows of no token have no say: they hold other sequences' queries or what
+        // was in shared memory, and the item's rows would be rounded differently)
+        raised = named_bar_or(pair, 64, i == 0 || (valid && (mt - m) * c > 8.f));
         if (raised) {
           // raise the reference to the whole row's maximum
           *own = mt;
