@@ -14,12 +14,12 @@ constexpr int kReduceThreads = 256;
 constexpr int kReduceRows = 2;                        // of a warp, at once (one or four: 1-2% of a call more)
 constexpr int kReduceCtaRows = kReduceThreads / 32 * kReduceRows;
 
-// Joins the pieces of the items that were cut: out = sum_p 2^(e_p - E) o_p /
-// sum_p 2^(e_p - E) l_p with E the largest exponent, in the keys' order.  CTA
+// Joins the pieces of the items that were cut: out = sum_p 2^((m_p - M) c) o_p /
+// sum_p 2^((m_p - M) c) l_p with M the largest reference, in the keys' order.  CTA
 // (c, y) looks after the item whose second piece attention's CTA c had, if it
 // had one, rows 16 y and up.  Bound by the latency of its few loads, so each step
 // asks for all that it needs at once: the CTAs behind c, a lane each; the pieces'
-// exponents and sums, a lane each, of two rows; these rows' outputs.
+// references and sums, a lane each, of two rows; these rows' outputs.
 template <bool BF, int D>
 __global__ void __launch_bounds__(kReduceThreads) prefill_reduce_kernel(const __grid_constant__ PrefillArgs a) {
   constexpr int C = D / 32, R = kReduceRows;
@@ -56,8 +56,8 @@ __global__ void __launch_bounds__(kReduceThreads) prefill_reduce_kernel(const __
       float up = ml[r].y != 0.f ? fmaxf(top[r], ml[r].x) : top[r];
 #pragma unroll
       for (int i = 16; i > 0; i >>= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, i));
-      const float keep = top[r] == -INFINITY ? 0.f : fast_exp2(top[r] - up);
-      w[r] = ml[r].y != 0.f ? fast_exp2(ml[r].x - up) : 0.f;
+      const float keep = top[r] == -INFINITY ? 0.f : fast_exp2((top[r] - up) * a.scale_log2);
+      w[r] = ml[r].y != 0.f ? fast_exp2((ml[r].x - up) * a.scale_log2) : 0.f;
       float sum = w[r] * ml[r].y;
 #pragma unroll
       for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);

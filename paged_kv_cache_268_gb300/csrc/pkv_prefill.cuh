@@ -1036,7 +1036,12 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
       const bool valid = has_token && j < item->ntok && (w == 0 || two);
       const int lim = a.causal ? off + j : L - 1;   // last key that the row sees
       const int all_see = __reduce_min_sync(kFullMask, valid ? lim : 0x7fffffff);   // last key that all of the warp's rows see
-      float m = -INFINITY;
+      // The row's reference.  m c is rounded, by up to 2^-24 of it, and all of the
+      // row's weights are off by one factor.  So that this stays small, far from
+      // zero the reference is held apart, m is as in a row that has seen nothing,
+      // which raises the reference at every key tile, and the scores take it off
+      // before they are scaled.
+      float m = -INFINITY, held = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
       bool raised = true;                           // by the last key tile (or the item before used the exchange)
       for (int i = 0; i < n; ++i) {
@@ -1073,7 +1078,8 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
           // raise the reference to the whole row's maximum
           *own = mt;
           named_bar_sync(pair, 64);
-          const float up = fmaxf(m, fmaxf(mt, *others)), keep = m == -INFINITY ? 0.f : fast_exp2((m - up) * c);
+          const float was = m == -INFINITY ? held : m, up = fmaxf(was, fmaxf(mt, *others));
+          const float keep = was == -INFINITY ? 0.f : fast_exp2((was - up) * c);
           if (i > 0) {
             // O holds the products up to the last tile's.  (That barrier is at
             // this phase or the next: the one before had ended when S was
@@ -1091,7 +1097,14 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
           }
           l2.x *= keep;
           l2.y *= keep;
-          m = up;
+          const bool far = valid && up != -INFINITY && fabsf(up * c) > kPrefillFar;
+          if (__any_sync(kFullMask, far)) {
+            const float less = far ? up : 0.f;
+#pragma unroll
+            for (int e = 0; e < HN; ++e) x[e] -= less;
+          }
+          m = far ? -INFINITY : up;
+          held = far ? up : -INFINITY;
         }
         const float mc = (m == -INFINITY ? 0.f : m * c) - kShift;
         const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
@@ -1227,7 +1240,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         }
       }
       if (piece >= 0 && valid && h == 0)
-        a.part_ml[prow] = make_float2(l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m * c) - kShift, l);
+        a.part_ml[prow] = make_float2(l == 0.f ? -INFINITY : (m == -INFINITY ? held : m), l);
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar(i_empty(slot)));

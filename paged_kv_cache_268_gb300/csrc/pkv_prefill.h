@@ -18,6 +18,9 @@ constexpr int kPrefillMinPart = 512;
 // one row tile, as its keys cost: mixed steps 1.2% slower, prompts the same.)
 constexpr int kPrefillKeyCost = 3, kPrefillItemCost = 3 * 320, kPrefillTokenCost = 3;
 constexpr int kPrefillKeyCost1 = 2, kPrefillItemCost1 = 3 * 320;   // with one row tile of two
+// A reference score's exponent beyond which scores are taken relative to it before
+// they are scaled (2^-16 of a weight is lost below).
+constexpr float kPrefillFar = 256.f;
 // Below so many items a key head, and lines of less than 2^31 in all, the
 // scheduler counts in 32 bits.
 constexpr int kPrefillSmallItems = 30000;
@@ -39,7 +42,7 @@ struct PrefillArgs {
   const uint16_t* v;             // packed: [S, Hkv, D]; paged: [NB, Hkv, bs, D]
   uint16_t* out;                 // [T, Hq, D]
   PrefillCut* cuts;              // [CTAs], or null: no item is cut
-  float2* part_ml;               // (exponent, sum) of a partial row, `rows` for a piece:
+  float2* part_ml;               // (reference score, sum) of a partial row, `rows` for a piece:
   float* part_o;                 //   piece 2c is CTA c's with keys before it, 2c + 1 its
                                  //   with only keys behind; the un-normalised output [D]
   int* err;
