@@ -29,8 +29,10 @@
 // with the rest of P, which the decode kernels can afford as bytes bound them,
 // would cost half of the rate here).  P in
 // binary16 is scaled by 2^7 so that weights of down to 2^-21 of the largest
-// keep all their bits; the largest, 2^15, is still in range.  The sums are of
-// P in FP32, before its rounding.
+// keep all their bits; the largest, 2^15, is still in range.  In bfloat16 it is
+// scaled by 2^-8: the largest is 1, and O in FP32 holds what a plain softmax's
+// sums hold of values near the type's end.  The sums are of P in FP32, before
+// its rounding.
 //
 // Hidden keys: P is zero there, but 0 times an infinity or NaN is not.  In key
 // tiles that hide something from some row, values past the sequence's end are
@@ -1006,7 +1008,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
     // So none of them leaves an item early: after a failed wait a warp skips its
     // later waits and runs on with whatever is there, and before the next item
     // the two leave together.
-    constexpr float kShift = BF ? 0.f : 7.f;        // P is 2^kShift times the weight
+    constexpr float kShift = BF ? -8.f : 7.f;       // P is 2^kShift times the weight relative to m
     constexpr int HN = BN / 2, HD = D / 2;
     const int w = warp >> 3, h = (warp >> 2) & 1, pair = 1 + w * 4 + (warp & 3);
     const int r = (warp & 3) * 32 + lane;           // row of the tile
