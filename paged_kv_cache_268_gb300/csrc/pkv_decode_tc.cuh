@@ -27,8 +27,9 @@
 //     raised only when a group exceeds them by more than 2^8, detected with
 //     one barrier reduction per group; then O and the partial sums are
 //     rescaled in TMEM.
-//     P = 2^(s - m) (so P < 256) goes to shared memory as a K-major operand
-//     (bfloat16 as a hi + lo pair, binary16 as is); with N = 32 it alternates
+//     P = 2^(s - m) (so P < 256; in bfloat16, whose values may be near FP32's end,
+//     2^-8 of it) goes to shared memory as a K-major operand (bfloat16 as a hi +
+//     lo pair, binary16 as is); with N = 32 it alternates
 //     between two buffers, so the softmax of group g + 1 does not wait for
 //     the PV of group g.
 // At the end a softmax thread holds output dimension d = t of its 16 heads.
@@ -425,7 +426,8 @@ __global__ void __launch_bounds__(TcLayout<N>::THREADS, N > 16 ? 1 : 2)
             sb + LY::OFF_P + pb * 2 * LY::P_BYTES + chunk * (N * 128) + (t & 7) * 2;
 #pragma unroll
         for (int n = 0; n < HPT; ++n) {
-          const float p = fast_exp2(x[n] - m[n]);
+          float p = fast_exp2(x[n] - m[n]);
+          if constexpr (BF) p *= 0x1p-8f;       // at most 1: O and the sum stay in FP32's range
           lth[n] += p;
           const int h = h0 + n;
           const uint32_t addr = pbase + h * 128 + (((t >> 3) ^ (h & 7)) << 4);
