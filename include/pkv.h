@@ -63,7 +63,9 @@ enum {
 enum {
   PKV_DEV_OK = 0,
   PKV_DEV_BAD_BLOCK_ID = 1,  /* a block table entry outside [0, num_blocks) */
-  PKV_DEV_BAD_CONTEXT = 2,   /* a context length outside [1, max_context_len] */
+  PKV_DEV_BAD_CONTEXT = 2,   /* a context length above max_context_len or below 1 (below 0
+                                where a call allows empty sequences), or above what a call
+                                takes */
   PKV_DEV_BAD_SLOT = 3,      /* a slot >= num_blocks * block_size */
   PKV_DEV_TIMEOUT = 4,       /* a pipeline wait gave up (should never happen) */
   PKV_DEV_BAD_POSITION = 5,  /* a position outside [0, max_position) */
@@ -444,17 +446,17 @@ int pkv_kv4_workspace_bytes(const pkv_shape* shape, size_t* bytes);
  *     out[row][h][:] = sum_{t <= p} softmax_t(scale * q[row][h] . k_t) * v_t
  * A row that sees no token (p < 0) is set to zero.
  *
- *   shape         as for pkv_paged_attn_decode; num_seqs is B, kernel must be
- *                 0; split_tokens > 0 sets the keys that a CTA takes of a
- *                 sequence at least where it takes a part of them (rounded up
- *                 to 128 tokens, 64 at head_dim 256; 2^20 at most),
+ *   shape         as for pkv_paged_attn_decode; num_seqs is B (2^24 at most),
+ *                 kernel must be 0; split_tokens > 0 sets the keys that a CTA
+ *                 takes of a sequence at least where it takes a part of them
+ *                 (rounded up to 128 tokens, 64 at head_dim 256; 2^20 at most),
  *                 0 means 512
  *   q             [T, Hq, D], 16-byte aligned, q_stride elements from one
  *                 token's row to the next: a multiple of 8, at least Hq * D; 0
  *                 means dense
  *   query_starts  [B + 1] int32, 0 <= s_0 <= s_1 <= ... <= s_B <= T.  Rows that
  *                 no sequence has are left as they were in out.
- *   context_lens  [B] int32, each in [0, max_context_len]
+ *   context_lens  [B] int32, each in [0, max_context_len], 2^24 at most
  *   out           [T, Hq, D] dense, 16-byte aligned, not overlapping q
  *   workspace     as for pkv_paged_attn_decode, pkv_chunk_workspace_bytes long
  * A sequence whose length (PKV_DEV_BAD_CONTEXT) or rows (PKV_DEV_BAD_STARTS)
@@ -477,7 +479,7 @@ int pkv_chunk_workspace_bytes(const pkv_shape* shape, int32_t num_tokens, size_t
 
 /*
  * Attention over prompts packed one after the other.
- *   num_seqs      B
+ *   num_seqs      B, 2^24 at most
  *   num_tokens    T, query rows of all sequences; num_keys: S, key rows
  *   causal        not 0: a query sees the keys up to its own position, the
  *                 last query standing at the last key; 0: all keys
@@ -510,13 +512,14 @@ typedef struct {
  *   q, k, v       [T, Hq, D], [S, Hkv, D], [S, Hkv, D], 16-byte aligned, with
  *                 the token strides of `prompt`
  *   query_starts, key_starts  [B + 1] int32, from 0 up, not falling, at most T
- *                 and S; the same array where keys and queries are the same
- *                 tokens
+ *                 and S, 2^24 keys a sequence at most; the same array where keys
+ *                 and queries are the same tokens
  *   out           [T, Hq, D] dense, 16-byte aligned, not overlapping q, k, v
  *   workspace     pkv_prompt_workspace_bytes long; NULL takes the workspace
  *                 set with pkv_set_workspace
- * A sequence whose starts pass T or S, or whose key_starts fall, is skipped;
- * where query_starts fall, nothing is done (PKV_DEV_BAD_STARTS).
+ * A sequence whose starts pass T or S, whose key_starts fall or that has more
+ * than 2^24 keys is skipped; where query_starts fall, nothing is done
+ * (PKV_DEV_BAD_STARTS).
  */
 int pkv_prompt_attn(const pkv_prompt* prompt, const void* q, const void* k, const void* v,
                     const int32_t* query_starts, const int32_t* key_starts, float scale,

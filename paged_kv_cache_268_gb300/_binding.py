@@ -947,7 +947,7 @@ def paged_attn_chunk(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     rows at any stride that is a multiple of 8 elements; sequence i has rows
     query_starts[i] .. query_starts[i + 1] (int32 [B + 1]).  caches [NB, Hkv,
     bs, D]; block_tables [B, MB] int32; context_lens [B] int32 count the new
-    tokens.  Row j of a sequence's n sees the tokens up to position
+    tokens, 2^24 in all at most.  Row j of a sequence's n sees the tokens up to position
     context_len - n + j.  Returns out [T, Hq, D] (allocated if not given; rows
     of no sequence are not written).  split_tokens: the keys of the smallest part
     of a sequence that a CTA takes, 0 = library's choice.  workspace as for
@@ -1026,7 +1026,8 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, query_starts:
     q [T, Hq, D]; k, v [S, Hkv, D]: heads dense, token rows at any stride that
     is a multiple of 8 elements (slices of a fused projection).  Sequence i has
     the query rows query_starts[i] .. query_starts[i + 1] and the key rows
-    key_starts[i] .. key_starts[i + 1] (int32 [B + 1]; None: query_starts).
+    key_starts[i] .. key_starts[i + 1], 2^24 at most (int32 [B + 1]; None:
+    query_starts).
     causal: a query sees the keys up to its position, the last query standing
     at the last key (more keys than queries: a prefix).  A row that sees no key
     is zero.  Returns out [T, Hq, D] (allocated if not given; rows of no

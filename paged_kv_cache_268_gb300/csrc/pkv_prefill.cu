@@ -117,8 +117,8 @@ struct CallSizes {
   int small;                     // PrefillArgs
 };
 
-// Keys that a CTA is asked to take of a sequence at most: its warps wait for one
-// another for half a second, which longer pieces could take.
+// The largest smallest part that split_tokens may ask for.  (A CTA's share may be
+// more; what bounds an item's time is a sequence's length, kPrefillMostKeys.)
 constexpr int kMostPart = 1 << 20;
 
 CallSizes call_sizes(int B, int T, int Hq, int Hkv, int D, int max_keys, int split_tokens, int sms) {
@@ -191,6 +191,9 @@ int check_stride(int64_t stride, int64_t row) {
 
 // Rows and keys are counted in 32 bits, with room for the tiles' ends.
 constexpr int kMostRows = 1 << 30;
+// Every CTA looks at all sequences before its first load: 32 of them in about half
+// a microsecond, a quarter of a second for so many.
+constexpr int kMostSeqs = 1 << 24;
 
 int check_prompt(const pkv_prompt* p) {
   if (!p) return PKV_ERR_NULL;
@@ -199,7 +202,8 @@ int check_prompt(const pkv_prompt* p) {
     return PKV_ERR_INVALID;
   if (p->dtype != PKV_F16 && p->dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
   if (p->head_dim != 64 && p->head_dim != 128 && p->head_dim != 256) return PKV_ERR_UNSUPPORTED;
-  if (p->num_q_heads / p->num_kv_heads > 32 || p->num_tokens > kMostRows || p->num_keys > kMostRows)
+  if (p->num_q_heads / p->num_kv_heads > 32 || p->num_tokens > kMostRows || p->num_keys > kMostRows ||
+      p->num_seqs > kMostSeqs)
     return PKV_ERR_UNSUPPORTED;
   const int64_t kd = static_cast<int64_t>(p->num_kv_heads) * p->head_dim;
   int rc = check_stride(p->q_stride, static_cast<int64_t>(p->num_q_heads) * p->head_dim);
@@ -211,7 +215,9 @@ int check_chunk(const pkv_shape* s, int64_t q_stride, int num_tokens) {
   const int rc = check_decode_shape(s);
   if (rc != PKV_OK) return rc;
   if (num_tokens < 0) return PKV_ERR_INVALID;
-  if (s->kernel != 0 || num_tokens > kMostRows || s->max_context_len > kMostRows) return PKV_ERR_UNSUPPORTED;
+  if (s->kernel != 0 || num_tokens > kMostRows || s->max_context_len > kMostRows ||
+      s->num_seqs > kMostSeqs)
+    return PKV_ERR_UNSUPPORTED;
   return check_stride(q_stride, static_cast<int64_t>(s->num_q_heads) * s->head_dim);
 }
 

@@ -167,7 +167,10 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v) {
 }
 
 // mbar_wait in few instructions: a try sleeps for up to a microsecond, and after
-// half a million of them the wait gives up.
+// four million of them the wait gives up.  Some waits are as long as an item (of
+// the warps that are told of items ahead, that look values over or that have the
+// second row tile): one of the longest sequence, 2^24 keys, takes 0.1 to 0.4
+// seconds (1500 to 2700 cycles for 128 keys, or their bytes at an SM's share).
 __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -177,7 +180,7 @@ __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity) {
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "@p bra DONE;\n\t"
       "add.u32 n, n, 1;\n\t"
-      "setp.lt.u32 q, n, 500000;\n\t"
+      "setp.lt.u32 q, n, 4000000;\n\t"
       "@q bra TRY;\n\t"
       "DONE:\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
@@ -188,7 +191,7 @@ __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity) {
 }
 
 // A wait of the warp that the others wait for: asks without a pause (an answer
-// takes a third of the time that a try's does), twenty million times at most.
+// takes a third of the time that a try's does), 160 million times at most.
 __device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -198,7 +201,7 @@ __device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity) {
       "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "@p bra DONE;\n\t"
       "add.u32 n, n, 1;\n\t"
-      "setp.lt.u32 q, n, 20000000;\n\t"
+      "setp.lt.u32 q, n, 160000000;\n\t"
       "@q bra TRY;\n\t"
       "DONE:\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
@@ -356,7 +359,7 @@ __device__ __forceinline__ PrefillSeq prefill_seq(const PrefillArgs& a, int b) {
   const bool packed = a.key_starts != nullptr;
   const int32_t* keys = packed ? a.key_starts : a.context_lens;
   const int k0 = packed ? keys[i] : 0, k1 = keys[packed ? i + 1 : i];
-  const bool rows = q0 >= 0 && q1 >= q0 && q1 <= a.T, cols = k0 >= 0 && k1 >= k0 && k1 <= a.max_keys;
+  const bool rows = q0 >= 0 && q1 >= q0 && q1 <= a.T, cols = k0 >= 0 && k1 >= k0 && k1 <= a.max_keys && k1 - k0 <= kPrefillMostKeys;
   const bool fine = rows && cols && b < a.B;
   PrefillSeq s;
   s.q0 = q0;

@@ -10,6 +10,9 @@ namespace pkv {
 constexpr int prefill_row_tiles(int D) { return D == 256 ? 1 : 2; }   // of 128 rows, an item
 constexpr int prefill_key_tile(int D) { return D == 256 ? 64 : 128; }
 
+// Keys of a sequence at most (checked on the device): the kernel's waits, some of
+// which are as long as an item, give up after a few seconds.
+constexpr int kPrefillMostKeys = 1 << 24;
 // Keys of the smallest part of an item's keys that a CTA is given.
 constexpr int kPrefillMinPart = 512;
 // What an item costs a CTA: so much a key, and so much besides (a third of what
