@@ -447,10 +447,11 @@ int pkv_kv4_workspace_bytes(const pkv_shape* shape, size_t* bytes);
  * A row that sees no token (p < 0) is set to zero.
  *
  *   shape         as for pkv_paged_attn_decode; num_seqs is B (2^24 at most),
- *                 kernel must be 0; split_tokens > 0 sets the keys that a CTA
- *                 takes of a sequence at least where it takes a part of them
- *                 (rounded up to 128 tokens, 64 at head_dim 256; 2^20 at most),
- *                 0 means 512
+ *                 kernel must be 0; split_tokens > 0 sets the keys that the
+ *                 first and the last of the CTAs that share a sequence take at
+ *                 least (rounded up to 128 tokens, 64 at head_dim 256; 2^20 at
+ *                 most; the CTAs between take their even share of all work), 0
+ *                 means 512
  *   q             [T, Hq, D], 16-byte aligned, q_stride elements from one
  *                 token's row to the next: a multiple of 8, at least Hq * D; 0
  *                 means dense

@@ -949,8 +949,8 @@ def paged_attn_chunk(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     bs, D]; block_tables [B, MB] int32; context_lens [B] int32 count the new
     tokens, 2^24 in all at most.  Row j of a sequence's n sees the tokens up to position
     context_len - n + j.  Returns out [T, Hq, D] (allocated if not given; rows
-    of no sequence are not written).  split_tokens: the keys of the smallest part
-    of a sequence that a CTA takes, 0 = library's choice.  workspace as for
+    of no sequence are not written).  split_tokens: the keys that the first and the
+    last of the CTAs that share a sequence take at least, 0 = library's choice.  workspace as for
     paged_attn_decode (chunk_workspace_bytes).
     """
     q_stride = -1

@@ -110,7 +110,7 @@ cudaError_t launch_reduce(const PrefillArgs& a, int D, unsigned ctas, cudaStream
 
 // Sizes of a call: the grid, and the workspace where items may be cut.
 struct CallSizes {
-  int min_part;                  // key tiles of a piece at least
+  int min_part;                  // key tiles of an item's first and last pieces at least
   int rows;                      // of an item at most
   size_t cut_bytes, bytes;
   unsigned grid;

@@ -71,9 +71,8 @@
 // the device error word is set.
 #pragma once
 
-#include <type_traits>
-
 #include "pkv_prefill.h"
+#include "pkv_prefill_line.h"
 #include "pkv_ptx.cuh"
 
 namespace pkv {
@@ -371,65 +370,6 @@ __device__ __forceinline__ PrefillSeq prefill_seq(const PrefillArgs& a, int b) {
   return s;
 }
 
-// The work of one key head of a sequence, as a line: its items, of `per` tokens
-// each (two row tiles of `half`, or one), one after the other, as long as they
-// take.  I: the integers of lengths.
-template <typename I>
-struct PrefillLine {
-  int n, L, per, half, tiles, causal, item, item1;
-  __device__ __forceinline__ PrefillLine(int n_, int L_, int per_, int half_, int causal_)
-      : n(n_), L(L_), per(per_), half(half_), tiles((n_ + per_ - 1) / per_), causal(causal_),
-        item(kPrefillItemCost + (causal_ ? per_ * kPrefillTokenCost : 0)),
-        item1(kPrefillItemCost1 + (causal_ ? half_ * kPrefillTokenCost : 0)) {}
-  // (products that wrap in 32 bits where their sum does not)
-  static __device__ __forceinline__ I mul(I a, I b) {
-    using U = std::make_unsigned_t<I>;
-    return static_cast<I>(static_cast<U>(a) * static_cast<U>(b));
-  }
-  // keys that item t sees
-  __device__ __forceinline__ int keys(int t) const {
-    if (!causal) return L;
-    const long long last = static_cast<long long>(t + 1) * per;
-    return max(0, L - n + static_cast<int>(min(last, static_cast<long long>(n))));
-  }
-  __device__ __forceinline__ bool one(int t) const {          // one row tile of two
-    return half < per && n - static_cast<long long>(t) * per <= half;
-  }
-  __device__ __forceinline__ I cost(int t) const {
-    const I k = keys(t);
-    return one(t) ? k * kPrefillKeyCost1 + item1 : k * kPrefillKeyCost + item;
-  }
-  // where item t begins (all before the last are whole)
-  __device__ __forceinline__ I begin(int t) const {
-    I sum;                                          // of the keys before
-    if (!causal) {
-      sum = mul(t, L);
-    } else {
-      const int d = L - n, blind = d < 0 ? -d / per : 0;      // items that see none
-      const I i = t, b = blind;
-      sum = t <= blind ? 0 : static_cast<I>(static_cast<std::make_unsigned_t<I>>(mul(i - b, d)) + mul(per, (i * (i + 1) - b * (b + 1)) / 2));
-    }
-    return t * static_cast<I>(item) + sum * kPrefillKeyCost;
-  }
-  __device__ __forceinline__ I length() const { return tiles > 0 ? begin(tiles - 1) + cost(tiles - 1) : 0; }
-};
-
-// Key tile, of BN keys, of an item at which the line is cut `x` into it: what
-// comes before costs x, the item's own cost included (which the part behind pays
-// once more, as that of every CTA that starts amid an item).  No part is shorter
-// than `least` tiles.
-template <int BN, typename I>
-__device__ __forceinline__ int prefill_cut(I x, bool one, int item, int tiles, int least) {
-  const int key = BN * (one ? kPrefillKeyCost1 : kPrefillKeyCost);
-  const I most = static_cast<I>(tiles) * key;
-  const uint32_t keys = static_cast<uint32_t>(min(max(x - item + key / 2, static_cast<I>(0)), most));   // below 2^32: 3 a key, 2^30 keys
-  const int p = static_cast<int>(one ? keys / (BN * kPrefillKeyCost1) : keys / (BN * kPrefillKeyCost));
-  if (tiles < 2 * least) return 2 * p <= tiles ? 0 : tiles;
-  if (p < least) return 2 * p <= least ? 0 : least;
-  if (tiles - p < least) return 2 * (tiles - p) <= least ? tiles : tiles - least;
-  return p;
-}
-
 template <bool BF, int D>
 __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
     prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ CUtensorMap tmQ,
@@ -522,8 +462,8 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         for (int i = 16; i > 0; i >>= 1) more += __shfl_xor_sync(kFullMask, more, i);
         total += more;
       }
-      const I share = total / static_cast<int>(gridDim.x), extra = total - share * static_cast<int>(gridDim.x);
-      auto cut_at = [&](int c) { return share * c + min(static_cast<I>(c), extra); };
+      const PrefillShares<I> shares(total, static_cast<int>(gridDim.x));
+      auto cut_at = [&](int c) { return shares.begin(c); };
       const I x0 = cut_at(blockIdx.x), x1 = cut_at(blockIdx.x + 1);
 
       // sequences [chunk, chunk + 32) are looked at; their line begins at `before`
@@ -561,8 +501,8 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
           const I cost = line.cost(tile);
           const int keys = line.keys(tile), tiles = (keys + BN - 1) / BN;
           const bool one = line.one(tile);
-          auto cut_in = [&](I x) {                  // (the item's end belongs to it)
-            return x - at >= cost ? tiles : prefill_cut<BN>(x - at, one, one ? line.item1 : line.item, tiles, least);
+          auto cut_in = [&](I x) {
+            return prefill_cut<BN>(x - at, cost, one, one ? line.item1 : line.item, tiles, least);
           };
           const int from = cut_in(x0), to = cut_in(x1);
           if (from < to || (tiles == 0 && at >= x0)) {

@@ -13,7 +13,7 @@ constexpr int prefill_key_tile(int D) { return D == 256 ? 64 : 128; }
 // Keys of a sequence at most (checked on the device): the kernel's waits, some of
 // which are as long as an item, give up after a few seconds.
 constexpr int kPrefillMostKeys = 1 << 24;
-// Keys of the smallest part of an item's keys that a CTA is given.
+// Keys of the smallest part of an item's keys that is left at one of its ends.
 constexpr int kPrefillMinPart = 512;
 // What an item costs a CTA: so much a key, and so much besides (a third of what
 // a key of two row tiles takes is the unit), where it is causal more for its
@@ -55,7 +55,7 @@ struct PrefillArgs {
   int MB, NB, bs_log2;
   int causal, negative;          // negative: the scale is
   int rows;                      // of an item at most
-  int min_part;                  // key tiles of a piece at least
+  int min_part;                  // key tiles of an item's first and last pieces at least
   int small;                     // the scheduler may count in 32 bits
   float scale_log2;              // |softmax scale| * log2(e)
 };
