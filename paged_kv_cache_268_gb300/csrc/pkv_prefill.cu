@@ -136,7 +136,8 @@ CallSizes call_sizes(int B, int T, int Hq, int Hkv, int D, int max_keys, int spl
   c.grid = static_cast<unsigned>(pieces < sms ? pieces : sms);
   const double longest = static_cast<double>(max_keys) * kPrefillKeyCost + kPrefillItemCost +
                          static_cast<double>(per_item) * kPrefillTokenCost;
-  c.small = T / per_item < kPrefillSmallItems && static_cast<double>(items) * longest < 2147483648.0;
+  c.small = T / per_item < kPrefillSmallItems && max_keys <= kPrefillMostKeys &&
+            static_cast<double>(items) * longest < 2147483648.0;
   if (cuts && c.grid > 1) {
     c.cut_bytes = (c.grid * sizeof(PrefillCut) + 31) / 32 * 32;
     c.bytes = 16 + c.cut_bytes + 2ull * c.grid * c.rows * (D * 4 + 8);   // 16: to a 32-byte boundary

@@ -346,11 +346,13 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 
 // Queries and keys of sequence b: rows [q0, q0 + n) attend over L keys, whose
 // first is key row k0 (packed).  n = 0 where the arrays hold no valid range;
-// `code` then says what is wrong.
+// `code` then says what is wrong.  I: the scheduler's integers (with 32 bits no
+// sequence can be too long).
 struct PrefillSeq {
   int q0, n, k0, L, code;
   bool falls;                    // its rows end before they begin: rows may be several sequences'
 };
+template <typename I>
 __device__ __forceinline__ PrefillSeq prefill_seq(const PrefillArgs& a, int b) {
   // (all loads at once)
   const int i = min(b, a.B - 1);
@@ -358,7 +360,8 @@ __device__ __forceinline__ PrefillSeq prefill_seq(const PrefillArgs& a, int b) {
   const bool packed = a.key_starts != nullptr;
   const int32_t* keys = packed ? a.key_starts : a.context_lens;
   const int k0 = packed ? keys[i] : 0, k1 = keys[packed ? i + 1 : i];
-  const bool rows = q0 >= 0 && q1 >= q0 && q1 <= a.T, cols = k0 >= 0 && k1 >= k0 && k1 <= a.max_keys && k1 - k0 <= kPrefillMostKeys;
+  const bool rows = q0 >= 0 && q1 >= q0 && q1 <= a.T, cols = k0 >= 0 && k1 >= k0 && k1 <= a.max_keys &&
+                    (sizeof(I) == 4 || k1 - k0 <= kPrefillMostKeys);
   const bool fine = rows && cols && b < a.B;
   PrefillSeq s;
   s.q0 = q0;
@@ -437,7 +440,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         return PrefillLine<I>(q.n, q.L, per_item, TPT, a.causal).length() * a.Hkv;
       };
       auto look = [&](int b) {
-        s = prefill_seq(a, b + lane);
+        s = prefill_seq<I>(a, b + lane);
         upto = mine = length_of(s);
 #pragma unroll
         for (int i = 1; i < 32; i <<= 1) {
@@ -453,7 +456,7 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
         I more = 0;
 #pragma unroll 4
         for (int b = 32 + lane; b < a.B; b += 32) {
-          const PrefillSeq q = prefill_seq(a, b);
+          const PrefillSeq q = prefill_seq<I>(a, b);
           if (q.code != 0 && blockIdx.x == 0) record_error(a.err, q.code);
           falls |= q.falls;
           more += length_of(q);
@@ -1044,9 +1047,14 @@ __global__ void __launch_bounds__(PrefillLayout<D>::THREADS, 1)
           l2.y *= keep;
           const bool far = valid && up != -INFINITY && fabsf(up * c) > kPrefillFar;
           if (__any_sync(kFullMask, far)) {
-            const float less = far ? up : 0.f;
+            // (in pairs, as what skips this pays for its length)
+            const float less = far ? -up : 0.f;
 #pragma unroll
-            for (int e = 0; e < HN; ++e) x[e] -= less;
+            for (int e = 0; e < HN; e += 2) {
+              const float2 y = add2(make_float2(x[e], x[e + 1]), make_float2(less, less));
+              x[e] = y.x;
+              x[e + 1] = y.y;
+            }
           }
           m = far ? -INFINITY : up;
           held = far ? up : -INFINITY;

@@ -24,8 +24,8 @@ constexpr int kPrefillKeyCost1 = 2, kPrefillItemCost1 = 3 * 320;   // with one r
 // A reference score's exponent beyond which scores are taken relative to it before
 // they are scaled (2^-16 of a weight is lost below).
 constexpr float kPrefillFar = 256.f;
-// Below so many items a key head, and lines of less than 2^31 in all, the
-// scheduler counts in 32 bits.
+// Below so many items a key head, lines of less than 2^31 in all and no sequence
+// longer than allowed, the scheduler counts in 32 bits.
 constexpr int kPrefillSmallItems = 30000;
 
 // What the reduce has to know of an item that CTA c goes on with where another
