@@ -32,8 +32,8 @@ struct RopeArgs {
   int T, Hq, Hkv, bs, bs_log2, NB;
   int rows;                                 // head rows of one slice
   int rot, inter, max_pos;
-  int axes;                                 // rows of positions, [axes, T]
-  int bound[kMaxAxes - 1];                  // first channel pair of axes 1, 2, ... (rot / 2: none)
+  int bound[kMaxAxes - 1];                  // first channel pair of axes 1, 2, ... (rot / 2: none), which are
+                                            //   the rows of positions that are read besides the first
 };
 
 template <bool BF>
@@ -505,7 +505,7 @@ int append(const pkv_shape* s, const pkv_rope* rope, const pkv_rope_axes* axes, 
   if (rope->rot_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
   const int D = s->head_dim, half = rope->rot_dim / 2;
   RopeArgs a{};
-  a.axes = rope->rot_dim > 0 ? 1 : 0;
+  const bool several = axes && axes->num_axes > 1;
   for (int x = 0; x < kMaxAxes - 1; ++x) a.bound[x] = half;
   if (axes) {
     if (axes->num_axes < 1 || axes->num_axes > kMaxAxes || rope->rot_dim == 0) return PKV_ERR_INVALID;
@@ -516,7 +516,6 @@ int append(const pkv_shape* s, const pkv_rope* rope, const pkv_rope_axes* axes, 
       if (x + 1 < axes->num_axes) a.bound[x] = sum < half ? static_cast<int>(sum) : half;
     }
     if (sum != half) return PKV_ERR_INVALID;
-    a.axes = axes->num_axes;
   }
   const long long qd = static_cast<long long>(s->num_q_heads) * D;
   const long long kd = static_cast<long long>(s->num_kv_heads) * D;
@@ -559,9 +558,9 @@ int append(const pkv_shape* s, const pkv_rope* rope, const pkv_rope_axes* axes, 
   a.max_pos = rope->max_position;
   const bool bf = s->dtype == PKV_BF16;
   void (*kern)(RopeArgs) = nullptr;
-  if (D == 64) kern = append_kernel<64, KV4>(bf, a.axes > 1);
-  if (D == 128) kern = append_kernel<128, KV4>(bf, a.axes > 1);
-  if (D == 256) kern = append_kernel<256, KV4>(bf, a.axes > 1);
+  if (D == 64) kern = append_kernel<64, KV4>(bf, several);
+  if (D == 128) kern = append_kernel<128, KV4>(bf, several);
+  if (D == 256) kern = append_kernel<256, KV4>(bf, several);
   int sms = 0;
   rc = device_sms(&sms);
   if (rc != PKV_OK) return rc;
@@ -585,7 +584,7 @@ int append(const pkv_shape* s, const pkv_rope* rope, const pkv_rope_axes* axes, 
   const dim3 grid(static_cast<unsigned>(num_tokens < walkers ? num_tokens : walkers),
                   static_cast<unsigned>(slices));
   const size_t smem = static_cast<size_t>(kStages) * (static_cast<size_t>(a.rows) * D * 2 + a.rot * 4);
-  cudaError_t e = raise_smem(reinterpret_cast<const void*>(kern), KV4, a.axes > 1, bf, D);
+  cudaError_t e = raise_smem(reinterpret_cast<const void*>(kern), KV4, several, bf, D);
   if (e != cudaSuccess) return PKV_ERR_CUDA;
   e = launch_pdl(kern, grid, kThreads, smem, reinterpret_cast<cudaStream_t>(stream), a);
   if (e != cudaSuccess) return PKV_ERR_CUDA;
