@@ -25,10 +25,13 @@
 // then O and the sum are rescaled (rare: the first key tile sets it).  P is held
 // in the inputs' type, as the tensor cores want both operands alike; that adds
 // half a step of the type to each weight (the whole result of bfloat16 rows is
-// then off by 1.4 times the store's own rounding, in the mean; a second product
-// with the rest of P, which the decode kernels can afford as bytes bound them,
-// would cost half of the rate here).  P in
-// binary16 is scaled by 2^7 so that weights of down to 2^-21 of the largest
+// then off by 1.4 times the store's own rounding, in the mean).  A second product
+// with the rest of P would cost long rows half of their rate.  For few rows, which
+// bytes bound, it was tried in items of one row tile whose keys no other item
+// reads: bfloat16 rows then round only in the store (2.3e-3 to 1.7e-3), as the
+// decode kernels' do, but 4 x 8 tokens after 32760 take 89.4 us instead of 87.0,
+// all other calls 1 to 3% more for the longer loop (binary16 25%: the registers).
+// P in binary16 is scaled by 2^7 so that weights of down to 2^-21 of the largest
 // keep all their bits; the largest, 2^15, is still in range.  In bfloat16 it is
 // scaled by 2^-8: the largest is 1, and O in FP32 holds what a plain softmax's
 // sums hold of values near the type's end.  The sums are of P in FP32, before
@@ -49,8 +52,9 @@
 // on 8: a prompt of 8192 tokens 328 us, 1675 TFLOP/s, 0.86 of the library's
 // 8192^3 product; 2048 tokens after 8192 in blocks of 16 190 us, 1630; 4 x 8 tokens of
 // 64/8 heads after 32760 each 88 us, 6.1 TB/s, 0.90 of a copy; without a mask,
-// 4096 tokens, head_dim 64 / 128 / 256: 1010, 1630, 1505 TFLOP/s (at 64 the softmax
-// of both row tiles is all there is).
+// 4096 tokens, head_dim 64 / 128 / 256: 1010, 1630, 1505 TFLOP/s (at 64 no unit is
+// full: issue slots 59%, exponentials and tensor pipe 44% each; it is the chain from
+// scores to weights to products of the two row tiles).
 // On the way (a prompt of 8192): 729 us with one issuing lane that worked out its
 // descriptors, 501 with descriptors in uniform registers, 411 with two threads a
 // row, 371 with items cut evenly over the CTAs, V looked over by a warp of its
@@ -58,7 +62,7 @@
 // two barriers asked at once, 337 with an issuer that does not sleep.  32 prompts
 // of 1-2048 tokens, 32 heads of 128: 371 us, 365 with items told of further ahead,
 // 354 with masks against constants and a quicker look at the values, 348 with
-// output stores that pass L1 by.
+// output stores that pass L1 by, 351 since logits of any size are taken.
 // Tried and slower: P beside S with scores that need not wait for it (head_dim 64,
 // 138 to 160 us); four output warps (80 registers for the softmax, 337 to 367);
 // a quarter of the exponentials by polynomial (175 to 200 of 4096 tokens); the
@@ -289,9 +293,9 @@ __device__ __forceinline__ void tma_3d_if(uint32_t dst, const CUtensorMap* map, 
       : "memory");
 }
 
-// 32 bytes to global memory, which nobody here reads again: L1 is passed by (1-3%
-// of the kernel's time).  Rows of the output (to an address that is `wide`,
-// aligned to them: in one piece, else in two) are the first to leave L2.
+// 32 bytes to global memory, which nobody here reads again.  Rows of the output: to
+// an address that is `wide`, aligned to them, in one piece that passes L1 by (1-3%
+// of the kernel's time) and is the first to leave L2; else in two plain ones.
 __device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8], bool wide) {
   if (wide) {
     asm volatile("st.global.L1::no_allocate.L2::evict_first.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p),
