@@ -69,7 +69,8 @@ enum {
   PKV_DEV_BAD_SLOT = 3,      /* a slot >= num_blocks * block_size */
   PKV_DEV_TIMEOUT = 4,       /* a pipeline wait gave up (should never happen) */
   PKV_DEV_BAD_POSITION = 5,  /* a position outside [0, max_position) */
-  PKV_DEV_BAD_STARTS = 6     /* query or key starts that fall or pass the rows' end */
+  PKV_DEV_BAD_STARTS = 6     /* query or key starts that fall, pass the rows' end or hold more
+                                keys than a call takes */
 };
 
 /* Shape of one paged cache and of the batch that reads it.
